@@ -8,6 +8,7 @@ an exception is raised.  PyTorch supplies device memory and the current stream o
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -18,7 +19,7 @@ __all__ = [
     "workspace_bytes", "plan_rows_cap", "MOE_OK", "MOE_EINVAL", "MOE_EUNSUPPORTED", "MOE_EWORKSPACE",
     "MOE_EHIP", "OP_PERMUTE", "OP_ROUTE_TR", "OP_GEMM_FWD", "OP_LAYER_BWD", "OP_ROUTER_BWD",
     "OP_ROUTER_LOGITS", "PLAN_TOPK", "PLAN_TR", "PLAN_CAP", "CAP_POSITION", "CAP_PROBS",
-    "EXPORTED_SYMBOLS", "KERNEL_IDS", "set_kernel_events",
+    "EXPORTED_SYMBOLS", "KERNEL_IDS", "set_kernel_events", "add_rmsnorm", "add_rmsnorm_bwd", "OP_ADD_RMSNORM_BWD",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
@@ -28,6 +29,7 @@ CAP_POSITION, CAP_PROBS = 0, 1
 OP_PERMUTE, OP_ROUTE_TR, OP_GEMM_FWD, OP_LAYER_BWD, OP_ROUTER_BWD, OP_ROUTER_LOGITS = 0, 1, 2, 3, 4, 5
 OP_GEMM_FWD_MXFP8 = 6
 OP_LAYER_BWD_MXFP8 = 7
+OP_ADD_RMSNORM_BWD = 8
 
 EXPORTED_SYMBOLS = (
     "moe_plan_rows_cap", "moe_workspace_bytes", "moe_last_error", "moe_route_topk", "moe_permute",
@@ -36,13 +38,14 @@ EXPORTED_SYMBOLS = (
     "moe_layer_bwd",
     "moe_router_logits", "moe_router_bwd", "moe_set_kernel_events", "moe_quantize_mxfp8",
     "moe_grouped_gemm_fwd_mxfp8", "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8",
+    "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
 )
 
 # kernel ids of the measurement hook (moe_kernel_id in include/moe.h)
 KERNEL_IDS = {"gateup": 0, "down": 1, "dh": 2, "dx": 3, "dwd": 4, "dw1": 5, "combine": 6, "dx_combine": 7,
               "route": 8, "permute": 9, "route_tr_plan": 10, "dswiglu": 11, "router_logits": 12,
               "router_dz": 13, "router_dx": 14, "router_dw": 15, "gateup_fp8": 16, "down_fp8": 17, "quant": 18,
-              "dx_fp8": 19}
+              "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -110,12 +113,15 @@ def load_library(path: str):
     L.moe_quantize_dx_weights_mxfp8.argtypes = [ctypes.c_int, vp, vp, i32, i32, i32, vp, vp, vp]
     L.moe_layer_bwd_mxfp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, pp, vp, vp, vp, vp, vp, vp, vp, sz,
                                       vp]
+    f32 = ctypes.c_float
+    L.moe_add_rmsnorm.argtypes = [ctypes.c_int, ctypes.c_int, vp, vp, vp, f32, i32, i32, vp, vp, vp, vp, vp]
+    L.moe_add_rmsnorm_bwd.argtypes = [ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, f32, i32, i32, vp, vp, vp, vp, sz, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
                "moe_unpermute_combine", "moe_layer_bwd", "moe_router_logits", "moe_router_bwd",
                "moe_set_kernel_events", "moe_quantize_mxfp8", "moe_grouped_gemm_fwd_mxfp8",
-               "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8"):
+               "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -451,3 +457,127 @@ def router_bwd(logits, topk_idx, plan: Plan, ds, x, w_r, bias=None, dx_in=None, 
                                 H, _ptr(dx_in), _ptr(dx_out), _ptr(dlogits), _ptr(dw_r), _ptr(dbias), _ptr(ws), nb,
                                 _stream(stream)))
     return dict(dlogits=dlogits, dx=dx_out, dw_r=dw_r, dbias=dbias)
+
+
+# ---- the operators around the layer: these bindings check every tensor they are given ----
+def _want(name, t, shape, dtype):
+    """Refuse a tensor whose type, shape or layout (contiguous, row-major) is not the one asked for."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (strides {t.stride()})")
+    return t
+
+
+def _out(name, t, shape, dtype, like):
+    """The caller's output tensor, checked, or a new one."""
+    import torch
+    return torch.empty(shape, dtype=dtype, device=like.device) if t is None else _want(name, t, shape, dtype)
+
+
+def _same_device(first, *others):
+    if not first.is_cuda:
+        raise ValueError(f"tensors must be on a GPU (got {first.device})")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_stream(fn):
+    """Run a binding on its first tensor's device and, if `stream` is given, with that stream as
+    the current one: what the call allocates then belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        import torch
+        if not first.is_cuda:
+            return fn(first, *args, **kw)  # refused there
+        if stream is None and first.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.device(first.device):
+            if stream is None:
+                return fn(first, *args, **kw)
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+    return call
+
+
+def _cur(t):
+    """The current stream's handle on t's device."""
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+@_on_stream
+def add_rmsnorm(x, w=None, residual=None, eps: float = 1e-6, want_h=True, want_y=True, quantize=False, h=None, y=None,
+                q=None, scales=None):
+    """Residual addition with RMS norm: s = x + residual, y = s / rms(s) * w, optionally quantized.
+
+    x [N,H] bf16 or fp32; residual [N,H] of x's type or fp32 (None: none); w fp32 [H] (None: ones).
+    -> dict(h [N,H] (the sum, in residual's type), y [N,H] (x's type), q uint8 [N,H], scales uint8
+    [N, 4 ceil(H/128)]: y as MX-FP8, as quantize_mxfp8 lays it out); what is not wanted is None.
+    h may be residual (in place).  stream: a torch stream to run on (default: the current one)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, H] (got {tuple(x.shape)})")
+    N, H = x.shape
+    dt = _dtype_code(x)
+    rtype = x.dtype if residual is None else residual.dtype
+    _want("x", x, (N, H), x.dtype)
+    if residual is not None:
+        _want("residual", residual, (N, H), rtype)
+        rdt = _dtype_code(residual)
+    else:
+        if h is not None and h.dtype == torch.float32:
+            rtype = torch.float32
+        rdt = MOE_F32 if rtype == torch.float32 else dt
+    if w is not None:
+        _want("w", w, (H,), torch.float32)
+    want_h, want_y = want_h or h is not None, want_y or y is not None
+    quantize = quantize or q is not None or scales is not None
+    _same_device(x, residual, w, h, y, q, scales)
+    h = _out("h", h, (N, H), rtype, x) if want_h else None
+    y = _out("y", y, (N, H), x.dtype, x) if want_y else None
+    q = _out("q", q, (N, H), torch.uint8, x) if quantize else None
+    scales = _out("scales", scales, (N, mx_scale_cols(H)), torch.uint8, x) if quantize else None
+    if N:
+        _check(lib().moe_add_rmsnorm(dt, rdt, x.data_ptr(), _addr(residual), _addr(w), eps, N, H, _addr(h), _addr(y),
+                                     _addr(q), _addr(scales), _cur(x)))
+    return dict(h=h, y=y, q=q, scales=scales)
+
+
+@_on_stream
+def add_rmsnorm_bwd(dy, h, w=None, dh_in=None, eps: float = 1e-6, want_dx=False, want_dw=True, dh=None, dx=None,
+                    dw=None, ws=None):
+    """Backward of add_rmsnorm at the stored sum h: dy [N,H] is the gradient of y, dh_in (h's type, or
+    None) the one that reaches h itself.  -> dict(dh [N,H] in h's type (the gradient of x and of
+    residual), dx: dh in dy's type if wanted, dw fp32 [H] or None).  dh may be dh_in (in place)."""
+    import torch
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be [N, H] (got {tuple(dy.shape)})")
+    N, H = dy.shape
+    dt, rdt = _dtype_code(dy), _dtype_code(h)
+    _want("dy", dy, (N, H), dy.dtype)
+    _want("h", h, (N, H), h.dtype)
+    if dh_in is not None:
+        _want("dh_in", dh_in, (N, H), h.dtype)
+    if w is not None:
+        _want("w", w, (H,), torch.float32)
+    _same_device(dy, h, dh_in, w, dh, dx, dw, ws)
+    dh = _out("dh", dh, (N, H), h.dtype, dy)
+    dx = _out("dx", dx, (N, H), dy.dtype, dy) if want_dx or dx is not None else None
+    dw = _out("dw", dw, (H,), torch.float32, dy) if want_dw or dw is not None else None
+    nb = 0
+    if dw is not None:
+        nb = workspace_bytes(OP_ADD_RMSNORM_BWD, dt, N, 1, 1, H, 0, 0)
+        ws = _ws(nb, dy.device, ws)
+    _check(lib().moe_add_rmsnorm_bwd(dt, rdt, dy.data_ptr(), h.data_ptr(), _addr(dh_in), _addr(w), eps, N, H,
+                                     dh.data_ptr(), _addr(dx), _addr(dw), _addr(ws) if nb else None, nb, _cur(dy)))
+    return dict(dh=dh, dx=dx, dw=dw)

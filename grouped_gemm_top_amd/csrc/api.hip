@@ -1,6 +1,7 @@
 // api.hip -- the extern "C" entry points of libmoe.so: argument validation, workspace
 // carving and launch sequencing on the caller's stream.  The operations themselves are
 // documented in moe.h.
+#include <float.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -62,6 +63,19 @@ moe_status check_plan(const moe_plan* p) {
   REQUIRE(p->counts && p->offsets && p->tok_ptr, MOE_EINVAL, "plan has a NULL counts/offsets/tok_ptr array");
   REQUIRE(p->M_cap == 0 || (p->row_token && p->row_w && p->row_pair && p->tok_rows), MOE_EINVAL,
           "plan has a NULL row array");
+  return MOE_OK;
+}
+
+// types and sizes of the norm calls: rdt is dt, or fp32 beside bf16
+moe_status check_norm(moe_dtype dt, moe_dtype rdt, int32_t N, int32_t H) {
+  moe_status st;
+  if ((st = check_dtype(dt)) != MOE_OK) return st;
+  if ((st = check_dtype(rdt)) != MOE_OK) return st;
+  REQUIRE(rdt == dt || rdt == MOE_F32, MOE_EUNSUPPORTED, "the residual type must be the activations' or fp32");
+  REQUIRE(N >= 0, MOE_EINVAL, "N must be >= 0 (got %d)", N);
+  REQUIRE(H >= 8, MOE_EINVAL, "H must be >= 8 (got %d)", H);
+  REQUIRE(H % 8 == 0 && H <= 16384, MOE_EUNSUPPORTED, "H must be a multiple of 8 up to 16384 (got %d)", H);
+  REQUIRE((int64_t)N * H < (int64_t)1 << 40, MOE_EUNSUPPORTED, "N*H too large");
   return MOE_OK;
 }
 
@@ -166,6 +180,9 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_LAYER_BWD_MXFP8:
       if (H < 32 || I < 32 || H % 32 || I % 32 || M_cap < 0) return 0;
       return moe::layer_bwd_mxfp8_ws_bytes(N, M_cap, H, I);
+    case MOE_OP_ADD_RMSNORM_BWD:
+      if (check_norm(dt, dt, N, H) != MOE_OK) return 0;
+      return moe::add_rmsnorm_bwd_ws_bytes(N, H);
   }
   return 0;
 }
@@ -472,6 +489,50 @@ moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, 
   return hip_status(moe::launch_router_bwd(dt, logits, bias, topk_idx, *plan, ds, x, w_r, H, dx_in, dx_out, dlogits,
                                            dw_r, dbias, ws, (hipStream_t)stream),
                     "moe_router_bwd");
+}
+
+moe_status moe_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const void* res, const float* w, float eps,
+                           int32_t N, int32_t H, void* h, void* y, uint8_t* q, uint8_t* scales, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_norm(dt, rdt, N, H)) != MOE_OK) return st;
+  REQUIRE(eps >= 0.f && eps <= FLT_MAX, MOE_EINVAL, "eps must be finite and >= 0");
+  REQUIRE(!q || H % 32 == 0, MOE_EUNSUPPORTED, "an MX-FP8 output needs H a multiple of 32 (got %d)", H);
+  REQUIRE(h || y || q, MOE_EINVAL, "no output requested");
+  REQUIRE((q != nullptr) == (scales != nullptr), MOE_EINVAL, "q and scales are given together or not at all");
+  REQUIRE(N == 0 || x, MOE_EINVAL, "NULL x");
+  REQUIRE(h == nullptr || h != x || rdt == dt, MOE_EINVAL, "h can be x only where their types agree");
+  REQUIRE(y == nullptr || (y != h && y != x && y != res), MOE_EINVAL, "y must not be x, res or h");
+  REQUIRE(aligned16(x) && aligned16(res) && aligned16(w) && aligned16(h) && aligned16(y) && aligned16(q),
+          MOE_EUNSUPPORTED, "tensors must be 16-byte aligned");
+  moe::kernel_event(MOE_K_ADD_RMSNORM, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_add_rmsnorm(dt, rdt, x, res, w, eps, N, H, h, y, q, scales, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_ADD_RMSNORM, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_add_rmsnorm");
+}
+
+moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, const void* h, const void* dh_in,
+                               const float* w, float eps, int32_t N, int32_t H, void* dh, void* dx, float* dw,
+                               void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_norm(dt, rdt, N, H)) != MOE_OK) return st;
+  REQUIRE(eps >= 0.f && eps <= FLT_MAX, MOE_EINVAL, "eps must be finite and >= 0");
+  REQUIRE(N == 0 || (dy && h && dh), MOE_EINVAL, "NULL dy/h/dh");
+  REQUIRE(N == 0 || (dh != h && dh != dy && (!dx || (dx != dh && dx != h && dx != dh_in && dx != dy))), MOE_EINVAL,
+          "dh may be dh_in; it and dx must be no other argument");
+  REQUIRE(aligned16(dy) && aligned16(h) && aligned16(dh_in) && aligned16(w) && aligned16(dh) && aligned16(dx) &&
+              aligned16(dw) && aligned16(ws),
+          MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned");
+  if (dw) {
+    const size_t need = moe::add_rmsnorm_bwd_ws_bytes(N, H);
+    REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  }
+  moe::kernel_event(MOE_K_ADD_RMSNORM_BWD, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_add_rmsnorm_bwd(dt, rdt, dy, h, dh_in, w, eps, N, H, dh, dx, dw, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_ADD_RMSNORM_BWD, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_add_rmsnorm_bwd");
 }
 
 }  // extern "C"

@@ -140,4 +140,10 @@ hipError_t launch_layer_bwd_mxfp8(const void* dout, const void* x, const void* w
                                   const void* wtq, const void* wts, int H, int I, const moe_plan& p,
                                   const void* hcache, void* dx, void* dwg, void* dwu, void* dwd, float* ds, void* ws,
                                   hipStream_t s);
+size_t add_rmsnorm_bwd_ws_bytes(int N, int H);
+hipError_t launch_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const void* res, const float* w, float eps,
+                              int N, int H, void* h, void* y, uint8_t* q, uint8_t* scales, hipStream_t s);
+hipError_t launch_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, const void* h, const void* dh_in,
+                                  const float* w, float eps, int N, int H, void* dh, void* dx, float* dw, void* ws,
+                                  hipStream_t s);
 }  // namespace moe

@@ -79,7 +79,8 @@ typedef enum moe_op {
   MOE_OP_ROUTER_BWD = 4,
   MOE_OP_ROUTER_LOGITS = 5,
   MOE_OP_GEMM_FWD_MXFP8 = 6,
-  MOE_OP_LAYER_BWD_MXFP8 = 7
+  MOE_OP_LAYER_BWD_MXFP8 = 7,
+  MOE_OP_ADD_RMSNORM_BWD = 8
 } moe_op;
 
 /*
@@ -381,6 +382,42 @@ moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, 
                           void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Residual addition with RMS norm: what makes the layer's input x (and its MX-FP8 operand) from
+ * the residual stream.  For each of N rows of H values,
+ *   s = x + res                       (fp32; res NULL: s = x)
+ *   h = s                             (stored in the residual type rdt; NULL skips it)
+ *   r = 1 / sqrt(sum_c s_c^2 / H + eps)
+ *   y_c = s_c r w_c                   (w fp32 [H], NULL: ones; stored in dt; NULL skips it)
+ *   q, scales                         y as MX-FP8 in the layout of moe_quantize_mxfp8 (q NULL
+ *                                     skips both): the codes round the fp32 y, not the stored one
+ * x, y [N,H] of dt; res, h [N,H] of rdt.  rdt is dt, or MOE_F32 with dt = MOE_BF16 (an fp32
+ * residual stream).  h may be res, or x where rdt is dt (in place); the other outputs overlap no
+ * input and no other output.  At least one output is requested.  H is a multiple of 8 (of 32 with
+ * q) up to 16384, eps >= 0; x, res, w, h, y and q are 16-byte aligned; N H below 2^40.  Sums are
+ * fp32.  A row that holds an infinity or a NaN, or whose squares overflow fp32, gives what the
+ * formulas give in fp32; it does not touch other rows.
+ */
+moe_status moe_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const void* res, const float* w, float eps,
+                           int32_t N, int32_t H, void* h, void* y, uint8_t* q, uint8_t* scales, void* stream);
+
+/*
+ * Backward of moe_add_rmsnorm at the stored sum h, given dy, the gradient of y (of the dequantized
+ * codes too: the rounding passes gradients through), and dh_in, the gradient that reaches h
+ * itself (NULL: none):
+ *   r = 1 / sqrt(sum_c h_c^2 / H + eps),  a_c = dy_c w_c,  m = sum_c a_c h_c / H
+ *   dh_c = r a_c - r^3 m h_c + dh_in_c   (the gradient of s, so of x and of res)
+ *   dw_c = sum_t dy_tc h_tc r_t          (fp32 [H]; NULL skips it)
+ *   dx                                   dh in type dt, for x where rdt is fp32 (NULL skips it)
+ * dy, dx [N,H] of dt; h, dh_in, dh [N,H] of rdt; types and sizes as moe_add_rmsnorm.  dh may be
+ * dh_in (in place).  N == 0 sets dw to zero.  dw is summed in a fixed order (bitwise
+ * reproducible).  Workspace: moe_workspace_bytes(MOE_OP_ADD_RMSNORM_BWD, dt, N, 1, 1, H, 0, 0) when
+ * dw is requested, else none.
+ */
+moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, const void* h, const void* dh_in,
+                               const float* w, float eps, int32_t N, int32_t H, void* dh, void* dx, float* dw,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Measurement hook (for benchmarks and profilers, not needed for computing): kernels of
  * the library, identified by moe_kernel_id.  After moe_set_kernel_events(id, start, stop)
  * with two hipEvent_t handles (passed as void*), every later launch of that kernel records
@@ -412,7 +449,9 @@ typedef enum moe_kernel_id {
   MOE_K_QUANT = 18,      /* moe_quantize_mxfp8, moe_quantize_dx_weights_mxfp8, and moe_layer_bwd_mxfp8's
                             quantization of dH */
   MOE_K_DX_FP8 = 19,     /* moe_layer_bwd_mxfp8: the dX grouped GEMM on MX-FP8 operands */
-  MOE_K_COUNT = 20
+  MOE_K_ADD_RMSNORM = 20,     /* moe_add_rmsnorm */
+  MOE_K_ADD_RMSNORM_BWD = 21, /* moe_add_rmsnorm_bwd: the row kernel and the sum of dw's partials */
+  MOE_K_COUNT = 22
 } moe_kernel_id;
 
 moe_status moe_set_kernel_events(int32_t kernel_id, void* start_event, void* stop_event);

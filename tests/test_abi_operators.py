@@ -1,0 +1,98 @@
+"""Refusals of the operators around the layer, on the host: the C entry points return the documented
+status before anything is queued, and the Python bindings check every tensor they are given.  No
+test here launches a kernel."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import grouped_gemm_top_amd as G
+
+FAKE = 0x10000  # a non-NULL, 16-byte aligned address; never dereferenced by these calls
+F = ctypes.c_void_p(FAKE)
+ODD = ctypes.c_void_p(FAKE + 8)
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(G.lib_path()):
+        import grouped_gemm_top_amd.build as B
+        B.build()
+    return G.lib()
+
+
+def test_add_rmsnorm_errors(L):
+    def call(dt=G.MOE_BF16, rdt=G.MOE_BF16, x=F, res=F, w=F, eps=1e-6, N=4, H=64, h=F, y=ctypes.c_void_p(FAKE + 4096),
+             q=None, sc=None):
+        return L.moe_add_rmsnorm(dt, rdt, x, res, w, eps, N, H, h, y, q, sc, None)
+    assert call(dt=7) == G.MOE_EUNSUPPORTED
+    assert call(rdt=7) == G.MOE_EUNSUPPORTED
+    assert call(dt=G.MOE_F32, rdt=G.MOE_BF16) == G.MOE_EUNSUPPORTED       # bf16 stream under fp32 activations
+    assert call(N=-1) == G.MOE_EINVAL
+    assert call(H=0) == G.MOE_EINVAL
+    assert call(H=12) == G.MOE_EUNSUPPORTED
+    assert call(H=16392) == G.MOE_EUNSUPPORTED
+    assert call(H=40, q=F, sc=F) == G.MOE_EUNSUPPORTED                     # codes need H % 32
+    assert call(q=F) == G.MOE_EINVAL                                       # codes without scales
+    assert call(h=None, y=None) == G.MOE_EINVAL                            # no output
+    assert call(x=None) == G.MOE_EINVAL
+    assert call(eps=-1e-6) == G.MOE_EINVAL
+    assert call(eps=float("nan")) == G.MOE_EINVAL
+    assert call(eps=float("inf")) == G.MOE_EINVAL
+    assert call(x=ODD) == G.MOE_EUNSUPPORTED
+    assert call(w=ODD) == G.MOE_EUNSUPPORTED
+    assert call(y=F) == G.MOE_EINVAL                                       # y over h
+    assert call(rdt=G.MOE_F32) == G.MOE_EINVAL                             # h over an x of another type
+    assert call(N=1 << 30, H=2048) == G.MOE_EUNSUPPORTED
+    assert call(N=0, x=None) == G.MOE_OK                                   # nothing to do
+
+
+def test_add_rmsnorm_bwd_errors(L):
+    ptr = lambda k: ctypes.c_void_p(FAKE + 4096 * k)  # noqa: E731
+    need = L.moe_workspace_bytes(G.OP_ADD_RMSNORM_BWD, G.MOE_BF16, 40, 1, 1, 64, 0, 0)
+    assert need >= 64 * 4
+    assert L.moe_workspace_bytes(G.OP_ADD_RMSNORM_BWD, G.MOE_BF16, 40, 1, 1, 60, 0, 0) == 0
+    assert L.moe_workspace_bytes(G.OP_ADD_RMSNORM_BWD, 5, 40, 1, 1, 64, 0, 0) == 0
+
+    def call(dt=G.MOE_BF16, rdt=G.MOE_BF16, dy=ptr(0), h=ptr(1), din=ptr(2), N=40, H=64, dh=ptr(3), dx=ptr(4),
+             dw=ptr(5), ws=ptr(6), nb=need, eps=1e-6):
+        return L.moe_add_rmsnorm_bwd(dt, rdt, dy, h, din, F, eps, N, H, dh, dx, dw, ws, nb, None)
+    assert call(nb=need - 1) == G.MOE_EWORKSPACE
+    assert call(ws=None) == G.MOE_EINVAL
+    assert call(dy=None) == G.MOE_EINVAL
+    assert call(dh=None) == G.MOE_EINVAL
+    assert call(dh=ptr(1)) == G.MOE_EINVAL      # dh over h
+    assert call(dx=ptr(3)) == G.MOE_EINVAL      # dx over dh
+    assert call(dx=ptr(2)) == G.MOE_EINVAL      # dx over dh_in
+    assert call(H=20) == G.MOE_EUNSUPPORTED
+    assert call(dt=G.MOE_F32, rdt=G.MOE_BF16) == G.MOE_EUNSUPPORTED
+    assert call(eps=float("nan")) == G.MOE_EINVAL
+    assert call(dw=ODD) == G.MOE_EUNSUPPORTED
+
+
+def test_add_rmsnorm_bindings():
+    b, f = torch.bfloat16, torch.float32
+    x, r, w = torch.zeros(4, 64, dtype=b), torch.zeros(4, 64, dtype=b), torch.zeros(64)
+    with pytest.raises(ValueError, match="GPU"):
+        G.add_rmsnorm(x, w, residual=r)
+    with pytest.raises(TypeError):
+        G.add_rmsnorm(x.half(), w)
+    with pytest.raises(TypeError):
+        G.add_rmsnorm(x, w.to(b))
+    with pytest.raises(ValueError, match="shape"):
+        G.add_rmsnorm(x, w, residual=r[:3])
+    with pytest.raises(ValueError, match="shape"):
+        G.add_rmsnorm(x, w[:8])
+    with pytest.raises(ValueError, match="contiguous"):
+        G.add_rmsnorm(torch.zeros(64, 4, dtype=b).t())
+    with pytest.raises(ValueError, match="contiguous"):
+        G.add_rmsnorm(x, w, residual=torch.zeros(4, 128, dtype=b)[:, ::2])
+    with pytest.raises(ValueError):
+        G.add_rmsnorm(x[0])
+    with pytest.raises(ValueError, match="GPU"):
+        G.add_rmsnorm_bwd(x, r, w)
+    with pytest.raises(ValueError, match="shape"):
+        G.add_rmsnorm_bwd(x, r, w, dh_in=r[:1])
+    with pytest.raises(TypeError):
+        G.add_rmsnorm_bwd(x, r.to(f), w, dh_in=r)
