@@ -20,6 +20,7 @@ __all__ = [
     "MOE_EHIP", "OP_PERMUTE", "OP_ROUTE_TR", "OP_GEMM_FWD", "OP_LAYER_BWD", "OP_ROUTER_BWD",
     "OP_ROUTER_LOGITS", "PLAN_TOPK", "PLAN_TR", "PLAN_CAP", "CAP_POSITION", "CAP_PROBS",
     "EXPORTED_SYMBOLS", "KERNEL_IDS", "set_kernel_events", "add_rmsnorm", "add_rmsnorm_bwd", "OP_ADD_RMSNORM_BWD",
+    "balance_loss", "balance_loss_bwd", "OP_BALANCE_LOSS",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
@@ -30,6 +31,7 @@ OP_PERMUTE, OP_ROUTE_TR, OP_GEMM_FWD, OP_LAYER_BWD, OP_ROUTER_BWD, OP_ROUTER_LOG
 OP_GEMM_FWD_MXFP8 = 6
 OP_LAYER_BWD_MXFP8 = 7
 OP_ADD_RMSNORM_BWD = 8
+OP_BALANCE_LOSS = 9
 
 EXPORTED_SYMBOLS = (
     "moe_plan_rows_cap", "moe_workspace_bytes", "moe_last_error", "moe_route_topk", "moe_permute",
@@ -38,14 +40,15 @@ EXPORTED_SYMBOLS = (
     "moe_layer_bwd",
     "moe_router_logits", "moe_router_bwd", "moe_set_kernel_events", "moe_quantize_mxfp8",
     "moe_grouped_gemm_fwd_mxfp8", "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8",
-    "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
+    "moe_add_rmsnorm", "moe_add_rmsnorm_bwd", "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
 )
 
 # kernel ids of the measurement hook (moe_kernel_id in include/moe.h)
 KERNEL_IDS = {"gateup": 0, "down": 1, "dh": 2, "dx": 3, "dwd": 4, "dw1": 5, "combine": 6, "dx_combine": 7,
               "route": 8, "permute": 9, "route_tr_plan": 10, "dswiglu": 11, "router_logits": 12,
               "router_dz": 13, "router_dx": 14, "router_dw": 15, "gateup_fp8": 16, "down_fp8": 17, "quant": 18,
-              "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21}
+              "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21, "balance": 22,
+              "balance_bwd": 23}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -116,12 +119,16 @@ def load_library(path: str):
     f32 = ctypes.c_float
     L.moe_add_rmsnorm.argtypes = [ctypes.c_int, ctypes.c_int, vp, vp, vp, f32, i32, i32, vp, vp, vp, vp, vp]
     L.moe_add_rmsnorm_bwd.argtypes = [ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, f32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.moe_balance_loss.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp, vp, vp, sz, vp]
+    L.moe_balance_loss_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.moe_router_bwd_acc.argtypes = [ctypes.c_int, vp, vp, vp, pp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
                "moe_unpermute_combine", "moe_layer_bwd", "moe_router_logits", "moe_router_bwd",
                "moe_set_kernel_events", "moe_quantize_mxfp8", "moe_grouped_gemm_fwd_mxfp8",
-               "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd"):
+               "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
+               "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -428,9 +435,11 @@ def router_logits(x, w_r, bias=None, logits=None, ws=None, stream=None):
 
 
 def router_bwd(logits, topk_idx, plan: Plan, ds, x, w_r, bias=None, dx_in=None, dx_out=None, dlogits=None,
-               dw_r=None, dbias=None, want_dx=True, want_dw=True, want_dbias=True, ws=None, stream=None):
+               dw_r=None, dbias=None, want_dx=True, want_dw=True, want_dbias=True, ws=None, stream=None,
+               dlogits_in=None):
     """Router backward from dS (moe_layer_bwd's ds) -> dict(dlogits, dx, dw_r, dbias).
-    dx = dx_in + the router's share (dx_in defaults to zeros; dx_out may be dx_in)."""
+    dx = dx_in + the router's share (dx_in defaults to zeros; dx_out may be dx_in).  dlogits_in
+    fp32 [N,E]: a further gradient of the logits (balance_loss_bwd's), included in all four."""
     import torch
     N, H = x.shape
     E = logits.shape[1]
@@ -453,9 +462,12 @@ def router_bwd(logits, topk_idx, plan: Plan, ds, x, w_r, bias=None, dx_in=None, 
     nb = workspace_bytes(OP_ROUTER_BWD, dt, plan.N, plan.E, plan.k, H, 8, 0) if (want_dx or want_dw or want_dbias) \
         else 0
     ws = _ws(nb, dev, ws) if nb else None
-    _check(lib().moe_router_bwd(dt, _ptr(logits), _ptr(bias), _ptr(topk_idx), plan.c, _ptr(ds), _ptr(x), _ptr(w_r),
-                                H, _ptr(dx_in), _ptr(dx_out), _ptr(dlogits), _ptr(dw_r), _ptr(dbias), _ptr(ws), nb,
-                                _stream(stream)))
+    if dlogits_in is not None:
+        _want("dlogits_in", dlogits_in, (N, E), torch.float32)
+        _same_device(logits, dlogits_in)
+    _check(lib().moe_router_bwd_acc(dt, _ptr(logits), _ptr(bias), _ptr(topk_idx), plan.c, _ptr(ds), _ptr(dlogits_in),
+                                    _ptr(x), _ptr(w_r), H, _ptr(dx_in), _ptr(dx_out), _ptr(dlogits), _ptr(dw_r),
+                                    _ptr(dbias), _ptr(ws), nb, _stream(stream)))
     return dict(dlogits=dlogits, dx=dx_out, dw_r=dw_r, dbias=dbias)
 
 
@@ -581,3 +593,73 @@ def add_rmsnorm_bwd(dy, h, w=None, dh_in=None, eps: float = 1e-6, want_dx=False,
     _check(lib().moe_add_rmsnorm_bwd(dt, rdt, dy.data_ptr(), h.data_ptr(), _addr(dh_in), _addr(w), eps, N, H,
                                      dh.data_ptr(), _addr(dx), _addr(dw), _addr(ws) if nb else None, nb, _cur(dy)))
     return dict(dh=dh, dx=dx, dw=dw)
+
+
+def _seqs(N, mask, seq_ptr):
+    """The sequences' checks shared by balance_loss and its backward -> B."""
+    import torch
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise TypeError(f"mask must be uint8 or bool (got {mask.dtype})")
+        _want("mask", mask, (N,), mask.dtype)
+    if seq_ptr is None:
+        return 1
+    if seq_ptr.dim() != 1 or seq_ptr.shape[0] < 2:
+        raise ValueError(f"seq_ptr must be [B + 1], B >= 1 (got {tuple(seq_ptr.shape)})")
+    _want("seq_ptr", seq_ptr, seq_ptr.shape, torch.int32)
+    return seq_ptr.shape[0] - 1
+
+
+@_on_stream
+def balance_loss(logits, topk_idx, alpha: float, beta: float = 0.0, bias=None, mask=None, seq_ptr=None, loss=None,
+                 counts=None, saved=None, ws=None):
+    """Balance loss and z-loss of the router over B sequences of tokens, with per-expert counts.
+
+    logits fp32 [N,E] and topk_idx int32 [N,k] as route_topk takes and gives them; seq_ptr int32
+    [B+1] (None: one sequence), mask uint8 or bool [N] (0: padding; None: no padding).
+    -> dict(loss fp32 [2] (alpha's balance loss, beta's z-loss), counts int32 [B,E], saved fp32
+    [B*E + 1] for balance_loss_bwd).  stream: a torch stream to run on (default: the current one)."""
+    import torch
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits must be [N, E] and topk_idx [N, k]")
+    N, E = logits.shape
+    k = topk_idx.shape[1]
+    _want("logits", logits, (N, E), torch.float32)
+    _want("topk_idx", topk_idx, (N, k), torch.int32)
+    if bias is not None:
+        _want("bias", bias, (E,), torch.float32)
+    B = _seqs(N, mask, seq_ptr)
+    _same_device(logits, topk_idx, bias, mask, seq_ptr, loss, counts, saved, ws)
+    loss = _out("loss", loss, (2,), torch.float32, logits)
+    counts = _out("counts", counts, (B, E), torch.int32, logits)
+    saved = _out("saved", saved, (B * E + 1,), torch.float32, logits)
+    nb = workspace_bytes(OP_BALANCE_LOSS, MOE_F32, N, E, k, 0, B)
+    ws = _ws(nb, logits.device, ws)
+    _check(lib().moe_balance_loss(_addr(logits), _addr(bias), _addr(topk_idx), _addr(mask), _addr(seq_ptr), B, N, E, k,
+                                  alpha, beta, _addr(loss), _addr(counts), _addr(saved), _addr(ws), nb, _cur(logits)))
+    return dict(loss=loss, counts=counts, saved=saved)
+
+
+@_on_stream
+def balance_loss_bwd(logits, saved, bias=None, mask=None, seq_ptr=None, dloss=None, dlogits_in=None, dlogits=None):
+    """Gradient of balance_loss with respect to the logits, from its `saved` and the same logits,
+    bias, mask and seq_ptr -> dlogits fp32 [N,E].  dloss fp32 [2]: the two losses' gradients (None:
+    ones); dlogits_in is added (dlogits may be dlogits_in)."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [N, E] (got {tuple(logits.shape)})")
+    N, E = logits.shape
+    _want("logits", logits, (N, E), torch.float32)
+    if bias is not None:
+        _want("bias", bias, (E,), torch.float32)
+    B = _seqs(N, mask, seq_ptr)
+    _want("saved", saved, (B * E + 1,), torch.float32)
+    if dloss is not None:
+        _want("dloss", dloss, (2,), torch.float32)
+    if dlogits_in is not None:
+        _want("dlogits_in", dlogits_in, (N, E), torch.float32)
+    _same_device(logits, saved, bias, mask, seq_ptr, dloss, dlogits_in, dlogits)
+    dlogits = _out("dlogits", dlogits, (N, E), torch.float32, logits)
+    _check(lib().moe_balance_loss_bwd(_addr(logits), _addr(bias), _addr(mask), _addr(seq_ptr), B, N, E, _addr(saved),
+                                      _addr(dloss), _addr(dlogits_in), _addr(dlogits), _cur(logits)))
+    return dlogits

@@ -66,6 +66,14 @@ moe_status check_plan(const moe_plan* p) {
   return MOE_OK;
 }
 
+constexpr int32_t kMaxSeqs = 1 << 20;
+
+moe_status check_seqs(int32_t B, const int32_t* seq_ptr) {
+  REQUIRE(B >= 1 && B <= kMaxSeqs, MOE_EINVAL, "B must be in [1, %d] (got %d)", kMaxSeqs, B);
+  REQUIRE(seq_ptr || B == 1, MOE_EINVAL, "B > 1 needs seq_ptr");
+  return MOE_OK;
+}
+
 // types and sizes of the norm calls: rdt is dt, or fp32 beside bf16
 moe_status check_norm(moe_dtype dt, moe_dtype rdt, int32_t N, int32_t H) {
   moe_status st;
@@ -180,6 +188,9 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_LAYER_BWD_MXFP8:
       if (H < 32 || I < 32 || H % 32 || I % 32 || M_cap < 0) return 0;
       return moe::layer_bwd_mxfp8_ws_bytes(N, M_cap, H, I);
+    case MOE_OP_BALANCE_LOSS:  // I: the sequences
+      if (I < 1 || I > kMaxSeqs) return 0;
+      return moe::balance_loss_ws_bytes(N, E, I);
     case MOE_OP_ADD_RMSNORM_BWD:
       if (check_norm(dt, dt, N, H) != MOE_OK) return 0;
       return moe::add_rmsnorm_bwd_ws_bytes(N, H);
@@ -465,10 +476,10 @@ moe_status moe_router_logits(moe_dtype dt, const void* x, const float* w_r, cons
                     "moe_router_logits");
 }
 
-moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, const int32_t* topk_idx,
-                          const moe_plan* plan, const float* ds, const void* x, const float* w_r, int32_t H,
-                          const void* dx_in, void* dx_out, float* dlogits, float* dw_r, float* dbias, void* ws,
-                          size_t ws_bytes, void* stream) {
+moe_status moe_router_bwd_acc(moe_dtype dt, const float* logits, const float* bias, const int32_t* topk_idx,
+                              const moe_plan* plan, const float* ds, const float* dlogits_in, const void* x,
+                              const float* w_r, int32_t H, const void* dx_in, void* dx_out, float* dlogits,
+                              float* dw_r, float* dbias, void* ws, size_t ws_bytes, void* stream) {
   g_err[0] = 0;
   moe_status st;
   if ((st = check_dtype(dt)) != MOE_OK) return st;
@@ -486,9 +497,17 @@ moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, 
     REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
   }
-  return hip_status(moe::launch_router_bwd(dt, logits, bias, topk_idx, *plan, ds, x, w_r, H, dx_in, dx_out, dlogits,
+  return hip_status(moe::launch_router_bwd(dt, logits, bias, topk_idx, *plan, ds, dlogits_in, x, w_r, H, dx_in, dx_out, dlogits,
                                            dw_r, dbias, ws, (hipStream_t)stream),
                     "moe_router_bwd");
+}
+
+moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, const int32_t* topk_idx,
+                          const moe_plan* plan, const float* ds, const void* x, const float* w_r, int32_t H,
+                          const void* dx_in, void* dx_out, float* dlogits, float* dw_r, float* dbias, void* ws,
+                          size_t ws_bytes, void* stream) {
+  return moe_router_bwd_acc(dt, logits, bias, topk_idx, plan, ds, nullptr, x, w_r, H, dx_in, dx_out, dlogits, dw_r,
+                            dbias, ws, ws_bytes, stream);
 }
 
 moe_status moe_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const void* res, const float* w, float eps,
@@ -533,6 +552,44 @@ moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, cons
   hipError_t e = moe::launch_add_rmsnorm_bwd(dt, rdt, dy, h, dh_in, w, eps, N, H, dh, dx, dw, ws, (hipStream_t)stream);
   moe::kernel_event(MOE_K_ADD_RMSNORM_BWD, 1, (hipStream_t)stream);
   return hip_status(e, "moe_add_rmsnorm_bwd");
+}
+
+moe_status moe_balance_loss(const float* logits, const float* bias, const int32_t* topk_idx, const uint8_t* mask,
+                            const int32_t* seq_ptr, int32_t B, int32_t N, int32_t E, int32_t k, float alpha,
+                            float beta, float* loss, int32_t* counts, float* saved, void* ws, size_t ws_bytes,
+                            void* stream) {
+  g_err[0] = 0;
+  moe_status st = check_dims(N, E, k);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(B, seq_ptr)) != MOE_OK) return st;
+  REQUIRE(alpha - alpha == 0.f && beta - beta == 0.f, MOE_EINVAL, "alpha and beta must be finite");
+  REQUIRE(N == 0 || (logits && topk_idx), MOE_EINVAL, "NULL logits/topk_idx");
+  REQUIRE(loss && counts && saved, MOE_EINVAL, "NULL loss/counts/saved");
+  const size_t need = moe::balance_loss_ws_bytes(N, E, B);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  REQUIRE(aligned16(ws), MOE_EUNSUPPORTED, "the workspace must be 16-byte aligned");
+  moe::kernel_event(MOE_K_BALANCE, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_balance_loss(logits, bias, topk_idx, mask, seq_ptr, B, N, E, k, alpha, beta, loss, counts,
+                                          saved, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_BALANCE, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_balance_loss");
+}
+
+moe_status moe_balance_loss_bwd(const float* logits, const float* bias, const uint8_t* mask, const int32_t* seq_ptr,
+                                int32_t B, int32_t N, int32_t E, const float* saved, const float* dloss,
+                                const float* dlogits_in, float* dlogits, void* stream) {
+  g_err[0] = 0;
+  moe_status st = check_dims(N, E, 1);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(B, seq_ptr)) != MOE_OK) return st;
+  REQUIRE(N == 0 || (logits && saved && dlogits), MOE_EINVAL, "NULL logits/saved/dlogits");
+  REQUIRE(N == 0 || (dlogits != logits && dlogits != saved), MOE_EINVAL, "dlogits must not be logits or saved");
+  moe::kernel_event(MOE_K_BALANCE_BWD, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_balance_loss_bwd(logits, bias, mask, seq_ptr, B, N, E, saved, dloss, dlogits_in, dlogits,
+                                              (hipStream_t)stream);
+  moe::kernel_event(MOE_K_BALANCE_BWD, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_balance_loss_bwd");
 }
 
 }  // extern "C"

@@ -125,8 +125,8 @@ hipError_t launch_router_dw_mm(moe_dtype dt, const void* x, const float* dlogits
 hipError_t launch_router_logits(moe_dtype dt, const void* x, const float* wr, const float* bias, int N, int H, int E,
                                 float* logits, void* ws, hipStream_t s);
 hipError_t launch_router_bwd(moe_dtype dt, const float* logits, const float* bias, const int32_t* idx,
-                             const moe_plan& p, const float* ds, const void* x, const float* wr, int H,
-                             const void* dx_in, void* dx_out, float* dlogits, float* dwr, float* dbias, void* ws,
+                             const moe_plan& p, const float* ds, const float* dz_in, const void* x,
+                             const float* wr, int H, const void* dx_in, void* dx_out, float* dlogits, float* dwr, float* dbias, void* ws,
                              hipStream_t s);
 size_t layer_bwd_ws_bytes(moe_dtype dt, int N, int M_cap, int H, int I);
 hipError_t launch_layer_bwd(moe_dtype dt, const void* dout, const void* x, const void* wg, const void* wu,
@@ -146,4 +146,11 @@ hipError_t launch_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const 
 hipError_t launch_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, const void* h, const void* dh_in,
                                   const float* w, float eps, int N, int H, void* dh, void* dx, float* dw, void* ws,
                                   hipStream_t s);
+size_t balance_loss_ws_bytes(int N, int E, int B);
+hipError_t launch_balance_loss(const float* logits, const float* bias, const int32_t* idx, const uint8_t* mask,
+                               const int32_t* ptr, int B, int N, int E, int k, float alpha, float beta, float* loss,
+                               int32_t* counts, float* saved, void* ws, hipStream_t s);
+hipError_t launch_balance_loss_bwd(const float* logits, const float* bias, const uint8_t* mask, const int32_t* ptr,
+                                   int B, int N, int E, const float* saved, const float* dloss, const float* din,
+                                   float* dz, hipStream_t s);
 }  // namespace moe

@@ -2,7 +2,8 @@
 //
 //   logits[t,e] = sum_h x[t,h] W_r[h,e] (+ bias[e])                       (router_mm.hip)
 //   dz[t,m]     = sum over final pairs f of t of dS_f w_f ([m == e_f] - q_m [m in K])
-//                 with q_m = exp(z_m) / sum_{j in K} exp(z_j), K the token's top-k set  (k_router_dz)
+//                 with q_m = exp(z_m) / sum_{j in K} exp(z_j), K the token's top-k set  (k_router_dz),
+//                 plus a gradient of the logits that the caller has already (dz_in)
 //   dx_out[t,h] = dx_in[t,h] + sum_m dz[t,m] W_r[h,m]                        (router_mm.hip)
 //   dW_r[h,m]   = sum_t x[t,h] dz[t,m],  dbias[m] = sum_t dz[t,m]            (router_mm.hip + k_dwr_reduce)
 //
@@ -82,7 +83,7 @@ __device__ __forceinline__ float wave_max(float v) {
 // LDS (the pair terms, then the normaliser terms; an expert can be in both), then written.
 __global__ __launch_bounds__(256) void k_router_dz(const float* __restrict__ logits, const float* __restrict__ bias,
                                                     const int32_t* __restrict__ idx, moe_plan p,
-                                                    const float* __restrict__ ds, float* __restrict__ dz) {
+                                                    const float* __restrict__ ds, const float* dz_in, float* dz) {
   extern __shared__ float s_rows[];  // four rows of E, then offsets[0 .. E]
   const int L = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int t = blockIdx.x * 4 + wv;
@@ -135,7 +136,8 @@ __global__ __launch_bounds__(256) void k_router_dz(const float* __restrict__ log
   }
   __builtin_amdgcn_s_waitcnt(0xc07f);
   __builtin_amdgcn_wave_barrier();
-  for (int m = L; m < E; m += 64) dz[(size_t)t * E + m] = row[m];
+  // (dz may be dz_in: a lane reads an element before it writes it)
+  for (int m = L; m < E; m += 64) dz[(size_t)t * E + m] = dz_in ? row[m] + dz_in[(size_t)t * E + m] : row[m];
 }
 
 }  // namespace rg
@@ -162,8 +164,8 @@ hipError_t launch_router_logits(moe_dtype dt, const void* x, const float* wr, co
 }
 
 hipError_t launch_router_bwd(moe_dtype dt, const float* logits, const float* bias, const int32_t* idx,
-                             const moe_plan& p, const float* ds, const void* x, const float* wr, int H,
-                             const void* dx_in, void* dx_out, float* dlogits, float* dwr, float* dbias, void* ws,
+                             const moe_plan& p, const float* ds, const float* dz_in, const void* x,
+                             const float* wr, int H, const void* dx_in, void* dx_out, float* dlogits, float* dwr, float* dbias, void* ws,
                              hipStream_t s) {
   const int N = p.N, E = p.E;
   if (N == 0) {
@@ -175,7 +177,7 @@ hipError_t launch_router_bwd(moe_dtype dt, const float* logits, const float* bia
   }
   kernel_event(MOE_K_ROUTER_DZ, 0, s);
   hipLaunchKernelGGL(rg::k_router_dz, dim3((unsigned)((N + 3) / 4)), dim3(256), (size_t)(5 * E + 1) * 4, s, logits, bias,
-                     idx, p, ds, dlogits);
+                     idx, p, ds, dz_in, dlogits);
   kernel_event(MOE_K_ROUTER_DZ, 1, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -80,7 +80,8 @@ typedef enum moe_op {
   MOE_OP_ROUTER_LOGITS = 5,
   MOE_OP_GEMM_FWD_MXFP8 = 6,
   MOE_OP_LAYER_BWD_MXFP8 = 7,
-  MOE_OP_ADD_RMSNORM_BWD = 8
+  MOE_OP_ADD_RMSNORM_BWD = 8,
+  MOE_OP_BALANCE_LOSS = 9
 } moe_op;
 
 /*
@@ -382,6 +383,47 @@ moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, 
                           void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Balance loss and z-loss of the router, with per-expert counts, and their gradient.
+ * The N tokens form B sequences: sequence b is the tokens seq_ptr[b] .. seq_ptr[b+1]-1 (seq_ptr
+ * int32 [B+1], ascending, within [0, N]; NULL: B = 1, all tokens) whose mask byte is not 0 (mask
+ * [N]; NULL: every token).  Tokens before seq_ptr[0], behind seq_ptr[B] or with mask 0 take no
+ * part, whatever their logits hold.  With n_b tokens in sequence b, n in all,
+ *   z[t,e] = logits[t,e] + bias[e]   (bias NULL: none; -inf gives an expert probability 0)
+ *   p = softmax(z) over e, lse_t = log sum_e exp z[t,e]  (all logits -inf: p = 0, lse = 0)
+ *   counts[b,e] = pairs (t, j) of sequence b with topk_idx[t,j] = e (a pair outside [0,E) and a
+ *                 second naming of e by one token count nothing, as in moe_permute)
+ *   loss[0] = alpha / B  sum_b  E / (k n_b^2)  sum_e counts[b,e] sum_t p[t,e]
+ *   loss[1] = beta / n  sum_t lse_t^2
+ * (a sequence without tokens adds 0; counts carry no gradient).  `saved` [B*E + 1] holds what the
+ * gradient needs: saved[b*E + e] = alpha E counts[b,e] / (B k n_b^2), saved[B*E] = 2 beta / n.
+ * moe_balance_loss_bwd, with dloss fp32 [2] the gradients of the two losses (device; NULL: ones):
+ *   dlogits[t,m] = dlogits_in[t,m] + dloss[0] p_m (saved[b,m] - sum_e saved[b,e] p_e)
+ *                                  + dloss[1] saved[B*E] lse_t p_m
+ * (dlogits_in NULL: zeros; tokens that take no part get dlogits_in; dlogits may be dlogits_in).
+ * moe_router_bwd_acc takes the result on.  logits, dlogits fp32 [N,E]; counts int32 [B,E].
+ * 1 <= E <= 1024, 1 <= k <= E, 1 <= B <= 2^20.  Everything is summed in fp32 in a fixed order (bitwise
+ * reproducible).  A seq_ptr that does not ascend gives wrong sums but touches no other memory.
+ * Workspace of moe_balance_loss: moe_workspace_bytes(MOE_OP_BALANCE_LOSS, MOE_F32, N, E, k, 0, B, 0).
+ */
+moe_status moe_balance_loss(const float* logits, const float* bias, const int32_t* topk_idx, const uint8_t* mask,
+                            const int32_t* seq_ptr, int32_t B, int32_t N, int32_t E, int32_t k, float alpha,
+                            float beta, float* loss, int32_t* counts, float* saved, void* ws, size_t ws_bytes,
+                            void* stream);
+moe_status moe_balance_loss_bwd(const float* logits, const float* bias, const uint8_t* mask, const int32_t* seq_ptr,
+                                int32_t B, int32_t N, int32_t E, const float* saved, const float* dloss,
+                                const float* dlogits_in, float* dlogits, void* stream);
+
+/*
+ * moe_router_bwd with a further gradient of the logits, dlogits_in fp32 [N,E] (moe_balance_loss_bwd's;
+ * NULL: none, which is moe_router_bwd): dlogits[t,m] gets dlogits_in[t,m] added before the products,
+ * so dx_out, dw_r and dbias include it.  dlogits may be dlogits_in.
+ */
+moe_status moe_router_bwd_acc(moe_dtype dt, const float* logits, const float* bias, const int32_t* topk_idx,
+                              const moe_plan* plan, const float* ds, const float* dlogits_in, const void* x,
+                              const float* w_r, int32_t H, const void* dx_in, void* dx_out, float* dlogits,
+                              float* dw_r, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Residual addition with RMS norm: what makes the layer's input x (and its MX-FP8 operand) from
  * the residual stream.  For each of N rows of H values,
  *   s = x + res                       (fp32; res NULL: s = x)
@@ -451,7 +493,9 @@ typedef enum moe_kernel_id {
   MOE_K_DX_FP8 = 19,     /* moe_layer_bwd_mxfp8: the dX grouped GEMM on MX-FP8 operands */
   MOE_K_ADD_RMSNORM = 20,     /* moe_add_rmsnorm */
   MOE_K_ADD_RMSNORM_BWD = 21, /* moe_add_rmsnorm_bwd: the row kernel and the sum of dw's partials */
-  MOE_K_COUNT = 22
+  MOE_K_BALANCE = 22,         /* moe_balance_loss */
+  MOE_K_BALANCE_BWD = 23,     /* moe_balance_loss_bwd */
+  MOE_K_COUNT = 24
 } moe_kernel_id;
 
 moe_status moe_set_kernel_events(int32_t kernel_id, void* start_event, void* stop_event);

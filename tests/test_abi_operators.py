@@ -96,3 +96,69 @@ def test_add_rmsnorm_bindings():
         G.add_rmsnorm_bwd(x, r, w, dh_in=r[:1])
     with pytest.raises(TypeError):
         G.add_rmsnorm_bwd(x, r.to(f), w, dh_in=r)
+
+
+def test_balance_loss_errors(L):
+    need = L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 64, 8, 2, 0, 3, 0)
+    assert need > 0
+    assert L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 64, 8, 2, 0, 0, 0) == 0
+    assert L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 64, 8, 9, 0, 1, 0) == 0
+    assert L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 0, 8, 2, 0, 1, 0) > 0
+
+    def call(lg=F, idx=F, ptr=F, B=3, N=64, E=8, k=2, al=0.1, be=0.1, loss=F, cnt=F, sv=F, ws=F, nb=need):
+        return L.moe_balance_loss(lg, None, idx, None, ptr, B, N, E, k, al, be, loss, cnt, sv, ws, nb, None)
+    assert call(nb=need - 1) == G.MOE_EWORKSPACE
+    assert call(ws=None) == G.MOE_EINVAL
+    assert call(ws=ODD) == G.MOE_EUNSUPPORTED
+    assert call(k=9) == G.MOE_EINVAL
+    assert call(E=1025) == G.MOE_EINVAL
+    assert call(N=-1) == G.MOE_EINVAL
+    assert call(B=0) == G.MOE_EINVAL
+    assert call(B=(1 << 20) + 1) == G.MOE_EINVAL
+    assert call(ptr=None) == G.MOE_EINVAL       # three sequences without their ends
+    assert call(lg=None) == G.MOE_EINVAL
+    assert call(idx=None) == G.MOE_EINVAL
+    assert call(loss=None) == G.MOE_EINVAL
+    assert call(sv=None) == G.MOE_EINVAL
+    assert call(al=float("nan")) == G.MOE_EINVAL
+    assert call(be=float("inf")) == G.MOE_EINVAL
+
+    def bwd(lg=F, ptr=F, B=3, N=64, E=8, sv=ctypes.c_void_p(FAKE + 4096), dl=ctypes.c_void_p(FAKE + 8192)):
+        return L.moe_balance_loss_bwd(lg, None, None, ptr, B, N, E, sv, None, None, dl, None)
+    assert bwd(lg=None) == G.MOE_EINVAL
+    assert bwd(dl=None) == G.MOE_EINVAL
+    assert bwd(dl=F) == G.MOE_EINVAL            # over the logits
+    assert bwd(sv=None) == G.MOE_EINVAL
+    assert bwd(B=0) == G.MOE_EINVAL
+    assert bwd(ptr=None) == G.MOE_EINVAL
+    assert bwd(E=0) == G.MOE_EINVAL
+    assert bwd(N=0, lg=None, sv=None, dl=None) == G.MOE_OK
+
+
+def test_balance_loss_bindings():
+    lg, idx = torch.zeros(6, 8), torch.zeros(6, 2, dtype=torch.int32)
+    ptr = torch.tensor([0, 6], dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        G.balance_loss(lg, idx, 0.1, seq_ptr=ptr, mask=torch.ones(6, dtype=torch.bool))
+    with pytest.raises(TypeError):
+        G.balance_loss(lg.bfloat16(), idx, 0.1)
+    with pytest.raises(TypeError):
+        G.balance_loss(lg, idx.long(), 0.1)
+    with pytest.raises(ValueError, match="shape"):
+        G.balance_loss(lg, idx[:5], 0.1)
+    with pytest.raises(ValueError, match="contiguous"):
+        G.balance_loss(torch.zeros(8, 6).t(), idx, 0.1)
+    with pytest.raises(TypeError):
+        G.balance_loss(lg, idx, 0.1, mask=torch.ones(6))
+    with pytest.raises(ValueError, match="shape"):
+        G.balance_loss(lg, idx, 0.1, mask=torch.ones(5, dtype=torch.bool))
+    with pytest.raises(TypeError):
+        G.balance_loss(lg, idx, 0.1, seq_ptr=ptr.long())
+    with pytest.raises(ValueError):
+        G.balance_loss(lg, idx, 0.1, seq_ptr=ptr[:1])
+    with pytest.raises(ValueError, match="shape"):
+        G.balance_loss_bwd(lg, torch.zeros(8))
+    with pytest.raises(TypeError):
+        G.balance_loss_bwd(lg, torch.zeros(9), dloss=torch.ones(2, dtype=torch.float64))
+    with pytest.raises(ValueError, match="GPU"):
+        G.balance_loss_bwd(lg, torch.zeros(9))
