@@ -463,8 +463,7 @@ def router_bwd(logits, topk_idx, plan: Plan, ds, x, w_r, bias=None, dx_in=None, 
         else 0
     ws = _ws(nb, dev, ws) if nb else None
     if dlogits_in is not None:
-        _want("dlogits_in", dlogits_in, (N, E), torch.float32)
-        _same_device(logits, dlogits_in)
+        _want("dlogits_in", dlogits_in, (N, E), torch.float32, logits.get_device())
     _check(lib().moe_router_bwd_acc(dt, _ptr(logits), _ptr(bias), _ptr(topk_idx), plan.c, _ptr(ds), _ptr(dlogits_in),
                                     _ptr(x), _ptr(w_r), H, _ptr(dx_in), _ptr(dx_out), _ptr(dlogits), _ptr(dw_r),
                                     _ptr(dbias), _ptr(ws), nb, _stream(stream)))
@@ -472,29 +471,43 @@ def router_bwd(logits, topk_idx, plan: Plan, ds, x, w_r, bias=None, dx_in=None, 
 
 
 # ---- the operators around the layer: these bindings check every tensor they are given ----
-def _want(name, t, shape, dtype):
-    """Refuse a tensor whose type, shape or layout (contiguous, row-major) is not the one asked for."""
-    if t.dtype != dtype:
+def _want(name, t, shape, dtype, dev):
+    """Refuse a tensor whose type, shape, layout (contiguous, row-major) or device (index dev, -1: the
+    host, which the call itself refuses) is not the one asked for."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (strides {t.stride()})")
-    return t
+    raise ValueError(f"tensors on different devices: {name} is on {t.device}")
 
 
-def _out(name, t, shape, dtype, like):
+def _out(name, t, shape, dtype, like, dev):
     """The caller's output tensor, checked, or a new one."""
+    return like.new_empty(shape, dtype=dtype) if t is None else _want(name, t, shape, dtype, dev)
+
+
+def _on_gpu(t):
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a GPU (got {t.device})")
+
+
+@functools.lru_cache(maxsize=1024)
+def _op_bytes(*query) -> int:
+    return workspace_bytes(*query)
+
+
+def _op_ws(nbytes, like, ws, dev):
+    """The caller's workspace, checked, or a new one."""
     import torch
-    return torch.empty(shape, dtype=dtype, device=like.device) if t is None else _want(name, t, shape, dtype)
-
-
-def _same_device(first, *others):
-    if not first.is_cuda:
-        raise ValueError(f"tensors must be on a GPU (got {first.device})")
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if ws is None:
+        return like.new_empty((nbytes,), dtype=torch.uint8)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on the tensors' device (is on {ws.device})")
+    return _ws(nbytes, None, ws)
 
 
 def _addr(t):
@@ -507,10 +520,9 @@ def _on_stream(fn):
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         import torch
-        if not first.is_cuda:
-            return fn(first, *args, **kw)  # refused there
-        if stream is None and first.device.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
+        if stream is None and (not first.is_cuda or first.get_device() == torch.cuda.current_device()):
+            return fn(first, *args, **kw)  # (a host tensor is refused there)
+        _on_gpu(first)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
         with torch.cuda.device(first.device):
@@ -521,10 +533,10 @@ def _on_stream(fn):
     return call
 
 
-def _cur(t):
-    """The current stream's handle on t's device."""
+def _cur(dev):
+    """The current stream's handle on device dev."""
     import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 @_on_stream
@@ -542,26 +554,28 @@ def add_rmsnorm(x, w=None, residual=None, eps: float = 1e-6, want_h=True, want_y
     N, H = x.shape
     dt = _dtype_code(x)
     rtype = x.dtype if residual is None else residual.dtype
-    _want("x", x, (N, H), x.dtype)
+    dev = x.get_device()
+    _want("x", x, (N, H), x.dtype, dev)
     if residual is not None:
-        _want("residual", residual, (N, H), rtype)
+        _want("residual", residual, (N, H), rtype, dev)
         rdt = _dtype_code(residual)
     else:
         if h is not None and h.dtype == torch.float32:
             rtype = torch.float32
         rdt = MOE_F32 if rtype == torch.float32 else dt
     if w is not None:
-        _want("w", w, (H,), torch.float32)
-    want_h, want_y = want_h or h is not None, want_y or y is not None
-    quantize = quantize or q is not None or scales is not None
-    _same_device(x, residual, w, h, y, q, scales)
-    h = _out("h", h, (N, H), rtype, x) if want_h else None
-    y = _out("y", y, (N, H), x.dtype, x) if want_y else None
-    q = _out("q", q, (N, H), torch.uint8, x) if quantize else None
-    scales = _out("scales", scales, (N, mx_scale_cols(H)), torch.uint8, x) if quantize else None
+        _want("w", w, (H,), torch.float32, dev)
+    _on_gpu(x)
+    if want_h or h is not None:
+        h = _out("h", h, (N, H), rtype, x, dev)
+    if want_y or y is not None:
+        y = _out("y", y, (N, H), x.dtype, x, dev)
+    if quantize or q is not None or scales is not None:
+        q = _out("q", q, (N, H), torch.uint8, x, dev)
+        scales = _out("scales", scales, (N, mx_scale_cols(H)), torch.uint8, x, dev)
     if N:
         _check(lib().moe_add_rmsnorm(dt, rdt, x.data_ptr(), _addr(residual), _addr(w), eps, N, H, _addr(h), _addr(y),
-                                     _addr(q), _addr(scales), _cur(x)))
+                                     _addr(q), _addr(scales), _cur(dev)))
     return dict(h=h, y=y, q=q, scales=scales)
 
 
@@ -576,37 +590,39 @@ def add_rmsnorm_bwd(dy, h, w=None, dh_in=None, eps: float = 1e-6, want_dx=False,
         raise ValueError(f"dy must be [N, H] (got {tuple(dy.shape)})")
     N, H = dy.shape
     dt, rdt = _dtype_code(dy), _dtype_code(h)
-    _want("dy", dy, (N, H), dy.dtype)
-    _want("h", h, (N, H), h.dtype)
+    dev = dy.get_device()
+    _want("dy", dy, (N, H), dy.dtype, dev)
+    _want("h", h, (N, H), h.dtype, dev)
     if dh_in is not None:
-        _want("dh_in", dh_in, (N, H), h.dtype)
+        _want("dh_in", dh_in, (N, H), h.dtype, dev)
     if w is not None:
-        _want("w", w, (H,), torch.float32)
-    _same_device(dy, h, dh_in, w, dh, dx, dw, ws)
-    dh = _out("dh", dh, (N, H), h.dtype, dy)
-    dx = _out("dx", dx, (N, H), dy.dtype, dy) if want_dx or dx is not None else None
-    dw = _out("dw", dw, (H,), torch.float32, dy) if want_dw or dw is not None else None
+        _want("w", w, (H,), torch.float32, dev)
+    _on_gpu(dy)
+    dh = _out("dh", dh, (N, H), h.dtype, dy, dev)
+    if want_dx or dx is not None:
+        dx = _out("dx", dx, (N, H), dy.dtype, dy, dev)
     nb = 0
-    if dw is not None:
-        nb = workspace_bytes(OP_ADD_RMSNORM_BWD, dt, N, 1, 1, H, 0, 0)
-        ws = _ws(nb, dy.device, ws)
+    if want_dw or dw is not None:
+        dw = _out("dw", dw, (H,), torch.float32, dy, dev)
+        nb = _op_bytes(OP_ADD_RMSNORM_BWD, dt, N, 1, 1, H, 0, 0)
+        ws = _op_ws(nb, dy, ws, dev)
     _check(lib().moe_add_rmsnorm_bwd(dt, rdt, dy.data_ptr(), h.data_ptr(), _addr(dh_in), _addr(w), eps, N, H,
-                                     dh.data_ptr(), _addr(dx), _addr(dw), _addr(ws) if nb else None, nb, _cur(dy)))
+                                     dh.data_ptr(), _addr(dx), _addr(dw), _addr(ws) if nb else None, nb, _cur(dev)))
     return dict(dh=dh, dx=dx, dw=dw)
 
 
-def _seqs(N, mask, seq_ptr):
+def _seqs(N, mask, seq_ptr, dev):
     """The sequences' checks shared by balance_loss and its backward -> B."""
     import torch
     if mask is not None:
         if mask.dtype not in (torch.uint8, torch.bool):
             raise TypeError(f"mask must be uint8 or bool (got {mask.dtype})")
-        _want("mask", mask, (N,), mask.dtype)
+        _want("mask", mask, (N,), mask.dtype, dev)
     if seq_ptr is None:
         return 1
     if seq_ptr.dim() != 1 or seq_ptr.shape[0] < 2:
         raise ValueError(f"seq_ptr must be [B + 1], B >= 1 (got {tuple(seq_ptr.shape)})")
-    _want("seq_ptr", seq_ptr, seq_ptr.shape, torch.int32)
+    _want("seq_ptr", seq_ptr, seq_ptr.shape, torch.int32, dev)
     return seq_ptr.shape[0] - 1
 
 
@@ -624,19 +640,20 @@ def balance_loss(logits, topk_idx, alpha: float, beta: float = 0.0, bias=None, m
         raise ValueError("logits must be [N, E] and topk_idx [N, k]")
     N, E = logits.shape
     k = topk_idx.shape[1]
-    _want("logits", logits, (N, E), torch.float32)
-    _want("topk_idx", topk_idx, (N, k), torch.int32)
+    dev = logits.get_device()
+    _want("logits", logits, (N, E), torch.float32, dev)
+    _want("topk_idx", topk_idx, (N, k), torch.int32, dev)
     if bias is not None:
-        _want("bias", bias, (E,), torch.float32)
-    B = _seqs(N, mask, seq_ptr)
-    _same_device(logits, topk_idx, bias, mask, seq_ptr, loss, counts, saved, ws)
-    loss = _out("loss", loss, (2,), torch.float32, logits)
-    counts = _out("counts", counts, (B, E), torch.int32, logits)
-    saved = _out("saved", saved, (B * E + 1,), torch.float32, logits)
-    nb = workspace_bytes(OP_BALANCE_LOSS, MOE_F32, N, E, k, 0, B)
-    ws = _ws(nb, logits.device, ws)
+        _want("bias", bias, (E,), torch.float32, dev)
+    B = _seqs(N, mask, seq_ptr, dev)
+    _on_gpu(logits)
+    loss = _out("loss", loss, (2,), torch.float32, logits, dev)
+    counts = _out("counts", counts, (B, E), torch.int32, logits, dev)
+    saved = _out("saved", saved, (B * E + 1,), torch.float32, logits, dev)
+    nb = _op_bytes(OP_BALANCE_LOSS, MOE_F32, N, E, k, 0, B, 0)
+    ws = _op_ws(nb, logits, ws, dev)
     _check(lib().moe_balance_loss(_addr(logits), _addr(bias), _addr(topk_idx), _addr(mask), _addr(seq_ptr), B, N, E, k,
-                                  alpha, beta, _addr(loss), _addr(counts), _addr(saved), _addr(ws), nb, _cur(logits)))
+                                  alpha, beta, _addr(loss), _addr(counts), _addr(saved), _addr(ws), nb, _cur(dev)))
     return dict(loss=loss, counts=counts, saved=saved)
 
 
@@ -649,17 +666,18 @@ def balance_loss_bwd(logits, saved, bias=None, mask=None, seq_ptr=None, dloss=No
     if logits.dim() != 2:
         raise ValueError(f"logits must be [N, E] (got {tuple(logits.shape)})")
     N, E = logits.shape
-    _want("logits", logits, (N, E), torch.float32)
+    dev = logits.get_device()
+    _want("logits", logits, (N, E), torch.float32, dev)
     if bias is not None:
-        _want("bias", bias, (E,), torch.float32)
-    B = _seqs(N, mask, seq_ptr)
-    _want("saved", saved, (B * E + 1,), torch.float32)
+        _want("bias", bias, (E,), torch.float32, dev)
+    B = _seqs(N, mask, seq_ptr, dev)
+    _want("saved", saved, (B * E + 1,), torch.float32, dev)
     if dloss is not None:
-        _want("dloss", dloss, (2,), torch.float32)
+        _want("dloss", dloss, (2,), torch.float32, dev)
     if dlogits_in is not None:
-        _want("dlogits_in", dlogits_in, (N, E), torch.float32)
-    _same_device(logits, saved, bias, mask, seq_ptr, dloss, dlogits_in, dlogits)
-    dlogits = _out("dlogits", dlogits, (N, E), torch.float32, logits)
+        _want("dlogits_in", dlogits_in, (N, E), torch.float32, dev)
+    _on_gpu(logits)
+    dlogits = _out("dlogits", dlogits, (N, E), torch.float32, logits, dev)
     _check(lib().moe_balance_loss_bwd(_addr(logits), _addr(bias), _addr(mask), _addr(seq_ptr), B, N, E, _addr(saved),
-                                      _addr(dloss), _addr(dlogits_in), _addr(dlogits), _cur(logits)))
+                                      _addr(dloss), _addr(dlogits_in), _addr(dlogits), _cur(dev)))
     return dlogits

@@ -30,7 +30,8 @@ __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
 }
 struct Add { __device__ static __forceinline__ float op(float a, float b) { return a + b; } };
-struct Max { __device__ static __forceinline__ float op(float a, float b) { return fmaxf(a, b); } };
+// (a NaN stays one, unlike with fmaxf)
+struct Max { __device__ static __forceinline__ float op(float a, float b) { return __builtin_elementwise_maximum(a, b); } };
 template <int LP, class O>
 __device__ __forceinline__ float group(float v) {
   if constexpr (LP >= 2) v = O::op(v, dpp<0xB1>(v));    // lane ^ 1
@@ -55,15 +56,15 @@ __device__ __forceinline__ float across(float v) {
   return v;
 }
 
-// e^x for x <= 0 to about one unit in the last place: 2^(x log2 e) with the product's rounding
-// error and log2 e's own carried as a first-order factor (v_exp_f32 alone would lose about
-// |x| 2^-24).  Below -200 it is 0, at -infinity too; a NaN stays one.
+// e^x for x <= 0 as 2^(x log2 e), the product's rounding error carried as a first-order factor
+// (v_exp_f32 of the rounded product alone would lose about |x| 2^-24; log2 e's own rounding costs
+// |x| 2^-26).  Below -200, at -infinity too, it is 0.  A NaN counts as -200: softmax() adds it
+// back for the whole token.
 __device__ __forceinline__ float exp_neg(float x) {
-  x = x < -200.f ? -200.f : x;
-  const float hi = 1.44269504088896340736f;                                // log2 e, rounded
-  const float lo = (float)(1.44269504088896340736 - (double)1.44269504088896340736f);
-  const float t = x * hi;
-  const float e = __builtin_fmaf(x, lo, __builtin_fmaf(x, hi, -t));
+  x = fmaxf(x, -200.f);
+  const float c = 1.44269504088896340736f;  // log2 e
+  const float t = x * c;
+  const float e = __builtin_fmaf(x, c, -t);
   const float r = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(r, e * 0.6931471805599453f, r);
 }
@@ -84,35 +85,34 @@ __device__ __forceinline__ void load_row(const float* __restrict__ p, int E, int
   }
 }
 
-// z -> e^(z - max) / sum in place, and the token's log sum exp.  A token whose logits are all -inf
-// has p = 0 and lse = 0.
+// z -> e^(z - max) in place; the caller gets 1 / sum and the token's log sum exp (hardware
+// reciprocal and logarithm, one unit in the last place each).  A token whose logits are all -inf has
+// 1 / sum = 0 and lse = 0; one with a NaN or +inf has NaN for both.
 template <int VW, int LP, int Q>
-__device__ __forceinline__ float softmax(float (&z)[Q][VW], const float (&b)[Q][VW]) {
+__device__ __forceinline__ float2 softmax(float (&z)[Q][VW], const float (&b)[Q][VW]) {
   float m = -__builtin_inff();
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int v = 0; v < VW; ++v) {
       z[q][v] += b[q][v];
-      m = fmaxf(m, z[q][v]);
+      m = __builtin_elementwise_maximum(m, z[q][v]);
     }
   m = group<LP, Max>(m);
-  const bool none = m == -__builtin_inff();
+  m = m == -__builtin_inff() ? 0.f : m;
   float s = 0.f;
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int v = 0; v < VW; ++v) {
-      z[q][v] = none && !(z[q][v] != z[q][v]) ? 0.f : exp_neg(z[q][v] - m);
+      z[q][v] = exp_neg(z[q][v] - m);
       s += z[q][v];
     }
   s = group<LP, Add>(s);
-  const float inv = none && s == 0.f ? 0.f : 1.0f / s;
-#pragma unroll
-  for (int q = 0; q < Q; ++q)
-#pragma unroll
-    for (int v = 0; v < VW; ++v) z[q][v] *= inv;
-  return none && s == 0.f ? 0.f : m + logf(s);
+  const float nan = m - m;  // 0, or NaN where m is NaN or infinite
+  const bool none = s == 0.f;
+  return make_float2((none ? 0.f : __builtin_amdgcn_rcpf(s)) + nan,
+                     (none ? 0.f : __builtin_fmaf(__builtin_amdgcn_logf(s), 0.6931471805599453f, m)) + nan);
 }
 
 // The first sequence b in [0, B) that ends behind token t (ptr[b+1] > t), or B: 64 probes a round.
@@ -160,22 +160,29 @@ __device__ __forceinline__ int seq_hi(const Args& a, int b, int lo) {
   return a.ptr ? min(max(a.ptr[b + 1], lo), a.N) : a.N;
 }
 
+// The expert of this lane's pair of the wavefront's next 64 / k tokens from t0 on (k <= 64), -1 for
+// none.  Its load is issued well before count_pairs needs the value.
+__device__ __forceinline__ int load_pair(const Args& a, int t0, int te) {
+  const int L = threadIdx.x & 63, k = a.k, tpw = 64 / k, tt = L / k, t = t0 + tt;
+  return tt < tpw && t < te && (!a.mask || a.mask[t]) ? a.idx[(size_t)t * k + (L - tt * k)] : -1;
+}
+
 // Counts the pairs of tokens [ts, te) into the LDS histogram: an index outside [0, E) and a second
-// naming of an expert by one token count nothing (they make no row of a plan either).
-__device__ __forceinline__ void count_pairs(const Args& a, int ts, int te, int* hist, uint32_t (*bits)[32]) {
+// naming of an expert by one token count nothing (they make no row of a plan either).  e: the
+// lane's first pair (load_pair at the wavefront's first token; k <= 64).
+__device__ __forceinline__ void count_pairs(const Args& a, int ts, int te, int e, int* hist, uint32_t (*bits)[32]) {
   const int wv = threadIdx.x >> 6, L = threadIdx.x & 63, k = a.k, E = a.E;
   if (k <= 64) {
-    const int tpw = 64 / k, tt = L / k, j = L - tt * k;  // tokens per wavefront at a time
+    const int tpw = 64 / k, j = L % k;  // tokens per wavefront at a time
     for (int t0 = ts + wv * tpw; t0 < te; t0 += 4 * tpw) {
-      const int t = t0 + tt;
-      int e = -1;
-      if (tt < tpw && t < te && (!a.mask || a.mask[t])) e = a.idx[(size_t)t * k + j];
+      const int next = load_pair(a, t0 + 4 * tpw, te);
       bool ok = e >= 0 && e < E;
       for (int d = 1; d < k; ++d) {
         const int o = __shfl_up(e, d);
         if (j >= d && o == e) ok = false;
       }
       if (ok) atomicAdd(&hist[e], 1);
+      e = next;
     }
   } else {
     for (int t = ts + wv; t < te; t += 4) {
@@ -184,10 +191,10 @@ __device__ __forceinline__ void count_pairs(const Args& a, int ts, int te, int* 
       __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
       __builtin_amdgcn_wave_barrier();
       for (int j = L; j < k; j += 64) {
-        const int e = a.idx[(size_t)t * k + j];
-        if (e < 0 || e >= E) continue;
-        const uint32_t bit = 1u << (e & 31);
-        if (!(atomicOr(&bits[wv][e >> 5], bit) & bit)) atomicAdd(&hist[e], 1);
+        const int x = a.idx[(size_t)t * k + j];
+        if (x < 0 || x >= E) continue;
+        const uint32_t bit = 1u << (x & 31);
+        if (!(atomicOr(&bits[wv][x >> 5], bit) & bit)) atomicAdd(&hist[x], 1);
       }
       __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -247,6 +254,7 @@ __global__ __launch_bounds__(NT) void k_balance(Args a) {
     if (!ONE && lo >= t1) break;
     const int ts = max(lo, t0), te = min(seq_hi(a, b, lo), t1);
     if (!ONE && ts >= te) continue;
+    const int pair = a.k <= 64 ? load_pair(a, ts + wv * (64 / a.k), te) : -1;
     for (int e = threadIdx.x; e < EP; e += NT) s_hist[e] = 0;
     __syncthreads();  // (the previous sequence's readers of s_sum and s_hist are done as well)
     float acc[Q][VW];
@@ -266,17 +274,17 @@ __global__ __launch_bounds__(NT) void k_balance(Args a) {
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float lse = softmax<VW, LP, Q>(z[u], bias);
+        const float2 il = softmax<VW, LP, Q>(z[u], bias);  // 1 / sum, lse
         if (live[u]) {  // (a token left out may hold anything: nothing of it is added)
 #pragma unroll
           for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int v = 0; v < VW; ++v) acc[q][v] += z[u][q][v];
-          if (l == 0) zsum += lse * lse, ++nt;
+            for (int v = 0; v < VW; ++v) acc[q][v] += z[u][q][v] * il.x;
+          if (l == 0) zsum += il.y * il.y, ++nt;
         }
       }
     }
-    count_pairs(a, ts, te, s_hist, s_bits);
+    count_pairs(a, ts, te, pair, s_hist, s_bits);
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -368,16 +376,18 @@ __global__ __launch_bounds__(1024) void k_balance_sum(Args a, int nch) {
       a.saved[(size_t)a.B * E] = n > 0 ? 2.f * a.beta / (float)n : 0.f;
     }
   }
-  // the last workgroup to come adds the shares of L0, in their order
+  // The last workgroup to come adds the shares of L0, in their order.  Each share is stored with
+  // device scope (past this XCD's L2) and has arrived before its ticket is drawn (the wait); the
+  // last one reads them with device scope.  So nothing else needs to leave the L2s: a device-scope
+  // fence, which writes back every dirty line there, cost 3 us of the 8.7 at N = 4096, E = 128.
   const unsigned total = gridDim.x;
   if (threadIdx.x == 0) {
     __hip_atomic_store(&a.part[blockIdx.x], l0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __threadfence();
-    s_last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    s_last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   float v = 0.f;
   for (unsigned i = threadIdx.x; i < total; i += 1024)
     v += __hip_atomic_load(&a.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -457,18 +467,18 @@ __global__ __launch_bounds__(NT) void k_balance_bwd(BwdArgs a) {
     if (in) {
       float gr[Q][VW];
       load_row<VW, LP, Q>(a.saved + (size_t)lo * E, E, l, 0.f, gr);
-      const float lse = softmax<VW, LP, Q>(z[u], bias);
+      const float2 il = softmax<VW, LP, Q>(z[u], bias);  // 1 / sum, lse
       float dot = 0.f;
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int v = 0; v < VW; ++v) dot += gr[q][v] * z[u][q][v];
-      dot = group<LP, Add>(dot);
-      const float zc = d1 * lse;
+      dot = group<LP, Add>(dot) * il.x;
+      const float zc = d1 * il.y;
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int v = 0; v < VW; ++v) o[q][v] = di[u][q][v] + z[u][q][v] * (d0 * (gr[q][v] - dot) + zc);
+        for (int v = 0; v < VW; ++v) o[q][v] = di[u][q][v] + z[u][q][v] * il.x * (d0 * (gr[q][v] - dot) + zc);
     } else {
 #pragma unroll
       for (int q = 0; q < Q; ++q)

@@ -169,23 +169,29 @@ struct BwdArgs {
   float eps;
 };
 
-// One row per workgroup of 64 WR threads at a time, rows blockIdx.x, blockIdx.x + gridDim.x, ...;
-// the column sums of dw stay in registers over the workgroup's rows.
-template <typename T, typename R, int WR, int V>
-__global__ __launch_bounds__(64 * WR) void k_add_rmsnorm_bwd(BwdArgs a) {
-  __shared__ float2 red[2][WR];
-  const int ww = threadIdx.x >> 6, L = threadIdx.x & 63;
+// RG rows per workgroup of 64 WR RG threads at a time, WR wavefronts on each: rows blockIdx.x RG + g,
+// then gridDim.x RG further on.  The column sums of dw stay in registers over a workgroup's rows
+// and its RG groups' sums are added in order through LDS.
+template <typename T, typename R, int WR, int V, int RG>
+__global__ __launch_bounds__(64 * WR * RG) void k_add_rmsnorm_bwd(BwdArgs a) {
+  __shared__ float2 red[2][RG][WR];
+  __shared__ float4 s_dw[RG > 1 ? 64 * WR * V * 2 : 1];
+  const int g = threadIdx.x / (64 * WR), tr = threadIdx.x % (64 * WR);
+  const int ww = tr >> 6, L = threadIdx.x & 63;
   const int H = a.H, nc = H >> 3;
   float w[V][8], dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = threadIdx.x + 64 * WR * i;
+    const int c = tr + 64 * WR * i;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = 1.f, dw[i][j] = 0.f;
     if (a.w && c < nc) ld8(a.w + 8 * c, w[i]);
   }
   int par = 0;
-  for (long long row = blockIdx.x; row < a.N; row += gridDim.x, par ^= 1) {
+  // (every group makes the same number of turns: the barrier inside meets all wavefronts)
+  for (long long r0 = (long long)blockIdx.x * RG; r0 < a.N; r0 += (long long)gridDim.x * RG, par ^= 1) {
+    const long long row = r0 + g;
+    const bool live = row < a.N;
     const long long base = row * H;
     const T* dy = static_cast<const T*>(a.dy) + base;
     const R* h = static_cast<const R*>(a.h) + base;
@@ -193,10 +199,10 @@ __global__ __launch_bounds__(64 * WR) void k_add_rmsnorm_bwd(BwdArgs a) {
     float vh[V][8], vd[V][8], vi[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + 64 * WR * i;
+      const int c = tr + 64 * WR * i;
 #pragma unroll
       for (int j = 0; j < 8; ++j) vh[i][j] = 0.f, vd[i][j] = 0.f, vi[i][j] = 0.f;
-      if (c < nc) {
+      if (live && c < nc) {
         ld8(h + 8 * c, vh[i]);
         ld8(dy + 8 * c, vd[i]);
         if (din) ld8(din + 8 * c, vi[i]);
@@ -213,24 +219,25 @@ __global__ __launch_bounds__(64 * WR) void k_add_rmsnorm_bwd(BwdArgs a) {
     p.x = wave_sum(p.x);
     p.y = wave_sum(p.y);
     if constexpr (WR > 1) {
-      // two slots by row parity: a wavefront writes a slot again only after the next row's barrier
-      if (L == 0) red[par][ww] = p;
+      // two slots by turn: a wavefront writes a slot again only after the next turn's barrier
+      if (L == 0) red[par][g][ww] = p;
       __syncthreads();
       p = make_float2(0.f, 0.f);
 #pragma unroll
       for (int q = 0; q < WR; ++q) {
-        const float2 t = red[par][q];
+        const float2 t = red[par][g][q];
         p.x += t.x;
         p.y += t.y;
       }
     }
     const float r = 1.0f / sqrtf(p.x / (float)H + a.eps);
     const float m = r * r * (p.y / (float)H);
+    if (!live) continue;  // (its wavefronts' sums took part in no other row)
     R* dh = static_cast<R*>(a.dh) + base;
     T* dx = a.dx ? static_cast<T*>(a.dx) + base : nullptr;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + 64 * WR * i;
+      const int c = tr + 64 * WR * i;
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -243,34 +250,69 @@ __global__ __launch_bounds__(64 * WR) void k_add_rmsnorm_bwd(BwdArgs a) {
       }
     }
   }
-  if (a.part) {
+  if (!a.part) return;
+  if constexpr (RG > 1) {
+    for (int q = 1; q < RG; ++q) {
+      __syncthreads();
+      if (g == q) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          s_dw[(i * 2) * 64 * WR + tr] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+          s_dw[(i * 2 + 1) * 64 * WR + tr] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        }
+      }
+      __syncthreads();
+      if (g == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float4 u = s_dw[(i * 2) * 64 * WR + tr], v = s_dw[(i * 2 + 1) * 64 * WR + tr];
+          dw[i][0] += u.x; dw[i][1] += u.y; dw[i][2] += u.z; dw[i][3] += u.w;
+          dw[i][4] += v.x; dw[i][5] += v.y; dw[i][6] += v.z; dw[i][7] += v.w;
+        }
+      }
+    }
+  }
+  if (g == 0) {
     float* part = a.part + (size_t)blockIdx.x * H;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + 64 * WR * i;
+      const int c = tr + 64 * WR * i;
       if (c < nc) st8(part + 8 * c, dw[i]);
     }
   }
 }
 
-// dw [H] from G partial rows [G, H]: a workgroup owns 64 columns; thread (g, c) sums the rows g,
-// g + 16, ... of four columns, then the 16 sums are added in order.
-__global__ __launch_bounds__(256) void k_dw_reduce(const float* __restrict__ part, int G, int H,
-                                                   float* __restrict__ dw) {
-  __shared__ float4 s[16][16];
-  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int col = blockIdx.x * 64 + 4 * c;
+// dw [H] from G partial rows [G, H]: a workgroup owns 32 columns; thread (g, c) sums the rows g,
+// g + 128, ... of four columns, then the 128 sums are added in a fixed order.
+__global__ __launch_bounds__(1024) void k_dw_reduce(const float* __restrict__ part, int G, int H,
+                                                    float* __restrict__ dw) {
+  __shared__ float4 s[128][8];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + 4 * c;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < H) {
-    for (int q = g; q < G; q += 16) {
+#pragma unroll 4
+    for (int q = g; q < G; q += 128) {
       const float4 u = *reinterpret_cast<const float4*>(part + (size_t)q * H + col);
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
   }
-  s[g][c] = v;
+#pragma unroll
+  for (int n = 128; n > 8; n /= 4) {
+    s[g][c] = v;
+    __syncthreads();
+    if (g < n / 4)
+      for (int q = 1; q < 4; ++q) {
+        const float4 u = s[g + q * (n / 4)][c];
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+      }
+    __syncthreads();
+  }
+  // eight rows are left (128 / 4 / 4)
+  if (g < 8) s[g][c] = v;
   __syncthreads();
   if (g == 0 && col < H) {
-    for (int q = 1; q < 16; ++q) {
+    for (int q = 1; q < 8; ++q) {
       const float4 u = s[q][c];
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
@@ -292,23 +334,25 @@ void fwd(const FwdArgs& a, hipStream_t s) {
   if (nc <= 64) NORM_FWD(1, 1);
   else if (nc <= 128) NORM_FWD(1, 2);
   else if (nc <= 256) NORM_FWD(4, 1);
-  else if (nc <= 512) NORM_FWD(4, 2);
-  else if (nc <= 1024) NORM_FWD(4, 4);
+  else if (nc <= 512) NORM_FWD(8, 1);
+  else if (nc <= 1024) NORM_FWD(8, 2);
   else NORM_FWD(16, 2);
 #undef NORM_FWD
 }
 
+template <typename T, typename R, int WR, int V, int RG>
+void bwd1(const BwdArgs& a, int G, hipStream_t s) {
+  hipLaunchKernelGGL((k_add_rmsnorm_bwd<T, R, WR, V, RG>), dim3(G), dim3(64 * WR * RG), 0, s, a);
+}
 template <typename T, typename R>
 void bwd(const BwdArgs& a, int G, hipStream_t s) {
   const int nc = a.H / 8;
-#define NORM_BWD(WR, V) hipLaunchKernelGGL((k_add_rmsnorm_bwd<T, R, WR, V>), dim3(G), dim3(64 * WR), 0, s, a)
-  if (nc <= 64) NORM_BWD(1, 1);
-  else if (nc <= 128) NORM_BWD(2, 1);
-  else if (nc <= 256) NORM_BWD(4, 1);
-  else if (nc <= 512) NORM_BWD(4, 2);
-  else if (nc <= 1024) NORM_BWD(8, 2);
-  else NORM_BWD(16, 2);
-#undef NORM_BWD
+  if (nc <= 64) bwd1<T, R, 1, 1, 4>(a, G, s);
+  else if (nc <= 128) bwd1<T, R, 2, 1, 4>(a, G, s);
+  else if (nc <= 256) bwd1<T, R, 4, 1, 2>(a, G, s);
+  else if (nc <= 512) bwd1<T, R, 8, 1, 2>(a, G, s);
+  else if (nc <= 1024) bwd1<T, R, 8, 2, 1>(a, G, s);
+  else bwd1<T, R, 16, 2, 1>(a, G, s);
 }
 
 // workgroups of the backward
@@ -343,7 +387,7 @@ hipError_t launch_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, c
   else if (rdt == MOE_F32) nm::bwd<bf16_t, float>(a, G, s);
   else nm::bwd<bf16_t, bf16_t>(a, G, s);
   if (dw && G > 1)
-    hipLaunchKernelGGL(nm::k_dw_reduce, dim3((unsigned)((H + 63) / 64)), dim3(256), 0, s, part, G, H, dw);
+    hipLaunchKernelGGL(nm::k_dw_reduce, dim3((unsigned)((H + 31) / 32)), dim3(1024), 0, s, part, G, H, dw);
   return hipGetLastError();
 }
 
