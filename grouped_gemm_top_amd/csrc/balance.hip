@@ -227,7 +227,7 @@ __device__ __forceinline__ int block_sum(int v, int* s) {
 template <int VW, int LP, int Q, bool ONE>
 __global__ __launch_bounds__(NT) void k_balance(Args a) {
   constexpr int SL = NT / LP, EP = LP * Q * VW;         // token slots; padded row
-  constexpr int U = Q * VW >= 16 ? 1 : (Q * VW >= 8 ? 2 : 4);  // tokens in flight per slot
+  constexpr int U = Q * VW >= 8 ? 1 : 2;  // tokens in flight per slot
   __shared__ float s_sum[4][EP];
   __shared__ int s_hist[EP];
   __shared__ uint32_t s_bits[4][32];
@@ -263,23 +263,38 @@ __global__ __launch_bounds__(NT) void k_balance(Args a) {
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int v = 0; v < VW; ++v) acc[q][v] = 0.f;
+    // The next U tokens' loads are issued before this turn's are used.
+    float z[U][Q][VW];
+    int mk[U];
+    auto load = [&](int tb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = min(tb + u * SL + slot, te - 1);
+        load_row<VW, LP, Q>(a.logits + (size_t)t * E, E, l, -__builtin_inff(), z[u]);
+        mk[u] = a.mask ? a.mask[t] : 1;
+      }
+    };
+    if (ts < te) load(ts);
     for (int tb = ts; tb < te; tb += U * SL) {
-      float z[U][Q][VW];
+      float c[U][Q][VW];
       bool live[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = tb + u * SL + slot;
-        live[u] = t < te && (!a.mask || a.mask[t]);
-        load_row<VW, LP, Q>(a.logits + (size_t)min(t, te - 1) * E, E, l, -__builtin_inff(), z[u]);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int v = 0; v < VW; ++v) c[u][q][v] = z[u][q][v];
+        live[u] = tb + u * SL + slot < te && mk[u] != 0;
       }
+      if (tb + U * SL < te) load(tb + U * SL);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float2 il = softmax<VW, LP, Q>(z[u], bias);  // 1 / sum, lse
+        const float2 il = softmax<VW, LP, Q>(c[u], bias);  // 1 / sum, lse
         if (live[u]) {  // (a token left out may hold anything: nothing of it is added)
 #pragma unroll
           for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int v = 0; v < VW; ++v) acc[q][v] += z[u][q][v] * il.x;
+            for (int v = 0; v < VW; ++v) acc[q][v] += c[u][q][v] * il.x;
           if (l == 0) zsum += il.y * il.y, ++nt;
         }
       }
@@ -434,12 +449,12 @@ __global__ __launch_bounds__(NT) void k_balance_bwd(BwdArgs a) {
       bias[q][v] = a.bias && e < E ? a.bias[e] : 0.f;
     }
   float z[U][Q][VW], di[U][Q][VW];
-  bool live[U];
+  int mk[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int t = (int)min(tb + u * SL + slot, (long long)tl);
-    live[u] = tb + u * SL + slot <= tl && (!a.mask || a.mask[t]);
     load_row<VW, LP, Q>(a.logits + (size_t)t * E, E, l, -__builtin_inff(), z[u]);
+    mk[u] = a.mask ? a.mask[t] : 1;
     if (a.din) {
       load_row<VW, LP, Q>(a.din + (size_t)t * E, E, l, 0.f, di[u]);
     } else {
@@ -462,7 +477,7 @@ __global__ __launch_bounds__(NT) void k_balance_bwd(BwdArgs a) {
       const int mid = (lo + hi) >> 1;
       if (a.ptr[mid + 1] > t) hi = mid; else lo = mid + 1;
     }
-    const bool in = live[u] && lo < a.B && (!a.ptr || a.ptr[lo] <= t);
+    const bool in = mk[u] != 0 && lo < a.B && (!a.ptr || a.ptr[lo] <= t);
     float o[Q][VW];
     if (in) {
       float gr[Q][VW];
