@@ -20,7 +20,8 @@ __all__ = [
     "MOE_EHIP", "OP_PERMUTE", "OP_ROUTE_TR", "OP_GEMM_FWD", "OP_LAYER_BWD", "OP_ROUTER_BWD",
     "OP_ROUTER_LOGITS", "PLAN_TOPK", "PLAN_TR", "PLAN_CAP", "CAP_POSITION", "CAP_PROBS",
     "EXPORTED_SYMBOLS", "KERNEL_IDS", "set_kernel_events", "add_rmsnorm", "add_rmsnorm_bwd", "OP_ADD_RMSNORM_BWD",
-    "balance_loss", "balance_loss_bwd", "OP_BALANCE_LOSS",
+    "balance_loss", "balance_loss_bwd", "OP_BALANCE_LOSS", "linear_fwd", "linear_bwd", "OP_LINEAR_FWD", "OP_LINEAR_BWD",
+    "ACTIVATIONS",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
@@ -32,6 +33,9 @@ OP_GEMM_FWD_MXFP8 = 6
 OP_LAYER_BWD_MXFP8 = 7
 OP_ADD_RMSNORM_BWD = 8
 OP_BALANCE_LOSS = 9
+OP_LINEAR_FWD, OP_LINEAR_BWD = 10, 11
+# activations of linear_fwd (moe_act in include/moe.h)
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 EXPORTED_SYMBOLS = (
     "moe_plan_rows_cap", "moe_workspace_bytes", "moe_last_error", "moe_route_topk", "moe_permute",
@@ -41,6 +45,7 @@ EXPORTED_SYMBOLS = (
     "moe_router_logits", "moe_router_bwd", "moe_set_kernel_events", "moe_quantize_mxfp8",
     "moe_grouped_gemm_fwd_mxfp8", "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8",
     "moe_add_rmsnorm", "moe_add_rmsnorm_bwd", "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
+    "moe_linear_fwd", "moe_linear_bwd",
 )
 
 # kernel ids of the measurement hook (moe_kernel_id in include/moe.h)
@@ -48,7 +53,7 @@ KERNEL_IDS = {"gateup": 0, "down": 1, "dh": 2, "dx": 3, "dwd": 4, "dw1": 5, "com
               "route": 8, "permute": 9, "route_tr_plan": 10, "dswiglu": 11, "router_logits": 12,
               "router_dz": 13, "router_dx": 14, "router_dw": 15, "gateup_fp8": 16, "down_fp8": 17, "quant": 18,
               "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21, "balance": 22,
-              "balance_bwd": 23}
+              "balance_bwd": 23, "linear": 24, "linear_bwd": 25}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -122,13 +127,16 @@ def load_library(path: str):
     L.moe_balance_loss.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp, vp, vp, sz, vp]
     L.moe_balance_loss_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
     L.moe_router_bwd_acc.argtypes = [ctypes.c_int, vp, vp, vp, pp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_linear_fwd.argtypes = [vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.moe_linear_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
                "moe_unpermute_combine", "moe_layer_bwd", "moe_router_logits", "moe_router_bwd",
                "moe_set_kernel_events", "moe_quantize_mxfp8", "moe_grouped_gemm_fwd_mxfp8",
                "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
-               "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc"):
+               "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
+               "moe_linear_fwd", "moe_linear_bwd"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -681,3 +689,74 @@ def balance_loss_bwd(logits, saved, bias=None, mask=None, seq_ptr=None, dloss=No
     _check(lib().moe_balance_loss_bwd(_addr(logits), _addr(bias), _addr(mask), _addr(seq_ptr), B, N, E, _addr(saved),
                                       _addr(dloss), _addr(dlogits_in), _addr(dlogits), _cur(dev)))
     return dlogits
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)} (got {act!r})")
+    return ACTIVATIONS[act]
+
+
+@_on_stream
+def linear_fwd(x, w, bias=None, act="none", residual=None, want_z=False, out=None, z=None, ws=None):
+    """out = act(x w^T + bias) + residual, bf16: x [N,K], w [O,K], bias fp32 [O], residual [N,O];
+    act: a key of ACTIVATIONS.  -> (out [N,O], z [N,O] (the product with its bias, for linear_bwd)
+    or None).  out may be residual (in place).  stream: a torch stream to run on."""
+    import torch
+    bf = torch.bfloat16
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [N, K] and w [O, K]")
+    N, K = x.shape
+    O = w.shape[0]
+    dev = x.get_device()
+    _want("x", x, (N, K), bf, dev)
+    _want("w", w, (O, K), bf, dev)
+    if bias is not None:
+        _want("bias", bias, (O,), torch.float32, dev)
+    if residual is not None:
+        _want("residual", residual, (N, O), bf, dev)
+    code = _act(act)
+    _on_gpu(x)
+    out = _out("out", out, (N, O), bf, x, dev)
+    if want_z or z is not None:
+        z = _out("z", z, (N, O), bf, x, dev)
+    nb = _op_bytes(OP_LINEAR_FWD, MOE_BF16, N, 1, 1, K, O, 0)
+    ws = _op_ws(nb, x, ws, dev)
+    _check(lib().moe_linear_fwd(_addr(x), _addr(w), _addr(bias), code, _addr(residual), N, K, O, _addr(out), _addr(z),
+                                _addr(ws), nb, _cur(dev)))
+    return out, z
+
+
+@_on_stream
+def linear_bwd(dout, x, w, z=None, act="none", want_dx=True, want_dw=True, want_dbias=True, dx=None, dw=None,
+               dbias=None, ws=None):
+    """Backward of linear_fwd from dout [N,O] and the z it stored (None for act "none") -> dict(dx
+    [N,K], dw [O,K], dbias fp32 [O]); what is not wanted is None.  residual's gradient is dout."""
+    import torch
+    bf = torch.bfloat16
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [N, K] and w [O, K]")
+    N, K = x.shape
+    O = w.shape[0]
+    dev = dout.get_device()
+    _want("dout", dout, (N, O), bf, dev)
+    _want("x", x, (N, K), bf, dev)
+    _want("w", w, (O, K), bf, dev)
+    code = _act(act)
+    if z is not None:
+        _want("z", z, (N, O), bf, dev)
+    elif code:
+        raise ValueError(f"the backward of {act} needs z")
+    _on_gpu(dout)
+    if want_dx or dx is not None:
+        dx = _out("dx", dx, (N, K), bf, dout, dev)
+    if want_dw or dw is not None:
+        dw = _out("dw", dw, (O, K), bf, dout, dev)
+    if want_dbias or dbias is not None:
+        dbias = _out("dbias", dbias, (O,), torch.float32, dout, dev)
+    nb = _op_bytes(OP_LINEAR_BWD, MOE_BF16, N, 1, 1, K, O, 0)
+    ws = _op_ws(nb, dout, ws, dev)
+    if N or dw is not None or dbias is not None:
+        _check(lib().moe_linear_bwd(_addr(dout), _addr(x), _addr(w), _addr(z), code, N, K, O, _addr(dx), _addr(dw),
+                                    _addr(dbias), _addr(ws), nb, _cur(dev)))
+    return dict(dx=dx, dw=dw, dbias=dbias)

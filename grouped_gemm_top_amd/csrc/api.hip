@@ -108,6 +108,16 @@ moe_status check_desc_sizes(moe_dtype dt, int64_t N, int64_t H, int64_t I, int64
   return MOE_OK;
 }
 
+// sizes of the dense products (their kernels address each tensor with 32-bit byte offsets)
+moe_status check_linear(int32_t N, int32_t K, int32_t O) {
+  REQUIRE(N >= 0, MOE_EINVAL, "N must be >= 0 (got %d)", N);
+  REQUIRE(K >= 8 && O >= 8, MOE_EINVAL, "K and O must be >= 8 (got K=%d, O=%d)", K, O);
+  REQUIRE(K % 8 == 0 && O % 8 == 0, MOE_EUNSUPPORTED, "K and O must be multiples of 8 (got K=%d, O=%d)", K, O);
+  REQUIRE((int64_t)N * K * 2 <= kDescBytes && (int64_t)N * O * 2 <= kDescBytes && (int64_t)O * K * 2 <= kDescBytes,
+          MOE_EUNSUPPORTED, "x [N=%d, K=%d], w [O=%d, K] and out [N, O] must each be < 2 GiB", N, K, O);
+  return MOE_OK;
+}
+
 }  // namespace
 
 namespace moe {
@@ -191,6 +201,12 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_BALANCE_LOSS:  // I: the sequences
       if (I < 1 || I > kMaxSeqs) return 0;
       return moe::balance_loss_ws_bytes(N, E, I);
+    case MOE_OP_LINEAR_FWD:
+      if (check_linear(N, H, I) != MOE_OK) return 0;
+      return moe::linear_fwd_ws_bytes(N, H, I);
+    case MOE_OP_LINEAR_BWD:
+      if (check_linear(N, H, I) != MOE_OK) return 0;
+      return moe::linear_bwd_ws_bytes(N, H, I);
     case MOE_OP_ADD_RMSNORM_BWD:
       if (check_norm(dt, dt, N, H) != MOE_OK) return 0;
       return moe::add_rmsnorm_bwd_ws_bytes(N, H);
@@ -590,6 +606,55 @@ moe_status moe_balance_loss_bwd(const float* logits, const float* bias, const ui
                                               (hipStream_t)stream);
   moe::kernel_event(MOE_K_BALANCE_BWD, 1, (hipStream_t)stream);
   return hip_status(e, "moe_balance_loss_bwd");
+}
+
+moe_status moe_linear_fwd(const void* x, const void* w, const float* bias, int32_t act, const void* res, int32_t N,
+                          int32_t K, int32_t O, void* out, void* z, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_linear(N, K, O)) != MOE_OK) return st;
+  REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, MOE_EINVAL, "unknown activation %d", act);
+  REQUIRE(w, MOE_EINVAL, "NULL w");
+  REQUIRE(N == 0 || (x && out), MOE_EINVAL, "NULL x/out");
+  REQUIRE(N == 0 || (out != x && out != w && (!z || (z != out && z != x && z != w && z != res))), MOE_EINVAL,
+          "out may be res; it and z must be no other argument");
+  REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(res) && aligned16(out) && aligned16(z) &&
+              aligned16(ws),
+          MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned");
+  const size_t need = moe::linear_fwd_ws_bytes(N, K, O);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  moe::kernel_event(MOE_K_LINEAR, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_linear_fwd(x, w, bias, act, res, N, K, O, out, z, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_LINEAR, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_linear_fwd");
+}
+
+moe_status moe_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int32_t act, int32_t N,
+                          int32_t K, int32_t O, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                          void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_linear(N, K, O)) != MOE_OK) return st;
+  REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, MOE_EINVAL, "unknown activation %d", act);
+  REQUIRE(dx || dw || dbias, MOE_EINVAL, "no gradient requested");
+  REQUIRE(N == 0 || dout, MOE_EINVAL, "NULL dout");
+  REQUIRE(N == 0 || act == MOE_ACT_NONE || z, MOE_EINVAL, "an activation's backward needs z");
+  REQUIRE(N == 0 || !dx || w, MOE_EINVAL, "dx needs w");
+  REQUIRE(N == 0 || !dw || x, MOE_EINVAL, "dw needs x");
+  REQUIRE(N == 0 || ((!dx || (dx != dout && dx != x && dx != w && dx != z && dx != dw)) &&
+                     (!dw || (dw != dout && dw != x && dw != w && dw != z))),
+          MOE_EINVAL, "dx and dw must be no other argument");
+  REQUIRE(aligned16(dout) && aligned16(x) && aligned16(w) && aligned16(z) && aligned16(dx) && aligned16(dw) &&
+              aligned16(dbias) && aligned16(ws),
+          MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned");
+  const size_t need = moe::linear_bwd_ws_bytes(N, K, O);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  moe::kernel_event(MOE_K_LINEAR_BWD, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_linear_bwd(dout, x, w, z, act, N, K, O, dx, dw, dbias, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_LINEAR_BWD, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_linear_bwd");
 }
 
 }  // extern "C"

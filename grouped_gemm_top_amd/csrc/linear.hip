@@ -1,0 +1,542 @@
+// linear.hip -- the dense bf16 product with bias, activation and residual in its epilogue, and its
+// backward, for gfx950.
+//
+//   z = x W^T + b,   out = act(z) + res,  z kept in bf16 where asked     x [N,K], W [O,K], out [N,O]
+//   dz = dout act'(z),   dx = dz W,   dW = dz^T x,   db = sum_t dz
+//
+// The three products are one kernel, C[m][n] = sum_k A(m,k) B(n,k), in three layouts: forward with
+// both operands K-contiguous, dx with B K-strided (W read along its rows), dW with both K-strided.
+// Accumulation, bias, activation and residual are fp32; each output is rounded once.  dz is rounded
+// to bf16 before its two products (the matrix cores take bf16), db sums it unrounded.
+#include "gemm_lds.h"
+
+namespace moe {
+namespace ln {
+
+using namespace gk;
+using gg::OOB;
+
+constexpr int BK = 64;  // k per LDS stage: a K-contiguous row of a stage is one 128-byte line
+
+enum Act { NONE = MOE_ACT_NONE, RELU = MOE_ACT_RELU, SILU = MOE_ACT_SILU, GELU = MOE_ACT_GELU,
+           GELU_TANH = MOE_ACT_GELU_TANH };
+
+// 1 / (1 + e^-v): hardware exponential and reciprocal, about one unit in the last place each, far
+// below the bf16 rounding of what they feed
+__device__ __forceinline__ float sig(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * v));
+}
+constexpr float kG = 0.7978845608028654f, kG3 = 0.044715f;  // gelu_tanh: tanh(kG (v + kG3 v^3))
+__device__ __forceinline__ float act_fwd(float v, int act) {
+  switch (act) {
+    case RELU: return v > 0.f ? v : (v != v ? v : 0.f);
+    case SILU: return v * sig(v);
+    case GELU: return 0.5f * v * (1.0f + erff(0.70710678118654752f * v));
+    case GELU_TANH: return v * sig(2.0f * kG * v * (1.0f + kG3 * v * v));  // (1 + tanh u) / 2 = sig(2u)
+    default: return v;
+  }
+}
+__device__ __forceinline__ float act_bwd(float v, int act) {
+  switch (act) {
+    case RELU: return v > 0.f ? 1.f : (v != v ? v : 0.f);
+    case SILU: {
+      const float s = sig(v);
+      return s * (1.0f + v * (1.0f - s));
+    }
+    case GELU:
+      return 0.5f * (1.0f + erff(0.70710678118654752f * v)) +
+             v * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.72134752044448170368f * v * v);
+    case GELU_TANH: {
+      const float s = sig(2.0f * kG * v * (1.0f + kG3 * v * v));
+      return s + v * s * (1.0f - s) * 2.0f * kG * (1.0f + 3.0f * kG3 * v * v);
+    }
+    default: return 1.f;
+  }
+}
+
+struct Args {
+  const void* A;  // K-contiguous [M, K] or K-strided [K, M]
+  const void* B;  // K-contiguous [N, K] or K-strided [K, N]
+  int M, N, K;
+  int nM, nN, S, per;  // tiles along M and N, K slices, workgroups per XCD
+  float* part;         // S > 1: [S, M, N]
+  void* out;           // [M, N]
+  void* z;             // forward: [M, N] or NULL
+  const float* bias;   // forward: [N] or NULL
+  const void* res;     // forward: [M, N] or NULL
+  int act;
+};
+
+// 16 rows x 64 columns of fp32 staged as rows of 256 bytes, 16-byte chunk q of row r at q ^ r
+__device__ __forceinline__ void stage_write(char* st, const f32x4* blk, int L) {
+  const int c = L & 15, g = L >> 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(st + c * 256 + (((4 * j + g) ^ c) << 4)) = blk[j];
+}
+__device__ __forceinline__ f32x4 stage_read(const char* st, int p, int L) {
+  const int r = 4 * p + (L >> 4), q = L & 15;
+  return *reinterpret_cast<const f32x4*>(st + r * 256 + ((q ^ r) << 4));
+}
+
+// the epilogue of four neighbouring columns n .. n + 3 of row m: acc -> outputs (N is a multiple of 8)
+__device__ __forceinline__ void finish4(const Args& a, int m, int n, f32x4 v, const float4& b) {
+  const size_t o = (size_t)m * a.N + n;
+  v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
+  if (a.z) *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.z) + o) = u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
+  if (a.act != NONE) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = act_fwd(v[j], a.act);
+  }
+  if (a.res) {
+    float r0, r1, r2, r3;
+    load4(static_cast<const bf16_t*>(a.res) + o, r0, r1, r2, r3);
+    v[0] += r0; v[1] += r1; v[2] += r2; v[3] += r3;
+  }
+  *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.out) + o) = u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
+}
+
+// One operand's loads: R rows (K-contiguous) or R columns (K-strided) of a 64-wide k-step, as R / 8
+// kilobytes; instruction q of wavefront w fills kilobyte w + NW q, lane L its bytes 16 L .. 16 L + 15.
+//  K-contiguous: kilobyte b holds rows 8b .. 8b + 7 of 128 bytes, k-chunk c of row r at c ^ ((r >> 1) & 7)
+//  K-strided: k-rows of 2R bytes, column chunk c of k-row k at c ^ mn_f(k)
+template <int R, int NW, bool KC>
+struct Op {
+  static constexpr int NI = R / 8 / NW;
+  static_assert(R % (8 * NW) == 0 && NW % 2 == 0 && (KC || R >= 128), "whole kilobytes per wavefront");
+  i32x4 r;
+  uint32_t v[NI];  // this lane's byte offset at k = 0 (OOB when masked)
+  int kl[NI];      // k of this lane inside a step
+
+  // rows or columns x0 .. x0 + R - 1 of X; ld: row length in elements
+  __device__ __forceinline__ void setup(const void* p, int X, int K, int x0, int w, int L) {
+    r = sgpr4(dmadesc(p, (long long)X * K * 2));
+#pragma unroll
+    for (int q = 0; q < NI; ++q) {
+      const int b = w + NW * q;
+      if constexpr (KC) {
+        const int row = x0 + 8 * b + (L >> 3);
+        const int c = (L & 7) ^ ((4 * (w & 1) + (L >> 4)) & 7);
+        kl[q] = 8 * c;
+        v[q] = row < X ? ((uint32_t)row * (uint32_t)K + 8u * c) * 2u : OOB;
+      } else {
+        constexpr int CPR = R / 8;  // chunks per k-row
+        const int k = b * (64 / CPR) + L / CPR;
+        const int col = x0 + 8 * ((L % CPR) ^ mn_f(k));
+        kl[q] = k;
+        v[q] = col < X ? ((uint32_t)k * (uint32_t)X + (uint32_t)col) * 2u : OOB;
+      }
+    }
+  }
+  // the step at k0 into the stage area at LDS address m
+  __device__ __forceinline__ void issue(uint32_t m, int X, int K, int k0, int w) const {
+    const uint32_t step = KC ? (uint32_t)k0 * 2u : (uint32_t)k0 * (uint32_t)X * 2u;
+    if (k0 + BK <= K) {
+      const uint32_t so = (uint32_t)ufl((int)step);
+#pragma unroll
+      for (int q = 0; q < NI; ++q) dma16(r, m + (uint32_t)(w + NW * q) * 1024u, v[q], so);
+    } else {  // K tail: k >= K masked (K is a multiple of 8 where a chunk runs along k)
+#pragma unroll
+      for (int q = 0; q < NI; ++q)
+        dma16(r, m + (uint32_t)(w + NW * q) * 1024u, v[q] != OOB && k0 + kl[q] < K ? v[q] + step : OOB, 0u);
+    }
+  }
+};
+
+// fragment of 16 rows (or columns) from x0 on, k-half sub of a stage (layouts: Op)
+template <int R, bool KC>
+struct Frag {
+  int o0, ff, bb;
+  __device__ __forceinline__ void init(int L) {
+    if constexpr (KC) {
+      o0 = (L & 15) * 128 + ((((L >> 4) ^ ((L >> 1) & 7)) & 7) << 4);
+    } else {
+      const int m = L & 15, g = L >> 4;
+      o0 = (8 * g + (m >> 2)) * (2 * R) + 8 * (m & 1);
+      ff = 2 * ((m >> 2) | ((g & 1) << 2));
+      bb = (m >> 1) & 1;
+    }
+  }
+  __device__ __forceinline__ bf16x8 get(const char* op, int x0, int sub) const {
+    if constexpr (KC) {
+      return *reinterpret_cast<const bf16x8*>(op + x0 * 128 + (o0 ^ (64 * sub)));
+    } else {
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const char* p = op + o0 + sub * (32 * 2 * R) + ((((x0 >> 3) ^ ff) | bb) << 4);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 2 * R));
+      struct P { s16x4 a, b; } pr{lo, hi};
+      return __builtin_bit_cast(bf16x8, pr);
+    }
+  }
+};
+
+enum Epi { FWD = 0, PLAIN = 1, PART = 2 };
+
+// A BM x BN tile by WM x WN wavefronts, each (BM / WM) x (BN / WN) in 16 x 16 blocks.
+template <int BM, int BN, int WM, int WN, bool AKC, bool BKC, int EPI>
+__global__ __launch_bounds__(64 * WM * WN) void k_linear(Args a) {
+  constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;
+  constexpr int OPA = BM * 128, STG = OPA + BN * 128;
+  static_assert(NB % 4 == 0, "the epilogue stages 64 columns at a time");
+  static_assert(2 * STG >= NW * 4096, "the epilogue's staging");
+  __shared__ __attribute__((aligned(1024))) char s_ring[2 * STG];
+  const int L = threadIdx.x & 63, w = ufl(threadIdx.x >> 6);
+  const int wm = w % WM, wn = w / WM;
+  // XCD x gets the tiles x per .. (x + 1) per - 1 (workgroups go to XCDs round robin), in groups of
+  // eight M-tiles so that what one L2 serves at a time is a compact block of C
+  const int t = (blockIdx.x & 7) * a.per + (blockIdx.x >> 3);
+  const int nT = a.nM * a.nN;
+  if ((int)(blockIdx.x >> 3) >= a.per || t >= nT * a.S) return;
+  const int s = t / nT, tt = t - s * nT;
+  const int gsz = 8 * a.nN, gr = tt / gsz, gm = min(8, a.nM - 8 * gr), in = tt - gr * gsz;
+  const int m0 = (8 * gr + in % gm) * BM, n0 = (in / gm) * BN;
+  const int steps = (a.K + BK - 1) / BK;
+  const int k_lo = (int)((long long)steps * s / a.S), nk = (int)((long long)steps * (s + 1) / a.S) - k_lo;
+
+  Op<BM, NW, AKC> oa;
+  Op<BN, NW, BKC> ob;
+  oa.setup(a.A, a.M, a.K, m0, w, L);
+  ob.setup(a.B, a.N, a.K, n0, w, L);
+  Frag<BM, AKC> fra;
+  Frag<BN, BKC> frb;
+  fra.init(L);
+  frb.init(L);
+  const uint32_t ring = lds_addr(s_ring);
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t m = ring + (uint32_t)(kt & 1) * STG;
+    oa.issue(m, a.M, a.K, (k_lo + kt) * BK, w);
+    ob.issue(m + OPA, a.N, a.K, (k_lo + kt) * BK, w);
+  };
+
+  f32x4 acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (nk > 0) issue(0);
+#pragma unroll 1
+  for (int kt = 0; kt < nk; ++kt) {
+    // step kt has landed for every wavefront, and every wavefront's reads of the other stage are
+    // complete
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + 1 < nk) issue(kt + 1);
+    const char* sa = s_ring + (kt & 1) * STG;
+    const char* sb = sa + OPA;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      bf16x8 fb[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) fb[j] = frb.get(sb, wn * (BN / WN) + 16 * j, sub);
+      bf16x8 fa = fra.get(sa, wm * (BM / WM), sub);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        bf16x8 fn;
+        if (i + 1 < MB) fn = fra.get(sa, wm * (BM / WM) + 16 * (i + 1), sub);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[j], fa, acc[i][j]);
+        if (i + 1 < MB) fa = fn;
+      }
+    }
+  }
+  lds_barrier();  // the ring is free: it stages the epilogue
+
+  // acc[i][j][v] = C[wm.. + 16 i + (L & 15)][wn.. + 16 j + 4 (L >> 4) + v]; through LDS a lane gets
+  // columns 4 (L & 15) .. + 3 of row 4 p + (L >> 4), so 16 lanes cover a row's 64 columns
+  char* st = s_ring + w * 4096;
+#pragma unroll
+  for (int h = 0; h < NB / 4; ++h) {
+    const int n = n0 + wn * (BN / WN) + 64 * h + 4 * (L & 15);
+    float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (EPI == FWD && a.bias && n < a.N) bv = *reinterpret_cast<const float4*>(a.bias + n);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      stage_write(st, &acc[i][4 * h], L);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const f32x4 v = stage_read(st, p, L);
+        const int m = m0 + wm * (BM / WM) + 16 * i + 4 * p + (L >> 4);
+        if (m < a.M && n < a.N) {
+          if constexpr (EPI == FWD)
+            finish4(a, m, n, v, bv);
+          else if constexpr (EPI == PLAIN)
+            *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.out) + (size_t)m * a.N + n) =
+                u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
+          else
+            *reinterpret_cast<f32x4*>(a.part + ((size_t)s * a.M + m) * a.N + n) = v;
+        }
+      }
+    }
+  }
+}
+
+// Split K: the slices' partial sums added in slice order, then the epilogue.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_linear_sum(Args a) {
+  const size_t nv = (size_t)a.M * a.N / 4;
+  const int cpr = a.N / 4;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nv; i += (size_t)gridDim.x * 256) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(a.part + 4 * i);
+    for (int s = 1; s < a.S; ++s) v += *reinterpret_cast<const f32x4*>(a.part + (size_t)s * a.M * a.N + 4 * i);
+    const int m = (int)(i / cpr), n = (int)(i - (size_t)m * cpr) * 4;
+    if constexpr (EPI == FWD) {
+      float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.bias) bv = *reinterpret_cast<const float4*>(a.bias + n);
+      finish4(a, m, n, v, bv);
+    } else {
+      *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.out) + 4 * i) = u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
+    }
+  }
+}
+
+// Few tokens (M <= 16 NT): the product is one pass over W, so it streams W straight into registers.
+// A workgroup owns 16 outputs; its KW wavefronts take 64-wide k-steps in turn (each lane 2 x 16 bytes
+// of a W row: a row's 128-byte line), with the 16-token blocks of x as the other operand, and their
+// sums meet in LDS in wavefront order.
+template <int NT, int KW>
+__global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
+  __shared__ f32x4 s_sum[KW][NT][64];
+  const int L = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int o0 = blockIdx.x * 16, K = a.K;
+  const int r = L & 15, g = L >> 4;
+  const bf16_t* wp = static_cast<const bf16_t*>(a.B) + (size_t)min(o0 + r, a.N - 1) * K;
+  const bf16_t* xp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) xp[i] = static_cast<const bf16_t*>(a.A) + (size_t)min(16 * i + r, a.M - 1) * K;
+  f32x4 acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int U = NT == 1 ? 4 : 2;  // k-steps in flight
+  const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
+  for (int k0 = w * 64; k0 < K; k0 += U * KW * 64) {
+    bf16x8 fw[U][2], fx[U][NT][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = k0 + u * KW * 64 + 32 * h + 8 * g;
+        const bool in = k < K;  // K is a multiple of 8
+        fw[u][h] = in ? *reinterpret_cast<const bf16x8*>(wp + k) : zero;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) fx[u][i][h] = in ? *reinterpret_cast<const bf16x8*>(xp[i] + k) : zero;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = mma(fw[u][h], fx[u][i][h], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) s_sum[w][i][L] = acc[i];
+  __syncthreads();
+  // acc[v] = C[token 16 i + (L & 15)][output o0 + 4 (L >> 4) + v]
+  for (int i = w; i < NT; i += KW) {
+    f32x4 v = s_sum[0][i][L];
+#pragma unroll
+    for (int q = 1; q < KW; ++q) v += s_sum[q][i][L];
+    const int m = 16 * i + r, n = o0 + 4 * g;
+    if (m < a.M && n < a.N) {
+      float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.bias) bv = *reinterpret_cast<const float4*>(a.bias + n);
+      finish4(a, m, n, v, bv);
+    }
+  }
+}
+
+// dz = dout act'(z) in bf16 (dz NULL: not written; z NULL: dz is dout) and the column sums of the
+// unrounded dz over this workgroup's rows (part NULL: not wanted).  A workgroup owns 512 columns
+// (64 threads of 8) and the rows g, g + 4 gridDim.y, ... (four at a time).
+__global__ __launch_bounds__(256) void k_linear_dz(const bf16_t* __restrict__ dout, const bf16_t* __restrict__ z, int N,
+                                                   int O, int act, bf16_t* __restrict__ dz, float* __restrict__ part) {
+  __shared__ float s[3][64][8];
+  const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int col = blockIdx.x * 512 + 8 * c;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (col < O) {
+#pragma unroll 2
+    for (int t = blockIdx.y * 4 + g; t < N; t += 4 * gridDim.y) {
+      const size_t o = (size_t)t * O + col;
+      float d[8], v[8];
+      const uint4 ud = *reinterpret_cast<const uint4*>(dout + o);
+      uint4 uz = make_uint4(0u, 0u, 0u, 0u);
+      if (z) uz = *reinterpret_cast<const uint4*>(z + o);
+      const uint32_t wd[4] = {ud.x, ud.y, ud.z, ud.w}, wz[4] = {uz.x, uz.y, uz.z, uz.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[2 * j] = __uint_as_float(wd[j] << 16);
+        d[2 * j + 1] = __uint_as_float(wd[j] & 0xFFFF0000u);
+        v[2 * j] = __uint_as_float(wz[j] << 16);
+        v[2 * j + 1] = __uint_as_float(wz[j] & 0xFFFF0000u);
+      }
+      if (z) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] *= act_bwd(v[j], act);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += d[j];
+      if (dz)
+        *reinterpret_cast<uint4*>(dz + o) = make_uint4(pk2(d[0], d[1]), pk2(d[2], d[3]), pk2(d[4], d[5]), pk2(d[6], d[7]));
+    }
+  }
+  if (!part) return;
+  if (g > 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[g - 1][c][j] = sum[j];
+  }
+  __syncthreads();
+  if (g == 0 && col < O) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = (sum[j] + s[0][c][j]) + (s[1][c][j] + s[2][c][j]);
+    float* p = part + (size_t)blockIdx.y * O + col;
+    *reinterpret_cast<float4*>(p) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+enum Kind { K_FWD, K_DX, K_DW };
+struct Shape { int big, S; };  // big: 2 = 256 x 256, 1 = 128 x 128, 0 = 64 x 64 (64 x 128 for dx)
+
+// Tile and K slices of a product: the choice with the least estimated time.
+Shape choose(Kind kind, int M, int N, int K) {
+  const int steps = (K + BK - 1) / BK;
+  // time of one k-step of a workgroup (us) and its fixed part (start, epilogue); workgroups per CU
+  struct C { int bm, bn, occ; double step, fix; };
+  const C cs[3] = {{64, kind == K_FWD ? 64 : 128, 4, 0.75, 4.0}, {128, 128, 2, 1.0, 5.0}, {256, 256, 1, 1.5, 10.0}};
+  Shape best{0, 1};
+  double tb = 1e30;
+  for (int b = 0; b < 3; ++b) {
+    if (kind == K_DW && b == 0) continue;
+    const long long tiles = (long long)((M + cs[b].bm - 1) / cs[b].bm) * ((N + cs[b].bn - 1) / cs[b].bn);
+    for (int S = 1; S <= 16 && S <= steps; S *= 2) {
+      if (S > 1 && (S * tiles > 1024 || (double)S * M * N * 4 > 64e6)) break;
+      const long long rounds = (tiles * S + 256 * cs[b].occ - 1) / (256 * cs[b].occ);
+      double t = rounds * (((steps + S - 1) / S) * cs[b].step + cs[b].fix);
+      if (S > 1) t += 3.0 + (double)S * M * N * 4 / 3e6;
+      if (t < tb) tb = t, best = Shape{b, S};
+    }
+  }
+  return best;
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+size_t part_bytes(Kind kind, int M, int N, int K) {
+  const Shape c = choose(kind, M, N, K);
+  return c.S > 1 ? up((size_t)c.S * M * N * 4) : 0;
+}
+
+template <int BM, int BN, int WM, int WN, bool AKC, bool BKC>
+void launch(Args& a, int S, hipStream_t s) {
+  a.nM = (a.M + BM - 1) / BM;
+  a.nN = (a.N + BN - 1) / BN;
+  a.S = S;
+  const long long T = (long long)a.nM * a.nN * S;
+  a.per = (int)((T + 7) / 8);
+  const dim3 g((unsigned)(8 * a.per)), b(64 * WM * WN);
+  if (S > 1)
+    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, AKC, BKC, PART>), g, b, 0, s, a);
+  else  // (both operands K-contiguous: the forward)
+    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, AKC, BKC, AKC && BKC ? FWD : PLAIN>), g, b, 0, s, a);
+}
+
+hipError_t product(Kind kind, Args a, void* ws, hipStream_t s) {
+  const Shape c = choose(kind, a.M, a.N, a.K);
+  a.part = static_cast<float*>(ws);
+  if (kind == K_FWD) {
+    if (c.big == 2) launch<256, 256, 2, 4, true, true>(a, c.S, s);
+    else if (c.big == 1) launch<128, 128, 2, 2, true, true>(a, c.S, s);
+    else launch<64, 64, 4, 1, true, true>(a, c.S, s);
+  } else if (kind == K_DX) {
+    if (c.big == 2) launch<256, 256, 2, 4, true, false>(a, c.S, s);
+    else if (c.big == 1) launch<128, 128, 2, 2, true, false>(a, c.S, s);
+    else launch<64, 128, 2, 2, true, false>(a, c.S, s);
+  } else {
+    if (c.big == 2) launch<256, 256, 2, 4, false, false>(a, c.S, s);
+    else launch<128, 128, 2, 2, false, false>(a, c.S, s);
+  }
+  if (c.S > 1) {
+    const size_t nv = (size_t)a.M * a.N / 4;
+    const unsigned g = (unsigned)((nv + 255) / 256 < 2048 ? (nv + 255) / 256 : 2048);
+    if (kind == K_FWD) hipLaunchKernelGGL(k_linear_sum<FWD>, dim3(g), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(k_linear_sum<PLAIN>, dim3(g), dim3(256), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+constexpr int FEW = 64;  // tokens up to which W is streamed into registers
+
+int dz_groups(int N) { return N <= 4 ? 1 : (N >= 512 ? 128 : (N + 3) / 4); }
+
+__global__ __launch_bounds__(256) void k_zero16(uint4* __restrict__ p, size_t n) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
+    p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+}  // namespace ln
+
+size_t linear_fwd_ws_bytes(int N, int K, int O) {
+  return 256 + (N <= ln::FEW ? 0 : ln::part_bytes(ln::K_FWD, N, O, K));
+}
+
+hipError_t launch_linear_fwd(const void* x, const void* w, const float* bias, int act, const void* res, int N, int K,
+                             int O, void* out, void* z, void* ws, hipStream_t s) {
+  using namespace ln;
+  if (N == 0) return hipSuccess;
+  Args a{};
+  a.A = x; a.B = w; a.M = N; a.N = O; a.K = K;
+  a.out = out; a.z = z; a.bias = bias; a.res = res; a.act = act;
+  if (N <= FEW) {
+    const dim3 g((unsigned)((O + 15) / 16));
+    if (N <= 16) hipLaunchKernelGGL((k_linear_few<1, 8>), g, dim3(512), 0, s, a);
+    else if (N <= 32) hipLaunchKernelGGL((k_linear_few<2, 8>), g, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_few<4, 8>), g, dim3(512), 0, s, a);
+    return hipGetLastError();
+  }
+  return product(K_FWD, a, ws, s);
+}
+
+size_t linear_bwd_ws_bytes(int N, int K, int O) {
+  using namespace ln;
+  const size_t dx = part_bytes(K_DX, N, K, O), dw = part_bytes(K_DW, O, K, N);
+  return 256 + up((size_t)N * O * 2) + up((size_t)dz_groups(N) * O * 4) + (dx > dw ? dx : dw);
+}
+
+hipError_t launch_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int act, int N, int K,
+                             int O, void* dx, void* dw, float* db, void* ws, hipStream_t s) {
+  using namespace ln;
+  if (N == 0) {  // the parameters' gradients are zero (a fill kernel, so that the call can be captured)
+    if (dw) hipLaunchKernelGGL(k_zero16, dim3(1024), dim3(256), 0, s, (uint4*)dw, (size_t)O * K / 8);
+    if (db) hipLaunchKernelGGL(k_zero16, dim3(16), dim3(256), 0, s, (uint4*)db, (size_t)O / 4);
+    return hipGetLastError();
+  }
+  char* p = static_cast<char*>(ws);
+  bf16_t* dz = reinterpret_cast<bf16_t*>(p);
+  p += up((size_t)N * O * 2);
+  float* dbp = reinterpret_cast<float*>(p);
+  p += up((size_t)dz_groups(N) * O * 4);
+  const bool make = act != NONE && (dx || dw);
+  if (make || db) {
+    const int G = dz_groups(N);
+    float* part = db ? (G == 1 ? db : dbp) : nullptr;
+    hipLaunchKernelGGL(k_linear_dz, dim3((O + 511) / 512, G), dim3(256), 0, s, (const bf16_t*)dout,
+                       act != NONE ? (const bf16_t*)z : nullptr, N, O, act, make ? dz : nullptr, part);
+    if (db && G > 1) launch_sum_rows(dbp, G, O, db, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  Args a{};
+  const void* d = make ? dz : dout;
+  if (dx) {
+    a.A = d; a.B = w; a.M = N; a.N = K; a.K = O; a.out = dx;
+    hipError_t e = product(K_DX, a, p, s);
+    if (e != hipSuccess) return e;
+  }
+  if (dw) {
+    a.A = d; a.B = x; a.M = O; a.N = K; a.K = N; a.out = dw;
+    return product(K_DW, a, p, s);
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

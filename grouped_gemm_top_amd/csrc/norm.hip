@@ -282,9 +282,9 @@ __global__ __launch_bounds__(64 * WR * RG) void k_add_rmsnorm_bwd(BwdArgs a) {
   }
 }
 
-// dw [H] from G partial rows [G, H]: a workgroup owns 32 columns; thread (g, c) sums the rows g,
+// The column sums of G partial rows [G, H] (H a multiple of 4): a workgroup owns 32 columns; thread (g, c) sums the rows g,
 // g + 128, ... of four columns, then the 128 sums are added in a fixed order.
-__global__ __launch_bounds__(1024) void k_dw_reduce(const float* __restrict__ part, int G, int H,
+__global__ __launch_bounds__(1024) void k_sum_rows(const float* __restrict__ part, int G, int H,
                                                     float* __restrict__ dw) {
   __shared__ float4 s[128][8];
   const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
@@ -360,6 +360,10 @@ int bwd_groups(long long N) { return (int)(N < 512 ? (N < 1 ? 1 : N) : 512); }
 
 }  // namespace nm
 
+void launch_sum_rows(const float* part, int G, int H, float* out, hipStream_t s) {
+  hipLaunchKernelGGL(nm::k_sum_rows, dim3((unsigned)((H + 31) / 32)), dim3(1024), 0, s, part, G, H, out);
+}
+
 size_t add_rmsnorm_bwd_ws_bytes(int N, int H) { return (size_t)nm::bwd_groups(N) * H * 4; }
 
 hipError_t launch_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const void* res, const float* w, float eps,
@@ -386,8 +390,7 @@ hipError_t launch_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, c
   if (dt == MOE_F32) nm::bwd<float, float>(a, G, s);
   else if (rdt == MOE_F32) nm::bwd<bf16_t, float>(a, G, s);
   else nm::bwd<bf16_t, bf16_t>(a, G, s);
-  if (dw && G > 1)
-    hipLaunchKernelGGL(nm::k_dw_reduce, dim3((unsigned)((H + 31) / 32)), dim3(1024), 0, s, part, G, H, dw);
+  if (dw && G > 1) launch_sum_rows(part, G, H, dw, s);
   return hipGetLastError();
 }
 

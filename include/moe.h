@@ -81,8 +81,18 @@ typedef enum moe_op {
   MOE_OP_GEMM_FWD_MXFP8 = 6,
   MOE_OP_LAYER_BWD_MXFP8 = 7,
   MOE_OP_ADD_RMSNORM_BWD = 8,
-  MOE_OP_BALANCE_LOSS = 9
+  MOE_OP_BALANCE_LOSS = 9,
+  MOE_OP_LINEAR_FWD = 10,
+  MOE_OP_LINEAR_BWD = 11
 } moe_op;
+
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,      /* v sigmoid(v) */
+  MOE_ACT_GELU = 3,      /* v (1 + erf(v / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 4  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+} moe_act;
 
 /*
  * Routing plan: the ragged, expert-sorted layout with its offset and index metadata
@@ -460,6 +470,31 @@ moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, cons
                                void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Dense product with bias, activation and residual (the projection in front of the layer, a dense
+ * MLP beside the experts), for bf16:
+ *   z[t,o]   = sum_k x[t,k] w[o,k] + bias[o]       (fp32 accumulation; bias fp32 [O] or NULL)
+ *   out[t,o] = act(z[t,o]) + res[t,o]              (act: moe_act; res NULL: none)
+ * x [N,K], w [O,K] (an nn.Linear weight), res, out, z [N,O], all bf16; z (the rounded z, what the
+ * backward takes) is written unless NULL.  out may be res (in place), z is neither.  Bias, activation
+ * and residual are applied in fp32 and out is rounded once.  K and O are multiples of 8, tensors
+ * and workspace 16-byte aligned, and x, w, out each smaller than 2 GiB.  N <= 64 reads w once,
+ * straight into registers (a decoding step).
+ * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_FWD, MOE_BF16, N, 1, 1, K, O, 0).
+ *
+ * moe_linear_bwd, given dout = the gradient of out (which is res's gradient as it stands):
+ *   dz = dout act'(z)    (z as the forward stored it; NULL for MOE_ACT_NONE)
+ *   dx = dz w [N,K],  dw = dz^T x [O,K],  dbias[o] = sum_t dz[t,o] (fp32 [O])      (NULL skips each)
+ * dz is rounded to bf16 for its two products; dbias sums it unrounded.  Everything is written
+ * fresh, in a fixed order (bitwise reproducible); N == 0 sets dw and dbias to zero.
+ * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_BWD, MOE_BF16, N, 1, 1, K, O, 0).
+ */
+moe_status moe_linear_fwd(const void* x, const void* w, const float* bias, int32_t act, const void* res, int32_t N,
+                          int32_t K, int32_t O, void* out, void* z, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int32_t act, int32_t N,
+                          int32_t K, int32_t O, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/*
  * Measurement hook (for benchmarks and profilers, not needed for computing): kernels of
  * the library, identified by moe_kernel_id.  After moe_set_kernel_events(id, start, stop)
  * with two hipEvent_t handles (passed as void*), every later launch of that kernel records
@@ -495,7 +530,9 @@ typedef enum moe_kernel_id {
   MOE_K_ADD_RMSNORM_BWD = 21, /* moe_add_rmsnorm_bwd: the row kernel and the sum of dw's partials */
   MOE_K_BALANCE = 22,         /* moe_balance_loss */
   MOE_K_BALANCE_BWD = 23,     /* moe_balance_loss_bwd */
-  MOE_K_COUNT = 24
+  MOE_K_LINEAR = 24,          /* moe_linear_fwd */
+  MOE_K_LINEAR_BWD = 25,      /* moe_linear_bwd: dz, dx, dw, dbias */
+  MOE_K_COUNT = 26
 } moe_kernel_id;
 
 moe_status moe_set_kernel_events(int32_t kernel_id, void* start_event, void* stop_event);

@@ -162,3 +162,76 @@ def test_balance_loss_bindings():
         G.balance_loss_bwd(lg, torch.zeros(9), dloss=torch.ones(2, dtype=torch.float64))
     with pytest.raises(ValueError, match="GPU"):
         G.balance_loss_bwd(lg, torch.zeros(9))
+
+
+def test_linear_errors(L):
+    ptr = lambda k: ctypes.c_void_p(FAKE + 4096 * k)  # noqa: E731
+    N, K, O = 100, 64, 72
+    for op in (G.OP_LINEAR_FWD, G.OP_LINEAR_BWD):
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, N, 1, 1, K, O, 0) > 0
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, 0, 1, 1, K, O, 0) > 0
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, N, 1, 1, 60, O, 0) == 0
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, N, 1, 1, K, 0, 0) == 0
+    need = L.moe_workspace_bytes(G.OP_LINEAR_FWD, G.MOE_BF16, N, 1, 1, K, O, 0)
+
+    def fwd(x=ptr(0), w=ptr(1), b=ptr(2), act=0, res=ptr(3), N=N, K=K, O=O, out=ptr(4), z=ptr(5), ws=ptr(6), nb=need):
+        return L.moe_linear_fwd(x, w, b, act, res, N, K, O, out, z, ws, nb, None)
+    assert fwd(nb=need - 1) == G.MOE_EWORKSPACE
+    assert fwd(ws=None) == G.MOE_EINVAL
+    assert fwd(act=5) == G.MOE_EINVAL
+    assert fwd(act=-1) == G.MOE_EINVAL
+    assert fwd(K=60) == G.MOE_EUNSUPPORTED
+    assert fwd(O=4) == G.MOE_EINVAL
+    assert fwd(O=76) == G.MOE_EUNSUPPORTED
+    assert fwd(N=-1) == G.MOE_EINVAL
+    assert fwd(N=1 << 20, K=1024) == G.MOE_EUNSUPPORTED       # x of 2 GiB
+    assert fwd(N=1 << 20, O=1024) == G.MOE_EUNSUPPORTED       # out of 2 GiB
+    assert fwd(K=1 << 15, O=1 << 15) == G.MOE_EUNSUPPORTED    # w of 2 GiB
+    assert fwd(x=None) == G.MOE_EINVAL
+    assert fwd(w=None) == G.MOE_EINVAL
+    assert fwd(out=None) == G.MOE_EINVAL
+    assert fwd(out=ptr(0)) == G.MOE_EINVAL                    # out over x
+    assert fwd(z=ptr(4)) == G.MOE_EINVAL                      # z over out
+    assert fwd(z=ptr(3)) == G.MOE_EINVAL                      # z over the residual
+    assert fwd(b=ODD) == G.MOE_EUNSUPPORTED
+    assert fwd(x=None, out=None, N=0) == G.MOE_OK
+    need = L.moe_workspace_bytes(G.OP_LINEAR_BWD, G.MOE_BF16, N, 1, 1, K, O, 0)
+
+    def bwd(d=ptr(0), x=ptr(1), w=ptr(2), z=ptr(3), act=2, N=N, K=K, O=O, dx=ptr(4), dw=ptr(5), db=ptr(6), ws=ptr(7),
+            nb=need):
+        return L.moe_linear_bwd(d, x, w, z, act, N, K, O, dx, dw, db, ws, nb, None)
+    assert bwd(nb=need - 1) == G.MOE_EWORKSPACE
+    assert bwd(z=None) == G.MOE_EINVAL
+    assert bwd(dx=None, dw=None, db=None) == G.MOE_EINVAL
+    assert bwd(d=None) == G.MOE_EINVAL
+    assert bwd(w=None) == G.MOE_EINVAL
+    assert bwd(x=None) == G.MOE_EINVAL
+    assert bwd(dx=ptr(0)) == G.MOE_EINVAL                     # dx over dout
+    assert bwd(dw=ptr(4)) == G.MOE_EINVAL                     # dw over dx
+    assert bwd(act=9) == G.MOE_EINVAL
+    assert bwd(db=ODD) == G.MOE_EUNSUPPORTED
+
+
+def test_linear_bindings():
+    b = torch.bfloat16
+    x, w, d = torch.zeros(4, 64, dtype=b), torch.zeros(24, 64, dtype=b), torch.zeros(4, 24, dtype=b)
+    with pytest.raises(ValueError, match="GPU"):
+        G.linear_fwd(x, w, bias=torch.zeros(24), residual=d, act="silu")
+    with pytest.raises(TypeError):
+        G.linear_fwd(x.float(), w)
+    with pytest.raises(TypeError):
+        G.linear_fwd(x, w, bias=torch.zeros(24, dtype=b))
+    with pytest.raises(ValueError, match="shape"):
+        G.linear_fwd(x, w[:, :32])
+    with pytest.raises(ValueError, match="shape"):
+        G.linear_fwd(x, w, residual=x)
+    with pytest.raises(ValueError, match="contiguous"):
+        G.linear_fwd(x, torch.zeros(64, 24, dtype=b).t())
+    with pytest.raises(ValueError, match="act"):
+        G.linear_fwd(x, w, act="tanh")
+    with pytest.raises(ValueError, match="needs z"):
+        G.linear_bwd(d, x, w, act="gelu")
+    with pytest.raises(ValueError, match="shape"):
+        G.linear_bwd(d[:3], x, w)
+    with pytest.raises(ValueError, match="GPU"):
+        G.linear_bwd(d, x, w)

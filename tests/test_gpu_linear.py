@@ -1,0 +1,224 @@
+"""moe_linear_fwd and moe_linear_bwd through the C ABI, every buffer guarded.
+
+Most cases take small whole numbers: every product and sum is then exact in fp32 (K 4 + bias stays
+below 2^24), so the outputs must equal the exact results rounded once to bf16, element for element,
+in every tile shape, slice count and layout.  With random inputs the tolerances follow the
+arithmetic (u = 2^-24, 2^-8 half a step of bf16): a sum of K products in any order is off by at most
+K u sum |x w|; the activations (their slope is at most 1.13) pass that on and add at most 16 u of
+their own value and argument each; dz is one rounding of at most 2^-8 |dz| on each term of dx and
+dw; dbias sums at most 64 + 64 + 128 values in a row."""
+import numpy as np
+import pytest
+import torch
+
+from harness import Guards
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+H = 2.0 ** -8
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import grouped_gemm_top_amd as G
+    G.lib()
+
+
+def _ints(shape, lo, hi, seed):
+    return torch.randint(lo, hi + 1, shape, generator=torch.Generator().manual_seed(seed)).float()
+
+
+def _rand(shape, seed, scale=1.0):
+    return (scale * torch.randn(*shape, generator=torch.Generator().manual_seed(seed))).to(BF)
+
+
+def _up(g, name, t):
+    if t is None:
+        return None
+    v = g.alloc(name, t.shape, t.dtype)
+    v.copy_(t)
+    return v
+
+
+def _mm(a, b):
+    """The exact product of whole-number matrices (fp32 on the CPU is exact at these sizes)."""
+    return a @ b
+
+
+SHAPES = [  # N, K, O
+    (1, 8, 8), (1, 4096, 16), (2, 64, 4104), (16, 520, 72), (17, 64, 24), (33, 136, 40), (64, 2880, 128), (65, 64, 64),
+    (70, 8, 8), (100, 72, 200), (129, 1000, 136), (333, 288, 264), (300, 2880, 512), (257, 520, 264), (513, 1032, 520),
+    (1000, 200, 1000), (2050, 264, 1544), (4097, 136, 2056), (8200, 72, 4104), (3000, 4096, 64),
+]
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("N,K,O", SHAPES)
+def test_forward_exact(N, K, O, act):
+    import grouped_gemm_top_amd as G
+    x, w = _ints((N, K), -2, 2, 1), _ints((O, K), -2, 2, 2)
+    b, r = _ints((O,), -50, 50, 3), _ints((N, O), -9, 9, 4)
+    g = Guards()
+    dx, dw, db, dr = _up(g, "x", x.to(BF)), _up(g, "w", w.to(BF)), _up(g, "b", b), _up(g, "r", r.to(BF))
+    out, z = g.alloc("out", (N, O), BF), g.alloc("z", (N, O), BF)
+    ws = g.alloc("ws", (G.workspace_bytes(G.OP_LINEAR_FWD, G.MOE_BF16, N, 1, 1, K, O),), torch.uint8)
+    G.linear_fwd(dx, dw, bias=db, act=act, residual=dr, out=out, z=z, ws=ws)
+    g.check("linear_fwd")
+    zr = _mm(x, w.t()) + b
+    f = (lambda v: v.clamp(min=0)) if act == "relu" else (lambda v: v)
+    assert torch.equal(z.cpu(), zr.to(BF)) and torch.equal(out.cpu(), (f(zr) + r).to(BF))
+    # no bias, no residual, no z; then in place over the residual
+    o2, z2 = G.linear_fwd(dx, dw, act=act)
+    assert z2 is None and torch.equal(o2.cpu(), f(_mm(x, w.t())).to(BF))
+    o3, _ = G.linear_fwd(dx, dw, bias=db, act=act, residual=dr, out=dr, ws=ws)
+    g.check("linear_fwd in place")
+    assert o3.data_ptr() == dr.data_ptr() and torch.equal(o3, out)
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("N,K,O", SHAPES)
+def test_backward_exact(N, K, O, act):
+    import grouped_gemm_top_amd as G
+    x, w = _ints((N, K), -2, 2, 5), _ints((O, K), -2, 2, 6)
+    d, z = _ints((N, O), -3, 3, 7), _ints((N, O), -1, 1, 8)
+    g = Guards()
+    D = {n: _up(g, n, t.to(BF)) for n, t in (("d", d), ("x", x), ("w", w), ("z", z))}
+    dx, dw, db = g.alloc("dx", (N, K), BF), g.alloc("dw", (O, K), BF), g.alloc("db", (O,), torch.float32)
+    ws = g.alloc("ws", (G.workspace_bytes(G.OP_LINEAR_BWD, G.MOE_BF16, N, 1, 1, K, O),), torch.uint8)
+    zz = D["z"] if act == "relu" else None
+    G.linear_bwd(D["d"], D["x"], D["w"], z=zz, act=act, dx=dx, dw=dw, dbias=db, ws=ws)
+    g.check("linear_bwd")
+    dz = d * (z > 0) if act == "relu" else d
+    assert torch.equal(dx.cpu(), _mm(dz, w).to(BF)), "dx"
+    assert torch.equal(dw.cpu(), _mm(dz.t(), x).to(BF)), "dw"
+    assert torch.equal(db.cpu(), dz.sum(0)), "dbias"
+    # each alone
+    for n, ref in (("dx", dx), ("dw", dw), ("dbias", db)):
+        r = G.linear_bwd(D["d"], D["x"], D["w"], z=zz, act=act, **{f"want_{m}": m == n for m in ("dx", "dw", "dbias")})
+        torch.cuda.synchronize()
+        assert torch.equal(r[n], ref) and all(r[m] is None for m in r if m != n)
+
+
+def _act64(v, act):
+    return {"none": lambda v: v, "relu": torch.relu, "silu": torch.nn.functional.silu,
+            "gelu": torch.nn.functional.gelu,
+            "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh")}[act](v)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("N,K,O", [(5, 264, 136), (200, 520, 328), (1030, 256, 1032)])
+def test_forward_activations(N, K, O, act):
+    import grouped_gemm_top_amd as G
+    x, w, b, r = _rand((N, K), 9), _rand((O, K), 10, K ** -0.5), _rand((O,), 11).float(), _rand((N, O), 12)
+    x[0] *= 30  # saturated activations too
+    out, z = G.linear_fwd(x.cuda(), w.cuda(), bias=b.cuda(), act=act, residual=r.cuda(), want_z=True)
+    z64 = x.double() @ w.double().t() + b.double()
+    ez = K * U * (x.double().abs() @ w.double().abs().t()) + U * z64.abs()
+    assert bool(((z.cpu().double() - z64).abs() <= ez + H * z64.abs()).all())
+    ref = _act64(z64, act) + r.double()
+    tol = 1.13 * ez + 16 * U * (z64.abs() + 1) + U * ref.abs() + H * ref.abs()
+    assert bool(((out.cpu().double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("N,K,O", [(1, 264, 136), (200, 520, 328), (1030, 256, 1032)])
+def test_backward_activations(N, K, O, act):
+    import grouped_gemm_top_amd as G
+    x, w, d, z = _rand((N, K), 13), _rand((O, K), 14, K ** -0.5), _rand((N, O), 15), _rand((N, O), 16, 1.5)
+    z[0, :4] = torch.tensor([40.0, -40.0, 0.0, 3e4])
+    r = G.linear_bwd(d.cuda(), x.cuda(), w.cuda(), z=z.cuda(), act=act)
+    z64 = z.double().requires_grad_(True)
+    slope = torch.autograd.grad(_act64(z64, act).sum(), z64)[0]
+    dz = d.double() * slope
+    e = 32 * U * d.double().abs()  # the slope's own error (it is at most 1.13)
+    each = H * dz.abs() + e * (1 + H)
+    x64, w64 = x.double(), w.double()
+    for n, ref, err, K_ in (("dx", dz @ w64, each @ w64.abs() + O * U * (dz.abs() @ w64.abs()), O),
+                            ("dw", dz.t() @ x64, each.t() @ x64.abs() + N * U * (dz.abs().t() @ x64.abs()), N)):
+        got = r[n].cpu().double()
+        assert bool(((got - ref).abs() <= err * 1.01 + H * ref.abs() + 2.0 ** -126).all()), n
+    tol = e.sum(0) + 256 * U * dz.abs().sum(0)
+    assert bool(((r["dbias"].cpu().double() - dz.sum(0)).abs() <= tol).all())
+
+
+def test_gradient_against_differences():
+    """dx, dw and dbias along random directions against central differences of the fp64 formula.
+    Beside the differences' own error (below 1e-5 of the size with steps of 2^-8) stand the two bf16
+    roundings, of dz and of the gradient: each term at most 2^-8, so at most 2^-7 of the sum of
+    the terms' magnitudes; they do not line up, so a tenth of that is asked for."""
+    import grouped_gemm_top_amd as G
+    N, K, O, act = 24, 64, 40, "gelu_tanh"
+    x, w, b, d = _rand((N, K), 17), _rand((O, K), 18, K ** -0.5), _rand((O,), 19).float(), _rand((N, O), 20)
+    _, z = G.linear_fwd(x.cuda(), w.cuda(), bias=b.cuda(), act=act, want_z=True)
+    r = {n: v.cpu().double() for n, v in G.linear_bwd(d.cuda(), x.cuda(), w.cuda(), z=z, act=act).items()}
+    off = z.cpu().double() - (x.double() @ w.double().t() + b.double())  # the stored z is the point
+    f = lambda xx, ww, bb: float((_act64(xx @ ww.t() + bb + off, act) * d.double()).sum())  # noqa: E731
+    st = 2.0 ** -8
+    base = [x.double(), w.double(), b.double()]
+    for i, n in enumerate(("dx", "dw", "dbias")):
+        for seed in range(3):
+            e = torch.randn(base[i].shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+            hi, lo = list(base), list(base)
+            hi[i], lo[i] = base[i] + st * e, base[i] - st * e
+            num = (f(*hi) - f(*lo)) / (2 * st)
+            terms = (r[n] * e).abs().sum()
+            assert abs(float((r[n] * e).sum()) - num) <= 0.1 * 2.0 ** -7 * float(terms), n
+
+
+def test_bad_rows_stay_alone():
+    """A NaN or infinity in one token's x reaches that token's outputs only, in every path."""
+    import grouped_gemm_top_amd as G
+    for N, K, O in ((5, 136, 72), (90, 200, 264), (700, 136, 520)):
+        x, w = _rand((N, K), 21), _rand((O, K), 22)
+        clean, _ = G.linear_fwd(x.cuda(), w.cuda())
+        x[2, K - 1] = float("nan")
+        x[4, 0] = float("inf")
+        got, _ = G.linear_fwd(x.cuda(), w.cuda())
+        keep = [t for t in range(N) if t not in (2, 4)]
+        assert torch.equal(got[keep], clean[keep]) and bool(got[2].isnan().all())
+
+
+def test_empty_input():
+    import grouped_gemm_top_amd as G
+    x, w = torch.empty((0, 64), dtype=BF, device="cuda"), _rand((24, 64), 23).cuda()
+    out, z = G.linear_fwd(x, w, want_z=True)
+    assert out.shape == (0, 24) and z.shape == (0, 24)
+    dw, db = torch.full((24, 64), 7.0, dtype=BF, device="cuda"), torch.full((24,), 7.0, device="cuda")
+    r = G.linear_bwd(out, x, w, dw=dw, dbias=db)
+    torch.cuda.synchronize()
+    assert r["dx"].shape == (0, 64) and float(dw.abs().max()) == 0.0 and float(db.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("N,K,O", [(3, 512, 264), (300, 2880, 512), (2050, 264, 1544)])
+def test_stream_and_graph(N, K, O):
+    import grouped_gemm_top_amd as G
+    x, w, b, d = _rand((N, K), 24).cuda(), _rand((O, K), 25, K ** -0.5).cuda(), _rand((O,), 26).float().cuda(), \
+        _rand((N, O), 27).cuda()
+
+    def both(**s):
+        out, z = G.linear_fwd(x, w, bias=b, act="gelu_tanh", residual=d, want_z=True, **s)
+        return dict(G.linear_bwd(d, x, w, z=z, act="gelu_tanh", **s), out=out, z=z)
+
+    eager = both()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = both(stream=s)
+    s.synchronize()
+    assert all(torch.equal(eager[n], other[n]) for n in eager)
+    graph, graph2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    with torch.cuda.graph(graph2):
+        got2 = both()
+    for seed in range(3):
+        x.copy_(_rand((N, K), 60 + seed))
+        graph.replay()
+        graph2.replay()
+        torch.cuda.synchronize()
+        eager = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(eager[n], got[n]) and torch.equal(eager[n], got2[n]) for n in eager)
