@@ -21,36 +21,55 @@ constexpr int BK = 64;  // k per LDS stage: a K-contiguous row of a stage is one
 enum Act { NONE = MOE_ACT_NONE, RELU = MOE_ACT_RELU, SILU = MOE_ACT_SILU, GELU = MOE_ACT_GELU,
            GELU_TANH = MOE_ACT_GELU_TANH };
 
-// 1 / (1 + e^-v): hardware exponential and reciprocal, about one unit in the last place each, far
-// below the bf16 rounding of what they feed
-__device__ __forceinline__ float sig(float v) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * v));
+// Activations and their slopes, compiled in: one dispatch serves eight values, which then run
+// interleaved.  Exponential and reciprocal are the hardware's, about one unit in the last place each,
+// far below the bf16 rounding of what they feed.
+// sig_scaled(t) = 1 / (1 + 2^-t), t = v log2 e for sigmoid(v)
+__device__ __forceinline__ float sig_scaled(float t) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-t));
 }
-constexpr float kG = 0.7978845608028654f, kG3 = 0.044715f;  // gelu_tanh: tanh(kG (v + kG3 v^3))
-__device__ __forceinline__ float act_fwd(float v, int act) {
-  switch (act) {
-    case RELU: return v > 0.f ? v : (v != v ? v : 0.f);
-    case SILU: return v * sig(v);
-    case GELU: return 0.5f * v * (1.0f + erff(0.70710678118654752f * v));
-    case GELU_TANH: return v * sig(2.0f * kG * v * (1.0f + kG3 * v * v));  // (1 + tanh u) / 2 = sig(2u)
-    default: return v;
+constexpr float kLog2e = 1.44269504088896340736f;
+// gelu_tanh: (1 + tanh u) / 2 = sigmoid(2u), u = kG (v + kG3 v^3), kG = sqrt(2 / pi)
+constexpr float kG = 0.7978845608028654f, kG3 = 0.044715f;
+template <int ACT>
+__device__ __forceinline__ float act_fwd1(float v) {
+  if constexpr (ACT == RELU) return v > 0.f ? v : (v != v ? v : 0.f);
+  else if constexpr (ACT == SILU) return v * sig_scaled(kLog2e * v);
+  else if constexpr (ACT == GELU) return 0.5f * v * (1.0f + erff(0.70710678118654752f * v));
+  else if constexpr (ACT == GELU_TANH)
+    return v * sig_scaled(v * (2.0f * kG * kLog2e + (2.0f * kG * kG3 * kLog2e) * (v * v)));
+  else return v;
+}
+template <int ACT>
+__device__ __forceinline__ float act_bwd1(float v) {
+  if constexpr (ACT == RELU) {
+    return v > 0.f ? 1.f : (v != v ? v : 0.f);
+  } else if constexpr (ACT == SILU) {
+    const float s = sig_scaled(kLog2e * v);
+    return s * (1.0f + v * (1.0f - s));
+  } else if constexpr (ACT == GELU) {
+    return 0.5f * (1.0f + erff(0.70710678118654752f * v)) +
+           v * 0.3989422804014327f * __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (v * v));
+  } else if constexpr (ACT == GELU_TANH) {
+    const float s = sig_scaled(v * (2.0f * kG * kLog2e + (2.0f * kG * kG3 * kLog2e) * (v * v)));
+    return s + v * s * (1.0f - s) * (2.0f * kG + (6.0f * kG * kG3) * (v * v));
+  } else {
+    return 1.f;
   }
 }
-__device__ __forceinline__ float act_bwd(float v, int act) {
+// v = act(v)
+template <int ACT>
+__device__ __forceinline__ void act_all(f32x4 (&v)[2]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = act_fwd1<ACT>(v[j >> 2][j & 3]);
+}
+__device__ __forceinline__ void act_fwd8(f32x4 (&v)[2], int act) {
   switch (act) {
-    case RELU: return v > 0.f ? 1.f : (v != v ? v : 0.f);
-    case SILU: {
-      const float s = sig(v);
-      return s * (1.0f + v * (1.0f - s));
-    }
-    case GELU:
-      return 0.5f * (1.0f + erff(0.70710678118654752f * v)) +
-             v * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.72134752044448170368f * v * v);
-    case GELU_TANH: {
-      const float s = sig(2.0f * kG * v * (1.0f + kG3 * v * v));
-      return s + v * s * (1.0f - s) * 2.0f * kG * (1.0f + 3.0f * kG3 * v * v);
-    }
-    default: return 1.f;
+    case RELU: act_all<RELU>(v); break;
+    case SILU: act_all<SILU>(v); break;
+    case GELU: act_all<GELU>(v); break;
+    case GELU_TANH: act_all<GELU_TANH>(v); break;
+    default: break;
   }
 }
 
@@ -73,28 +92,32 @@ __device__ __forceinline__ void stage_write(char* st, const f32x4* blk, int L) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(st + c * 256 + (((4 * j + g) ^ c) << 4)) = blk[j];
 }
-__device__ __forceinline__ f32x4 stage_read(const char* st, int p, int L) {
-  const int r = 4 * p + (L >> 4), q = L & 15;
-  return *reinterpret_cast<const f32x4*>(st + r * 256 + ((q ^ r) << 4));
+// columns 8 (L & 7) .. + 7 of row 8 p + (L >> 3)
+__device__ __forceinline__ void stage_read(const char* st, int p, int L, f32x4 (&v)[2]) {
+  const int r = 8 * p + (L >> 3), q = 2 * (L & 7);
+  v[0] = *reinterpret_cast<const f32x4*>(st + r * 256 + ((q ^ r) << 4));
+  v[1] = *reinterpret_cast<const f32x4*>(st + r * 256 + (((q + 1) ^ r) << 4));
+}
+__device__ __forceinline__ u32x4 pack8(const f32x4 (&v)[2]) {
+  return u32x4{pk2(v[0][0], v[0][1]), pk2(v[0][2], v[0][3]), pk2(v[1][0], v[1][1]), pk2(v[1][2], v[1][3])};
 }
 
-// the epilogue of four neighbouring columns n .. n + 3 of row m: acc -> outputs (N is a multiple of 8)
-__device__ __forceinline__ void finish4(const Args& a, int m, int n, f32x4 v, const float4& b) {
-  const size_t o = (size_t)m * a.N + n;
-  v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
-  if (a.z) *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.z) + o) = u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
-  if (a.act != NONE) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = act_fwd(v[j], a.act);
-  }
+// the epilogue of eight neighbouring columns: element o of the outputs, b their bias, r the residual's
+// values (read by the caller, before)
+__device__ __forceinline__ void finish8(const Args& a, size_t o, f32x4 (&v)[2], const f32x4 (&b)[2], const u32x4& r) {
+  v[0] += b[0];
+  v[1] += b[1];
+  if (a.z) *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.z) + o) = pack8(v);
+  act_fwd8(v, a.act);
   if (a.res) {
-    float r0, r1, r2, r3;
-    load4(static_cast<const bf16_t*>(a.res) + o, r0, r1, r2, r3);
-    v[0] += r0; v[1] += r1; v[2] += r2; v[3] += r3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j >> 1][2 * (j & 1)] += __uint_as_float(r[j] << 16);
+      v[j >> 1][2 * (j & 1) + 1] += __uint_as_float(r[j] & 0xFFFF0000u);
+    }
   }
-  *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.out) + o) = u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
+  *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.out) + o) = pack8(v);
 }
-
 // One operand's loads: R rows (K-contiguous) or R columns (K-strided) of a 64-wide k-step, as R / 8
 // kilobytes; instruction q of wavefront w fills kilobyte w + NW q, lane L its bytes 16 L .. 16 L + 15.
 //  K-contiguous: kilobyte b holds rows 8b .. 8b + 7 of 128 bytes, k-chunk c of row r at c ^ ((r >> 1) & 7)
@@ -105,7 +128,8 @@ struct Op {
   static_assert(R % (8 * NW) == 0 && NW % 2 == 0 && (KC || R >= 128), "whole kilobytes per wavefront");
   i32x4 r;
   uint32_t v[NI];  // this lane's byte offset at k = 0 (OOB when masked)
-  int kl[NI];      // k of this lane inside a step
+  int kl;          // k of this lane inside a step (K-strided: instruction 0's)
+  static constexpr int KQ = KC ? 0 : 512 * NW / R;  // and how much further each instruction's is
 
   // rows or columns x0 .. x0 + R - 1 of X; ld: row length in elements
   __device__ __forceinline__ void setup(const void* p, int X, int K, int x0, int w, int L) {
@@ -116,29 +140,24 @@ struct Op {
       if constexpr (KC) {
         const int row = x0 + 8 * b + (L >> 3);
         const int c = (L & 7) ^ ((4 * (w & 1) + (L >> 4)) & 7);
-        kl[q] = 8 * c;
+        kl = 8 * c;  // (the same for every q: NW is even)
         v[q] = row < X ? ((uint32_t)row * (uint32_t)K + 8u * c) * 2u : OOB;
       } else {
         constexpr int CPR = R / 8;  // chunks per k-row
         const int k = b * (64 / CPR) + L / CPR;
         const int col = x0 + 8 * ((L % CPR) ^ mn_f(k));
-        kl[q] = k;
+        if (q == 0) kl = k;
         v[q] = col < X ? ((uint32_t)k * (uint32_t)X + (uint32_t)col) * 2u : OOB;
       }
     }
   }
-  // the step at k0 into the stage area at LDS address m
-  __device__ __forceinline__ void issue(uint32_t m, int X, int K, int k0, int w) const {
-    const uint32_t step = KC ? (uint32_t)k0 * 2u : (uint32_t)k0 * (uint32_t)X * 2u;
-    if (k0 + BK <= K) {
-      const uint32_t so = (uint32_t)ufl((int)step);
-#pragma unroll
-      for (int q = 0; q < NI; ++q) dma16(r, m + (uint32_t)(w + NW * q) * 1024u, v[q], so);
-    } else {  // K tail: k >= K masked (K is a multiple of 8 where a chunk runs along k)
-#pragma unroll
-      for (int q = 0; q < NI; ++q)
-        dma16(r, m + (uint32_t)(w + NW * q) * 1024u, v[q] != OOB && k0 + kl[q] < K ? v[q] + step : OOB, 0u);
-    }
+  // Load instruction q of the step at k0 into the stage area at LDS address m; k >= kend (at most K)
+  // is masked per lane (K is a multiple of 8 where a chunk runs along k).  The uniform advance stays
+  // below 2^31, so a masked lane's offset is past the descriptor's range with and without it.
+  __device__ __forceinline__ void issue(int q, uint32_t m, int X, int k0, int kend, int w) const {
+    const uint32_t kk = (uint32_t)min(k0, kend);
+    dma16(r, m + (uint32_t)(w + NW * q) * 1024u, k0 + kl + KQ * q < kend ? v[q] : OOB,
+          (uint32_t)ufl((int)(KC ? kk * 2u : kk * (uint32_t)X * 2u)));
   }
 };
 
@@ -173,13 +192,14 @@ struct Frag {
 enum Epi { FWD = 0, PLAIN = 1, PART = 2 };
 
 // A BM x BN tile by WM x WN wavefronts, each (BM / WM) x (BN / WN) in 16 x 16 blocks.
-template <int BM, int BN, int WM, int WN, bool AKC, bool BKC, int EPI>
-__global__ __launch_bounds__(64 * WM * WN) void k_linear(Args a) {
+template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, int EPI>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
   constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;
   constexpr int OPA = BM * 128, STG = OPA + BN * 128;
   static_assert(NB % 4 == 0, "the epilogue stages 64 columns at a time");
-  static_assert(2 * STG >= NW * 4096, "the epilogue's staging");
-  __shared__ __attribute__((aligned(1024))) char s_ring[2 * STG];
+  static_assert(NST * STG >= NW * 4096, "the epilogue's staging");
+  static_assert(MB > 1 || NB == 4, "shapes below");
+  __shared__ __attribute__((aligned(1024))) char s_ring[NST * STG];
   const int L = threadIdx.x & 63, w = ufl(threadIdx.x >> 6);
   const int wm = w % WM, wn = w / WM;
   // XCD x gets the tiles x per .. (x + 1) per - 1 (workgroups go to XCDs round robin), in groups of
@@ -202,10 +222,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(Args a) {
   fra.init(L);
   frb.init(L);
   const uint32_t ring = lds_addr(s_ring);
-  auto issue = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t m = ring + (uint32_t)(kt & 1) * STG;
-    oa.issue(m, a.M, a.K, (k_lo + kt) * BK, w);
-    ob.issue(m + OPA, a.N, a.K, (k_lo + kt) * BK, w);
+  const int kend = min(a.K, (k_lo + nk) * BK);
+  constexpr int NIA = Op<BM, NW, AKC>::NI, NI = NIA + Op<BN, NW, BKC>::NI;
+  // load instruction q of step kt into stage st (a step past the last one is all masked)
+  auto issue = [&](int q, int kt, int st) __attribute__((always_inline)) {
+    const uint32_t m = ring + (uint32_t)st * STG;
+    if (q < NIA) oa.issue(q, m, a.M, (k_lo + kt) * BK, kend, w);
+    else ob.issue(q - NIA, m + OPA, a.N, (k_lo + kt) * BK, kend, w);
+  };
+  auto frag_a = [&](int i, int st, int sub) __attribute__((always_inline)) {
+    return fra.get(s_ring + st * STG, wm * (BM / WM) + 16 * i, sub);
+  };
+  auto frag_b = [&](int j, int st, int sub) __attribute__((always_inline)) {
+    return frb.get(s_ring + st * STG + OPA, wn * (BN / WN) + 16 * j, sub);
   };
 
   f32x4 acc[MB][NB];
@@ -214,56 +243,114 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(Args a) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  if (nk > 0) issue(0);
+  // A k-step is two half-steps of k = 32.  During a half-step's MFMAs the next one's fragments are
+  // read: a row block's A fragment is replaced as soon as its MFMAs are issued, B's have a second
+  // set.  The step's barrier sits inside its second half-step: by then every wavefront holds all of
+  // step kt in registers, so its stage takes the loads of step kt + NST, and step kt + 1 has landed
+  // for the reads that follow (its loads had NST - 1 steps; those of the NST - 2 steps after it may
+  // still be in flight).
+  bf16x8 fa[MB], fb[2][NB];
+#pragma unroll
+  for (int g = 0; g < NST; ++g)
+#pragma unroll
+    for (int q = 0; q < NI; ++q) issue(q, g, g);
+  vm_wait_barrier<(NST - 1) * NI>();
+#pragma unroll
+  for (int j = 0; j < NB; ++j) fb[0][j] = frag_b(j, 0, 0);
+#pragma unroll
+  for (int i = 0; i < MB; ++i) fa[i] = frag_a(i, 0, 0);
+  constexpr int BR = MB > 4 ? 2 : MB > 1 ? 1 : 0;  // row blocks of the second half-step before the barrier
+  constexpr int RP = (NB + MB + MB - BR - 1) / (MB - BR);  // fragment reads per row block after it
+  constexpr int LP = (NI + MB - BR - 1) / (MB - BR);       // and load instructions
+  // (sched_barrier keeps the compiler from gathering the reads at the end of a half-step)
+  int st3 = 0;
 #pragma unroll 1
   for (int kt = 0; kt < nk; ++kt) {
-    // step kt has landed for every wavefront, and every wavefront's reads of the other stage are
-    // complete
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kt + 1 < nk) issue(kt + 1);
-    const char* sa = s_ring + (kt & 1) * STG;
-    const char* sb = sa + OPA;
+    // this step's stage and the next one's
+    const int st = NST == 2 ? kt & 1 : st3, sn = NST == 2 ? st ^ 1 : (st + 1 == NST ? 0 : st + 1);
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      bf16x8 fb[NB];
+    for (int i = 0; i < MB; ++i) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) fb[j] = frb.get(sb, wn * (BN / WN) + 16 * j, sub);
-      bf16x8 fa = fra.get(sa, wm * (BM / WM), sub);
+      for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[0][j], fa[i], acc[i][j]);
+      fa[i] = frag_a(i, st, 1);
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        bf16x8 fn;
-        if (i + 1 < MB) fn = fra.get(sa, wm * (BM / WM) + 16 * (i + 1), sub);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[j], fa, acc[i][j]);
-        if (i + 1 < MB) fa = fn;
-      }
+      for (int j = i; j < NB; j += MB) fb[1][j] = frag_b(j, st, 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      if (i == BR)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NST - 2) * NI) : "memory");
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[1][j], fa[i], acc[i][j]);
+      if (i >= BR) {
+#pragma unroll
+        for (int q = (i - BR) * LP; q < (i - BR + 1) * LP && q < NI; ++q) issue(q, kt + NST, st);
+        // B's fragments first, then A's in order, each after its row block's MFMAs (past the last
+        // step they are read and never used)
+#pragma unroll
+        for (int q = (i - BR) * RP; q < (i - BR + 1) * RP && q < NB + MB; ++q) {
+          if (q < NB) fb[0][q] = frag_b(q, sn, 0);
+          else fa[q - NB] = frag_a(q - NB, sn, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    st3 = sn;
   }
+  vm_drain();  // (the masked loads past the last step write zeros into the ring)
   lds_barrier();  // the ring is free: it stages the epilogue
 
   // acc[i][j][v] = C[wm.. + 16 i + (L & 15)][wn.. + 16 j + 4 (L >> 4) + v]; through LDS a lane gets
-  // columns 4 (L & 15) .. + 3 of row 4 p + (L >> 4), so 16 lanes cover a row's 64 columns
-  char* st = s_ring + w * 4096;
+  // columns 8 (L & 7) .. + 7 of row 8 p + (L >> 3), so eight lanes cover a row's 128-byte line.  The
+  // residual of the whole 64-column strip is in flight before the first block needs it.
+  char* sg = s_ring + w * 4096;
 #pragma unroll
   for (int h = 0; h < NB / 4; ++h) {
-    const int n = n0 + wn * (BN / WN) + 64 * h + 4 * (L & 15);
-    float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (EPI == FWD && a.bias && n < a.N) bv = *reinterpret_cast<const float4*>(a.bias + n);
+    const int n = n0 + wn * (BN / WN) + 64 * h + 8 * (L & 7), mr = m0 + wm * (BM / WM) + (L >> 3);
+    u32x4 res[MB][2];
+    f32x4 bv[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    if constexpr (EPI == FWD) {
+      if (a.bias && n < a.N) {
+        bv[0] = *reinterpret_cast<const f32x4*>(a.bias + n);
+        bv[1] = *reinterpret_cast<const f32x4*>(a.bias + n + 4);
+      }
+      if (a.res) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int m = mr + 16 * i + 8 * p;
+            if (m < a.M && n < a.N)
+              res[i][p] = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(a.res) + (size_t)m * a.N + n);
+          }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      stage_write(st, &acc[i][4 * h], L);
+      stage_write(sg, &acc[i][4 * h], L);
+      if constexpr (EPI == PART) {  // fp32: sixteen lanes cover a row's 256 bytes
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const f32x4 v = stage_read(st, p, L);
-        const int m = m0 + wm * (BM / WM) + 16 * i + 4 * p + (L >> 4);
+        for (int p = 0; p < 4; ++p) {
+          const int r = 4 * p + (L >> 4), q = L & 15;
+          const f32x4 v = *reinterpret_cast<const f32x4*>(sg + r * 256 + ((q ^ r) << 4));
+          const int m = m0 + wm * (BM / WM) + 16 * i + r, nn = n0 + wn * (BN / WN) + 64 * h + 4 * q;
+          if (m < a.M && nn < a.N) *reinterpret_cast<f32x4*>(a.part + ((size_t)s * a.M + m) * a.N + nn) = v;
+        }
+        continue;
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        f32x4 v[2];
+        stage_read(sg, p, L, v);
+        const int m = mr + 16 * i + 8 * p;
+        const size_t o = (size_t)m * a.N + n;
         if (m < a.M && n < a.N) {
-          if constexpr (EPI == FWD)
-            finish4(a, m, n, v, bv);
-          else if constexpr (EPI == PLAIN)
-            *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.out) + (size_t)m * a.N + n) =
-                u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
-          else
-            *reinterpret_cast<f32x4*>(a.part + ((size_t)s * a.M + m) * a.N + n) = v;
+          if constexpr (EPI == FWD) {
+            finish8(a, o, v, bv, res[i][p]);
+          } else {
+            *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.out) + o) = pack8(v);
+          }
         }
       }
     }
@@ -273,27 +360,36 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(Args a) {
 // Split K: the slices' partial sums added in slice order, then the epilogue.
 template <int EPI>
 __global__ __launch_bounds__(256) void k_linear_sum(Args a) {
-  const size_t nv = (size_t)a.M * a.N / 4;
-  const int cpr = a.N / 4;
+  const size_t nv = (size_t)a.M * a.N / 8, slice = (size_t)a.M * a.N;
+  const int cpr = a.N / 8;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nv; i += (size_t)gridDim.x * 256) {
-    f32x4 v = *reinterpret_cast<const f32x4*>(a.part + 4 * i);
-    for (int s = 1; s < a.S; ++s) v += *reinterpret_cast<const f32x4*>(a.part + (size_t)s * a.M * a.N + 4 * i);
-    const int m = (int)(i / cpr), n = (int)(i - (size_t)m * cpr) * 4;
+    const int n = (int)(i % cpr) * 8;
+    u32x4 r = {0u, 0u, 0u, 0u};
+    f32x4 b[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     if constexpr (EPI == FWD) {
-      float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.bias) bv = *reinterpret_cast<const float4*>(a.bias + n);
-      finish4(a, m, n, v, bv);
-    } else {
-      *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(a.out) + 4 * i) = u32x2{pk2(v[0], v[1]), pk2(v[2], v[3])};
+      if (a.res) r = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(a.res) + 8 * i);
+      if (a.bias) {
+        b[0] = *reinterpret_cast<const f32x4*>(a.bias + n);
+        b[1] = *reinterpret_cast<const f32x4*>(a.bias + n + 4);
+      }
     }
+    f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 4
+    for (int s = 0; s < a.S; ++s) {
+      const float* p = a.part + (size_t)s * slice + 8 * i;
+      v[0] += *reinterpret_cast<const f32x4*>(p);
+      v[1] += *reinterpret_cast<const f32x4*>(p + 4);
+    }
+    if constexpr (EPI == FWD) finish8(a, 8 * i, v, b, r);
+    else *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.out) + 8 * i) = pack8(v);
   }
 }
 
 // Few tokens (M <= 16 NT): the product is one pass over W, so it streams W straight into registers.
 // A workgroup owns 16 outputs; its KW wavefronts take 64-wide k-steps in turn (each lane 2 x 16 bytes
 // of a W row: a row's 128-byte line), with the 16-token blocks of x as the other operand, and their
-// sums meet in LDS in wavefront order.
-template <int NT, int KW>
+// sums meet in LDS in wavefront order.  U k-steps' loads are in flight.
+template <int NT, int KW, int U>
 __global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
   __shared__ f32x4 s_sum[KW][NT][64];
   const int L = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -306,7 +402,6 @@ __global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = NT == 1 ? 4 : 2;  // k-steps in flight
   const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
   for (int k0 = w * 64; k0 < K; k0 += U * KW * 64) {
     bf16x8 fw[U][2], fx[U][NT][2];
@@ -330,18 +425,35 @@ __global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) s_sum[w][i][L] = acc[i];
   __syncthreads();
-  // acc[v] = C[token 16 i + (L & 15)][output o0 + 4 (L >> 4) + v]
-  for (int i = w; i < NT; i += KW) {
-    f32x4 v = s_sum[0][i][L];
+  // s_sum[..][l][v] = C[token 16 i + (l & 15)][output o0 + 4 (l >> 4) + v]: lane L finishes the eight
+  // outputs 8 (L >> 4) .. + 7 of token L & 15, lanes l and l + 16 with l = 32 (L >> 4) + (L & 15)
+  if (g < 2) {
+    for (int i = w; i < NT; i += KW) {
+      const int m = 16 * i + r, n = o0 + 8 * g;
+      if (m >= a.M || n >= a.N) continue;
+      const size_t o = (size_t)m * a.N + n;
+      f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+      f32x4 b[2] = {v[0], v[0]};
+      u32x4 res = {0u, 0u, 0u, 0u};
+      if (a.res) res = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(a.res) + o);
+      if (a.bias) {
+        b[0] = *reinterpret_cast<const f32x4*>(a.bias + n);
+        b[1] = *reinterpret_cast<const f32x4*>(a.bias + n + 4);
+      }
 #pragma unroll
-    for (int q = 1; q < KW; ++q) v += s_sum[q][i][L];
-    const int m = 16 * i + r, n = o0 + 4 * g;
-    if (m < a.M && n < a.N) {
-      float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.bias) bv = *reinterpret_cast<const float4*>(a.bias + n);
-      finish4(a, m, n, v, bv);
+      for (int q = 0; q < KW; ++q) {
+        v[0] += s_sum[q][i][32 * g + r];
+        v[1] += s_sum[q][i][32 * g + 16 + r];
+      }
+      finish8(a, o, v, b, res);
     }
   }
+}
+
+template <int ACT>
+__device__ __forceinline__ void times_slope(float (&d)[8], const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) d[j] *= act_bwd1<ACT>(v[j]);
 }
 
 // dz = dout act'(z) in bf16 (dz NULL: not written; z NULL: dz is dout) and the column sums of the
@@ -369,9 +481,12 @@ __global__ __launch_bounds__(256) void k_linear_dz(const bf16_t* __restrict__ do
         v[2 * j] = __uint_as_float(wz[j] << 16);
         v[2 * j + 1] = __uint_as_float(wz[j] & 0xFFFF0000u);
       }
-      if (z) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= act_bwd(v[j], act);
+      switch (act) {
+        case RELU: times_slope<RELU>(d, v); break;
+        case SILU: times_slope<SILU>(d, v); break;
+        case GELU: times_slope<GELU>(d, v); break;
+        case GELU_TANH: times_slope<GELU_TANH>(d, v); break;
+        default: break;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += d[j];
@@ -398,22 +513,28 @@ __global__ __launch_bounds__(256) void k_linear_dz(const bf16_t* __restrict__ do
 enum Kind { K_FWD, K_DX, K_DW };
 struct Shape { int big, S; };  // big: 2 = 256 x 256, 1 = 128 x 128, 0 = 64 x 64 (64 x 128 for dx)
 
-// Tile and K slices of a product: the choice with the least estimated time.
+// Tile and K slices of a product: the choice with the least estimated time,
+//   launch + rounds x (start and epilogue) + steps x max(latency of a step alone, tiles a CU x
+//   time of a step when the CU is full) (+ the partial sums' way to memory and back)
+// in us.  The constants are fitted to 110 random shapes (65 <= N <= 16384, 64 <= K, O <= 8192) with
+// every tile and slice count timed: the choice is on average 0.7 % slower than the best one
+// measured, at worst 17 %.
 Shape choose(Kind kind, int M, int N, int K) {
   const int steps = (K + BK - 1) / BK;
-  // time of one k-step of a workgroup (us) and its fixed part (start, epilogue); workgroups per CU
-  struct C { int bm, bn, occ; double step, fix; };
-  const C cs[3] = {{64, kind == K_FWD ? 64 : 128, 4, 0.75, 4.0}, {128, 128, 2, 1.0, 5.0}, {256, 256, 1, 1.5, 10.0}};
-  Shape best{0, 1};
+  struct C { int bm, bn, occ; double fix, lat, thr; };
+  const C cs[3] = {kind == K_FWD ? C{64, 64, 3, 3.0, 0.23, 0.26} : C{64, 128, 2, 3.0, 0.32, 0.47},
+                   {128, 128, 2, 3.1, 0.75, 0.49}, {256, 256, 1, 6.4, 0.40, 1.20}};
+  Shape best{1, 1};
   double tb = 1e30;
-  for (int b = 0; b < 3; ++b) {
-    if (kind == K_DW && b == 0) continue;
+  for (int b = kind == K_DW ? 1 : 0; b < 3; ++b) {
     const long long tiles = (long long)((M + cs[b].bm - 1) / cs[b].bm) * ((N + cs[b].bn - 1) / cs[b].bn);
     for (int S = 1; S <= 16 && S <= steps; S *= 2) {
-      if (S > 1 && (S * tiles > 1024 || (double)S * M * N * 4 > 64e6)) break;
-      const long long rounds = (tiles * S + 256 * cs[b].occ - 1) / (256 * cs[b].occ);
-      double t = rounds * (((steps + S - 1) / S) * cs[b].step + cs[b].fix);
-      if (S > 1) t += 3.0 + (double)S * M * N * 4 / 3e6;
+      const double elems = (double)S * M * N;
+      if (S > 1 && elems > 64e6) break;  // at most 256 MB of partial sums
+      const long long tpc = (tiles * S + 255) / 256, rounds = (tpc + cs[b].occ - 1) / cs[b].occ;
+      const double step = cs[b].thr * tpc > cs[b].lat ? cs[b].thr * tpc : cs[b].lat;
+      double t = 2.5 + rounds * cs[b].fix + (steps + S - 1) / S * step;
+      if (S > 1) t += 2.2 + 2.3e-6 * elems;
       if (t < tb) tb = t, best = Shape{b, S};
     }
   }
@@ -426,7 +547,7 @@ size_t part_bytes(Kind kind, int M, int N, int K) {
   return c.S > 1 ? up((size_t)c.S * M * N * 4) : 0;
 }
 
-template <int BM, int BN, int WM, int WN, bool AKC, bool BKC>
+template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC>
 void launch(Args& a, int S, hipStream_t s) {
   a.nM = (a.M + BM - 1) / BM;
   a.nN = (a.N + BN - 1) / BN;
@@ -435,25 +556,25 @@ void launch(Args& a, int S, hipStream_t s) {
   a.per = (int)((T + 7) / 8);
   const dim3 g((unsigned)(8 * a.per)), b(64 * WM * WN);
   if (S > 1)
-    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, AKC, BKC, PART>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, NST, AKC, BKC, PART>), g, b, 0, s, a);
   else  // (both operands K-contiguous: the forward)
-    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, AKC, BKC, AKC && BKC ? FWD : PLAIN>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, NST, AKC, BKC, AKC && BKC ? FWD : PLAIN>), g, b, 0, s, a);
 }
 
 hipError_t product(Kind kind, Args a, void* ws, hipStream_t s) {
   const Shape c = choose(kind, a.M, a.N, a.K);
   a.part = static_cast<float*>(ws);
   if (kind == K_FWD) {
-    if (c.big == 2) launch<256, 256, 2, 4, true, true>(a, c.S, s);
-    else if (c.big == 1) launch<128, 128, 2, 2, true, true>(a, c.S, s);
-    else launch<64, 64, 4, 1, true, true>(a, c.S, s);
+    if (c.big == 2) launch<256, 256, 2, 4, 2, true, true>(a, c.S, s);
+    else if (c.big == 1) launch<128, 128, 2, 2, 2, true, true>(a, c.S, s);
+    else launch<64, 64, 4, 1, 3, true, true>(a, c.S, s);
   } else if (kind == K_DX) {
-    if (c.big == 2) launch<256, 256, 2, 4, true, false>(a, c.S, s);
-    else if (c.big == 1) launch<128, 128, 2, 2, true, false>(a, c.S, s);
-    else launch<64, 128, 2, 2, true, false>(a, c.S, s);
+    if (c.big == 2) launch<256, 256, 2, 4, 2, true, false>(a, c.S, s);
+    else if (c.big == 1) launch<128, 128, 2, 2, 2, true, false>(a, c.S, s);
+    else launch<64, 128, 2, 2, 3, true, false>(a, c.S, s);
   } else {
-    if (c.big == 2) launch<256, 256, 2, 4, false, false>(a, c.S, s);
-    else launch<128, 128, 2, 2, false, false>(a, c.S, s);
+    if (c.big == 2) launch<256, 256, 2, 4, 2, false, false>(a, c.S, s);
+    else launch<128, 128, 2, 2, 2, false, false>(a, c.S, s);
   }
   if (c.S > 1) {
     const size_t nv = (size_t)a.M * a.N / 4;
@@ -488,9 +609,9 @@ hipError_t launch_linear_fwd(const void* x, const void* w, const float* bias, in
   a.out = out; a.z = z; a.bias = bias; a.res = res; a.act = act;
   if (N <= FEW) {
     const dim3 g((unsigned)((O + 15) / 16));
-    if (N <= 16) hipLaunchKernelGGL((k_linear_few<1, 8>), g, dim3(512), 0, s, a);
-    else if (N <= 32) hipLaunchKernelGGL((k_linear_few<2, 8>), g, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((k_linear_few<4, 8>), g, dim3(512), 0, s, a);
+    if (N <= 16) hipLaunchKernelGGL((k_linear_few<1, 8, 4>), g, dim3(512), 0, s, a);
+    else if (N <= 32) hipLaunchKernelGGL((k_linear_few<2, 8, 2>), g, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_few<4, 8, 2>), g, dim3(512), 0, s, a);
     return hipGetLastError();
   }
   return product(K_FWD, a, ws, s);
