@@ -585,9 +585,13 @@ hipError_t product(Kind kind, Args a, void* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int FEW = 64;  // tokens up to which W is streamed into registers
+// Calls whose W is streamed into registers (k_linear_few) rather than tiled.  Measured, us (few /
+// tiles): K = O = 2048: N = 1 5.5 / 7.8, 16 6.9 / 8.4, 32 8.9 / 8.8; K = O = 4096: N = 1 8.6 / 13.5,
+// 16 11.6 / 10.7, 32 14.6 / 10.9; K = 512, O = 4096: N = 32 4.4 / 5.5.
+bool few_tokens(int N, int K) { return N <= 16 || (N <= 32 && K <= 2048); }
 
-int dz_groups(int N) { return N <= 4 ? 1 : (N >= 512 ? 128 : (N + 3) / 4); }
+// row groups of the dz kernel: one (its column sums are dbias) for few rows
+int dz_groups(int N) { return N <= 64 ? 1 : (N >= 2048 ? 128 : (N + 15) / 16); }
 
 __global__ __launch_bounds__(256) void k_zero16(uint4* __restrict__ p, size_t n) {
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
@@ -597,7 +601,7 @@ __global__ __launch_bounds__(256) void k_zero16(uint4* __restrict__ p, size_t n)
 }  // namespace ln
 
 size_t linear_fwd_ws_bytes(int N, int K, int O) {
-  return 256 + (N <= ln::FEW ? 0 : ln::part_bytes(ln::K_FWD, N, O, K));
+  return 256 + (ln::few_tokens(N, K) ? 0 : ln::part_bytes(ln::K_FWD, N, O, K));
 }
 
 hipError_t launch_linear_fwd(const void* x, const void* w, const float* bias, int act, const void* res, int N, int K,
@@ -607,11 +611,10 @@ hipError_t launch_linear_fwd(const void* x, const void* w, const float* bias, in
   Args a{};
   a.A = x; a.B = w; a.M = N; a.N = O; a.K = K;
   a.out = out; a.z = z; a.bias = bias; a.res = res; a.act = act;
-  if (N <= FEW) {
+  if (few_tokens(N, K)) {
     const dim3 g((unsigned)((O + 15) / 16));
     if (N <= 16) hipLaunchKernelGGL((k_linear_few<1, 8, 4>), g, dim3(512), 0, s, a);
-    else if (N <= 32) hipLaunchKernelGGL((k_linear_few<2, 8, 2>), g, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((k_linear_few<4, 8, 2>), g, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_few<2, 8, 2>), g, dim3(512), 0, s, a);
     return hipGetLastError();
   }
   return product(K_FWD, a, ws, s);

@@ -477,7 +477,7 @@ moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, cons
  * x [N,K], w [O,K] (an nn.Linear weight), res, out, z [N,O], all bf16; z (the rounded z, what the
  * backward takes) is written unless NULL.  out may be res (in place), z is neither.  Bias, activation
  * and residual are applied in fp32 and out is rounded once.  K and O are multiples of 8, tensors
- * and workspace 16-byte aligned, and x, w, out each smaller than 2 GiB.  N <= 64 reads w once,
+ * and workspace 16-byte aligned, and x, w, out each smaller than 2 GiB.  N <= 16 reads w once,
  * straight into registers (a decoding step).
  * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_FWD, MOE_BF16, N, 1, 1, K, O, 0).
  *
