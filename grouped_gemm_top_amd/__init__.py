@@ -142,7 +142,7 @@ def load_library(path: str):
 
 
 def _check(st: int):
-    if st != MOE_OK:
+    if st:
         raise MoEError(st, lib().moe_last_error().decode(errors="replace"))
 
 
@@ -495,7 +495,9 @@ def _want(name, t, shape, dtype, dev):
 
 def _out(name, t, shape, dtype, like, dev):
     """The caller's output tensor, checked, or a new one."""
-    return like.new_empty(shape, dtype=dtype) if t is None else _want(name, t, shape, dtype, dev)
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _want(name, t, shape, dtype, dev)
 
 
 def _on_gpu(t):
@@ -510,9 +512,8 @@ def _op_bytes(*query) -> int:
 
 def _op_ws(nbytes, like, ws, dev):
     """The caller's workspace, checked, or a new one."""
-    import torch
     if ws is None:
-        return like.new_empty((nbytes,), dtype=torch.uint8)
+        return like.new_empty((nbytes,), dtype=_torch.uint8)
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"the workspace must be contiguous and on the tensors' device (is on {ws.device})")
     return _ws(nbytes, None, ws)
@@ -522,14 +523,25 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_torch = None  # the torch module, from the first call on
+
+
+def _first_use():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _on_stream(fn):
     """Run a binding on its first tensor's device and, if `stream` is given, with that stream as
     the current one: what the call allocates then belongs to the stream that uses it."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        import torch
-        if stream is None and (not first.is_cuda or first.get_device() == torch.cuda.current_device()):
-            return fn(first, *args, **kw)  # (a host tensor is refused there)
+        torch = _torch or _first_use()
+        # (a host tensor is refused by the binding)
+        if stream is None and (first.get_device() == torch._C._cuda_getDevice() if first.is_cuda else True):
+            return fn(first, *args, **kw)
         _on_gpu(first)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
@@ -543,8 +555,7 @@ def _on_stream(fn):
 
 def _cur(dev):
     """The current stream's handle on device dev."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 @_on_stream
@@ -556,7 +567,7 @@ def add_rmsnorm(x, w=None, residual=None, eps: float = 1e-6, want_h=True, want_y
     -> dict(h [N,H] (the sum, in residual's type), y [N,H] (x's type), q uint8 [N,H], scales uint8
     [N, 4 ceil(H/128)]: y as MX-FP8, as quantize_mxfp8 lays it out); what is not wanted is None.
     h may be residual (in place).  stream: a torch stream to run on (default: the current one)."""
-    import torch
+    torch = _torch
     if x.dim() != 2:
         raise ValueError(f"x must be [N, H] (got {tuple(x.shape)})")
     N, H = x.shape
@@ -593,7 +604,7 @@ def add_rmsnorm_bwd(dy, h, w=None, dh_in=None, eps: float = 1e-6, want_dx=False,
     """Backward of add_rmsnorm at the stored sum h: dy [N,H] is the gradient of y, dh_in (h's type, or
     None) the one that reaches h itself.  -> dict(dh [N,H] in h's type (the gradient of x and of
     residual), dx: dh in dy's type if wanted, dw fp32 [H] or None).  dh may be dh_in (in place)."""
-    import torch
+    torch = _torch
     if dy.dim() != 2:
         raise ValueError(f"dy must be [N, H] (got {tuple(dy.shape)})")
     N, H = dy.shape
@@ -621,7 +632,7 @@ def add_rmsnorm_bwd(dy, h, w=None, dh_in=None, eps: float = 1e-6, want_dx=False,
 
 def _seqs(N, mask, seq_ptr, dev):
     """The sequences' checks shared by balance_loss and its backward -> B."""
-    import torch
+    torch = _torch
     if mask is not None:
         if mask.dtype not in (torch.uint8, torch.bool):
             raise TypeError(f"mask must be uint8 or bool (got {mask.dtype})")
@@ -643,7 +654,7 @@ def balance_loss(logits, topk_idx, alpha: float, beta: float = 0.0, bias=None, m
     [B+1] (None: one sequence), mask uint8 or bool [N] (0: padding; None: no padding).
     -> dict(loss fp32 [2] (alpha's balance loss, beta's z-loss), counts int32 [B,E], saved fp32
     [B*E + 1] for balance_loss_bwd).  stream: a torch stream to run on (default: the current one)."""
-    import torch
+    torch = _torch
     if logits.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("logits must be [N, E] and topk_idx [N, k]")
     N, E = logits.shape
@@ -670,7 +681,7 @@ def balance_loss_bwd(logits, saved, bias=None, mask=None, seq_ptr=None, dloss=No
     """Gradient of balance_loss with respect to the logits, from its `saved` and the same logits,
     bias, mask and seq_ptr -> dlogits fp32 [N,E].  dloss fp32 [2]: the two losses' gradients (None:
     ones); dlogits_in is added (dlogits may be dlogits_in)."""
-    import torch
+    torch = _torch
     if logits.dim() != 2:
         raise ValueError(f"logits must be [N, E] (got {tuple(logits.shape)})")
     N, E = logits.shape
@@ -702,7 +713,7 @@ def linear_fwd(x, w, bias=None, act="none", residual=None, want_z=False, out=Non
     """out = act(x w^T + bias) + residual, bf16: x [N,K], w [O,K], bias fp32 [O], residual [N,O];
     act: a key of ACTIVATIONS.  -> (out [N,O], z [N,O] (the product with its bias, for linear_bwd)
     or None).  out may be residual (in place).  stream: a torch stream to run on."""
-    import torch
+    torch = _torch
     bf = torch.bfloat16
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N, K] and w [O, K]")
@@ -732,7 +743,7 @@ def linear_bwd(dout, x, w, z=None, act="none", want_dx=True, want_dw=True, want_
                dbias=None, ws=None):
     """Backward of linear_fwd from dout [N,O] and the z it stored (None for act "none") -> dict(dx
     [N,K], dw [O,K], dbias fp32 [O]); what is not wanted is None.  residual's gradient is dout."""
-    import torch
+    torch = _torch
     bf = torch.bfloat16
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N, K] and w [O, K]")
