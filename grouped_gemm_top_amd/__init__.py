@@ -127,8 +127,8 @@ def load_library(path: str):
     L.moe_balance_loss.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp, vp, vp, sz, vp]
     L.moe_balance_loss_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
     L.moe_router_bwd_acc.argtypes = [ctypes.c_int, vp, vp, vp, pp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
-    L.moe_linear_fwd.argtypes = [vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, sz, vp]
-    L.moe_linear_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.moe_linear_fwd.argtypes = [ctypes.c_int, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.moe_linear_bwd.argtypes = [ctypes.c_int, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
@@ -710,30 +710,30 @@ def _act(act):
 
 @_on_stream
 def linear_fwd(x, w, bias=None, act="none", residual=None, want_z=False, out=None, z=None, ws=None):
-    """out = act(x w^T + bias) + residual, bf16: x [N,K], w [O,K], bias fp32 [O], residual [N,O];
+    """out = act(x w^T + bias) + residual: x [N,K], w [O,K], residual [N,O] bf16 or fp32, bias fp32 [O];
     act: a key of ACTIVATIONS.  -> (out [N,O], z [N,O] (the product with its bias, for linear_bwd)
     or None).  out may be residual (in place).  stream: a torch stream to run on."""
     torch = _torch
-    bf = torch.bfloat16
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N, K] and w [O, K]")
     N, K = x.shape
     O = w.shape[0]
+    dt, ty = _dtype_code(x), x.dtype
     dev = x.get_device()
-    _want("x", x, (N, K), bf, dev)
-    _want("w", w, (O, K), bf, dev)
+    _want("x", x, (N, K), ty, dev)
+    _want("w", w, (O, K), ty, dev)
     if bias is not None:
         _want("bias", bias, (O,), torch.float32, dev)
     if residual is not None:
-        _want("residual", residual, (N, O), bf, dev)
+        _want("residual", residual, (N, O), ty, dev)
     code = _act(act)
     _on_gpu(x)
-    out = _out("out", out, (N, O), bf, x, dev)
+    out = _out("out", out, (N, O), ty, x, dev)
     if want_z or z is not None:
-        z = _out("z", z, (N, O), bf, x, dev)
-    nb = _op_bytes(OP_LINEAR_FWD, MOE_BF16, N, 1, 1, K, O, 0)
+        z = _out("z", z, (N, O), ty, x, dev)
+    nb = _op_bytes(OP_LINEAR_FWD, dt, N, 1, 1, K, O, 0)
     ws = _op_ws(nb, x, ws, dev)
-    _check(lib().moe_linear_fwd(_addr(x), _addr(w), _addr(bias), code, _addr(residual), N, K, O, _addr(out), _addr(z),
+    _check(lib().moe_linear_fwd(dt, _addr(x), _addr(w), _addr(bias), code, _addr(residual), N, K, O, _addr(out), _addr(z),
                                 _addr(ws), nb, _cur(dev)))
     return out, z
 
@@ -744,30 +744,30 @@ def linear_bwd(dout, x, w, z=None, act="none", want_dx=True, want_dw=True, want_
     """Backward of linear_fwd from dout [N,O] and the z it stored (None for act "none") -> dict(dx
     [N,K], dw [O,K], dbias fp32 [O]); what is not wanted is None.  residual's gradient is dout."""
     torch = _torch
-    bf = torch.bfloat16
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N, K] and w [O, K]")
     N, K = x.shape
     O = w.shape[0]
+    dt, ty = _dtype_code(dout), dout.dtype
     dev = dout.get_device()
-    _want("dout", dout, (N, O), bf, dev)
-    _want("x", x, (N, K), bf, dev)
-    _want("w", w, (O, K), bf, dev)
+    _want("dout", dout, (N, O), ty, dev)
+    _want("x", x, (N, K), ty, dev)
+    _want("w", w, (O, K), ty, dev)
     code = _act(act)
     if z is not None:
-        _want("z", z, (N, O), bf, dev)
+        _want("z", z, (N, O), ty, dev)
     elif code:
         raise ValueError(f"the backward of {act} needs z")
     _on_gpu(dout)
     if want_dx or dx is not None:
-        dx = _out("dx", dx, (N, K), bf, dout, dev)
+        dx = _out("dx", dx, (N, K), ty, dout, dev)
     if want_dw or dw is not None:
-        dw = _out("dw", dw, (O, K), bf, dout, dev)
+        dw = _out("dw", dw, (O, K), ty, dout, dev)
     if want_dbias or dbias is not None:
         dbias = _out("dbias", dbias, (O,), torch.float32, dout, dev)
-    nb = _op_bytes(OP_LINEAR_BWD, MOE_BF16, N, 1, 1, K, O, 0)
+    nb = _op_bytes(OP_LINEAR_BWD, dt, N, 1, 1, K, O, 0)
     ws = _op_ws(nb, dout, ws, dev)
     if N or dw is not None or dbias is not None:
-        _check(lib().moe_linear_bwd(_addr(dout), _addr(x), _addr(w), _addr(z), code, N, K, O, _addr(dx), _addr(dw),
+        _check(lib().moe_linear_bwd(dt, _addr(dout), _addr(x), _addr(w), _addr(z), code, N, K, O, _addr(dx), _addr(dw),
                                     _addr(dbias), _addr(ws), nb, _cur(dev)))
     return dict(dx=dx, dw=dw, dbias=dbias)

@@ -108,13 +108,18 @@ moe_status check_desc_sizes(moe_dtype dt, int64_t N, int64_t H, int64_t I, int64
   return MOE_OK;
 }
 
-// sizes of the dense products (their kernels address each tensor with 32-bit byte offsets)
-moe_status check_linear(int32_t N, int32_t K, int32_t O) {
+// type and sizes of the dense products: their kernels address each operand (in fp32 its three bf16
+// parts) with 32-bit byte offsets
+moe_status check_linear(moe_dtype dt, int32_t N, int32_t K, int32_t O) {
+  moe_status st;
+  if ((st = check_dtype(dt)) != MOE_OK) return st;
   REQUIRE(N >= 0, MOE_EINVAL, "N must be >= 0 (got %d)", N);
   REQUIRE(K >= 8 && O >= 8, MOE_EINVAL, "K and O must be >= 8 (got K=%d, O=%d)", K, O);
   REQUIRE(K % 8 == 0 && O % 8 == 0, MOE_EUNSUPPORTED, "K and O must be multiples of 8 (got K=%d, O=%d)", K, O);
-  REQUIRE((int64_t)N * K * 2 <= kDescBytes && (int64_t)N * O * 2 <= kDescBytes && (int64_t)O * K * 2 <= kDescBytes,
-          MOE_EUNSUPPORTED, "x [N=%d, K=%d], w [O=%d, K] and out [N, O] must each be < 2 GiB", N, K, O);
+  const int64_t es = dt == MOE_F32 ? 6 : 2;
+  REQUIRE((int64_t)N * K * es <= kDescBytes && (int64_t)N * O * es <= kDescBytes && (int64_t)O * K * es <= kDescBytes,
+          MOE_EUNSUPPORTED, "x [N=%d, K=%d], w [O=%d, K] and out [N, O] must each be < 2 GiB (bf16; fp32: a third of it "
+          "in elements)", N, K, O);
   return MOE_OK;
 }
 
@@ -202,11 +207,11 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
       if (I < 1 || I > kMaxSeqs) return 0;
       return moe::balance_loss_ws_bytes(N, E, I);
     case MOE_OP_LINEAR_FWD:
-      if (check_linear(N, H, I) != MOE_OK) return 0;
-      return moe::linear_fwd_ws_bytes(N, H, I);
+      if (check_linear(dt, N, H, I) != MOE_OK) return 0;
+      return moe::linear_fwd_ws_bytes(dt, N, H, I);
     case MOE_OP_LINEAR_BWD:
-      if (check_linear(N, H, I) != MOE_OK) return 0;
-      return moe::linear_bwd_ws_bytes(N, H, I);
+      if (check_linear(dt, N, H, I) != MOE_OK) return 0;
+      return moe::linear_bwd_ws_bytes(dt, N, H, I);
     case MOE_OP_ADD_RMSNORM_BWD:
       if (check_norm(dt, dt, N, H) != MOE_OK) return 0;
       return moe::add_rmsnorm_bwd_ws_bytes(N, H);
@@ -608,11 +613,12 @@ moe_status moe_balance_loss_bwd(const float* logits, const float* bias, const ui
   return hip_status(e, "moe_balance_loss_bwd");
 }
 
-moe_status moe_linear_fwd(const void* x, const void* w, const float* bias, int32_t act, const void* res, int32_t N,
-                          int32_t K, int32_t O, void* out, void* z, void* ws, size_t ws_bytes, void* stream) {
+moe_status moe_linear_fwd(moe_dtype dt, const void* x, const void* w, const float* bias, int32_t act, const void* res,
+                          int32_t N, int32_t K, int32_t O, void* out, void* z, void* ws, size_t ws_bytes,
+                          void* stream) {
   g_err[0] = 0;
   moe_status st;
-  if ((st = check_linear(N, K, O)) != MOE_OK) return st;
+  if ((st = check_linear(dt, N, K, O)) != MOE_OK) return st;
   REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, MOE_EINVAL, "unknown activation %d", act);
   REQUIRE(w, MOE_EINVAL, "NULL w");
   REQUIRE(N == 0 || (x && out), MOE_EINVAL, "NULL x/out");
@@ -621,21 +627,21 @@ moe_status moe_linear_fwd(const void* x, const void* w, const float* bias, int32
   REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(res) && aligned16(out) && aligned16(z) &&
               aligned16(ws),
           MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned");
-  const size_t need = moe::linear_fwd_ws_bytes(N, K, O);
+  const size_t need = moe::linear_fwd_ws_bytes(dt, N, K, O);
   REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
   REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
   moe::kernel_event(MOE_K_LINEAR, 0, (hipStream_t)stream);
-  hipError_t e = moe::launch_linear_fwd(x, w, bias, act, res, N, K, O, out, z, ws, (hipStream_t)stream);
+  hipError_t e = moe::launch_linear_fwd(dt, x, w, bias, act, res, N, K, O, out, z, ws, (hipStream_t)stream);
   moe::kernel_event(MOE_K_LINEAR, 1, (hipStream_t)stream);
   return hip_status(e, "moe_linear_fwd");
 }
 
-moe_status moe_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int32_t act, int32_t N,
-                          int32_t K, int32_t O, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+moe_status moe_linear_bwd(moe_dtype dt, const void* dout, const void* x, const void* w, const void* z, int32_t act,
+                          int32_t N, int32_t K, int32_t O, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
                           void* stream) {
   g_err[0] = 0;
   moe_status st;
-  if ((st = check_linear(N, K, O)) != MOE_OK) return st;
+  if ((st = check_linear(dt, N, K, O)) != MOE_OK) return st;
   REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH, MOE_EINVAL, "unknown activation %d", act);
   REQUIRE(dx || dw || dbias, MOE_EINVAL, "no gradient requested");
   REQUIRE(N == 0 || dout, MOE_EINVAL, "NULL dout");
@@ -648,11 +654,11 @@ moe_status moe_linear_bwd(const void* dout, const void* x, const void* w, const 
   REQUIRE(aligned16(dout) && aligned16(x) && aligned16(w) && aligned16(z) && aligned16(dx) && aligned16(dw) &&
               aligned16(dbias) && aligned16(ws),
           MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned");
-  const size_t need = moe::linear_bwd_ws_bytes(N, K, O);
+  const size_t need = moe::linear_bwd_ws_bytes(dt, N, K, O);
   REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
   REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
   moe::kernel_event(MOE_K_LINEAR_BWD, 0, (hipStream_t)stream);
-  hipError_t e = moe::launch_linear_bwd(dout, x, w, z, act, N, K, O, dx, dw, dbias, ws, (hipStream_t)stream);
+  hipError_t e = moe::launch_linear_bwd(dt, dout, x, w, z, act, N, K, O, dx, dw, dbias, ws, (hipStream_t)stream);
   moe::kernel_event(MOE_K_LINEAR_BWD, 1, (hipStream_t)stream);
   return hip_status(e, "moe_linear_bwd");
 }

@@ -155,10 +155,10 @@ hipError_t launch_balance_loss_bwd(const float* logits, const float* bias, const
                                    float* dz, hipStream_t s);
 // out [H] = the sum of G rows [G, H] in a fixed order (norm.hip)
 void launch_sum_rows(const float* part, int G, int H, float* out, hipStream_t s);
-size_t linear_fwd_ws_bytes(int N, int K, int O);
-size_t linear_bwd_ws_bytes(int N, int K, int O);
-hipError_t launch_linear_fwd(const void* x, const void* w, const float* bias, int act, const void* res, int N, int K,
-                             int O, void* out, void* z, void* ws, hipStream_t s);
-hipError_t launch_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int act, int N, int K,
-                             int O, void* dx, void* dw, float* db, void* ws, hipStream_t s);
+size_t linear_fwd_ws_bytes(moe_dtype dt, int N, int K, int O);
+size_t linear_bwd_ws_bytes(moe_dtype dt, int N, int K, int O);
+hipError_t launch_linear_fwd(moe_dtype dt, const void* x, const void* w, const float* bias, int act, const void* res,
+                             int N, int K, int O, void* out, void* z, void* ws, hipStream_t s);
+hipError_t launch_linear_bwd(moe_dtype dt, const void* dout, const void* x, const void* w, const void* z, int act,
+                             int N, int K, int O, void* dx, void* dw, float* db, void* ws, hipStream_t s);
 }  // namespace moe

@@ -1,13 +1,21 @@
-// linear.hip -- the dense bf16 product with bias, activation and residual in its epilogue, and its
-// backward, for gfx950.
+// linear.hip -- the dense product with bias, activation and residual in its epilogue, and its
+// backward, for gfx950 (bf16, and fp32 at fp32 accuracy).
 //
-//   z = x W^T + b,   out = act(z) + res,  z kept in bf16 where asked     x [N,K], W [O,K], out [N,O]
+//   z = x W^T + b,   out = act(z) + res,  z kept where asked             x [N,K], W [O,K], out [N,O]
 //   dz = dout act'(z),   dx = dz W,   dW = dz^T x,   db = sum_t dz
 //
 // The three products are one kernel, C[m][n] = sum_k A(m,k) B(n,k), in three layouts: forward with
 // both operands K-contiguous, dx with B K-strided (W read along its rows), dW with both K-strided.
-// Accumulation, bias, activation and residual are fp32; each output is rounded once.  dz is rounded
-// to bf16 before its two products (the matrix cores take bf16), db sums it unrounded.
+// Accumulation, bias, activation and residual are fp32; each output is rounded once.  In bf16 dz is
+// rounded to bf16 before its two products (the matrix cores take bf16), db sums it unrounded.
+//
+// fp32 operands are split exactly into three bf16 parts, v = v0 + v1 + v2 (8 significant bits
+// each), and the product is the sum of the part products (0,0) (0,1) (1,0) (1,1) (0,2) (2,0); the
+// others are below 2^-24 of the leading one.  The kernel walks those six terms as one contraction
+// six times as long: a term only moves the two operands' plane offsets.  The matrix cores' fp32
+// instructions would take 16 times as long as one bf16 term, these six take 6 times.
+#include <type_traits>
+
 #include "gemm_lds.h"
 
 namespace moe {
@@ -102,21 +110,48 @@ __device__ __forceinline__ u32x4 pack8(const f32x4 (&v)[2]) {
   return u32x4{pk2(v[0][0], v[0][1]), pk2(v[0][2], v[0][3]), pk2(v[1][0], v[1][1]), pk2(v[1][2], v[1][3])};
 }
 
+// eight values from element o of p on, in type T
+template <typename T>
+__device__ __forceinline__ void store8(void* p, size_t o, const f32x4 (&v)[2]) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<u32x4*>(static_cast<T*>(p) + o) = pack8(v);
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<T*>(p) + o) = v[0];
+    *reinterpret_cast<f32x4*>(static_cast<T*>(p) + o + 4) = v[1];
+  }
+}
+template <typename T> struct Res8 { u32x4 r; };           // eight values as they are stored
+template <> struct Res8<float> { f32x4 r[2]; };
+__device__ __forceinline__ void load_res(const void* p, size_t o, Res8<bf16_t>& r) {
+  r.r = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(p) + o);
+}
+__device__ __forceinline__ void load_res(const void* p, size_t o, Res8<float>& r) {
+  r.r[0] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + o);
+  r.r[1] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + o + 4);
+}
+__device__ __forceinline__ void add_res(f32x4 (&v)[2], const Res8<bf16_t>& r) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j >> 1][2 * (j & 1)] += __uint_as_float(r.r[j] << 16);
+    v[j >> 1][2 * (j & 1) + 1] += __uint_as_float(r.r[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void add_res(f32x4 (&v)[2], const Res8<float>& r) {
+  v[0] += r.r[0];
+  v[1] += r.r[1];
+}
+
 // the epilogue of eight neighbouring columns: element o of the outputs, b their bias, r the residual's
 // values (read by the caller, before)
-__device__ __forceinline__ void finish8(const Args& a, size_t o, f32x4 (&v)[2], const f32x4 (&b)[2], const u32x4& r) {
+template <typename T>
+__device__ __forceinline__ void finish8(const Args& a, size_t o, f32x4 (&v)[2], const f32x4 (&b)[2],
+                                        const Res8<T>& r) {
   v[0] += b[0];
   v[1] += b[1];
-  if (a.z) *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.z) + o) = pack8(v);
+  if (a.z) store8<T>(a.z, o, v);
   act_fwd8(v, a.act);
-  if (a.res) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j >> 1][2 * (j & 1)] += __uint_as_float(r[j] << 16);
-      v[j >> 1][2 * (j & 1) + 1] += __uint_as_float(r[j] & 0xFFFF0000u);
-    }
-  }
-  *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.out) + o) = pack8(v);
+  if (a.res) add_res(v, r);
+  store8<T>(a.out, o, v);
 }
 // One operand's loads: R rows (K-contiguous) or R columns (K-strided) of a 64-wide k-step, as R / 8
 // kilobytes; instruction q of wavefront w fills kilobyte w + NW q, lane L its bytes 16 L .. 16 L + 15.
@@ -132,8 +167,8 @@ struct Op {
   static constexpr int KQ = KC ? 0 : 512 * NW / R;  // and how much further each instruction's is
 
   // rows or columns x0 .. x0 + R - 1 of X; ld: row length in elements
-  __device__ __forceinline__ void setup(const void* p, int X, int K, int x0, int w, int L) {
-    r = sgpr4(dmadesc(p, (long long)X * K * 2));
+  __device__ __forceinline__ void setup(const void* p, int X, int K, int planes, int x0, int w, int L) {
+    r = sgpr4(dmadesc(p, (long long)planes * X * K * 2));
 #pragma unroll
     for (int q = 0; q < NI; ++q) {
       const int b = w + NW * q;
@@ -151,13 +186,13 @@ struct Op {
       }
     }
   }
-  // Load instruction q of the step at k0 into the stage area at LDS address m; k >= kend (at most K)
-  // is masked per lane (K is a multiple of 8 where a chunk runs along k).  The uniform advance stays
-  // below 2^31, so a masked lane's offset is past the descriptor's range with and without it.
-  __device__ __forceinline__ void issue(int q, uint32_t m, int X, int k0, int kend, int w) const {
-    const uint32_t kk = (uint32_t)min(k0, kend);
-    dma16(r, m + (uint32_t)(w + NW * q) * 1024u, k0 + kl + KQ * q < kend ? v[q] : OOB,
-          (uint32_t)ufl((int)(KC ? kk * 2u : kk * (uint32_t)X * 2u)));
+  // Load instruction q of the step at k0 of the plane at byte offset `plane` into the stage area at
+  // LDS address m; k >= klim (K; 0 for a step past the last) is masked per lane (K is a multiple of 8
+  // where a chunk runs along k).  The uniform advance stays below 2^31, so a masked lane's offset is
+  // past the descriptor's range with and without it.
+  __device__ __forceinline__ void issue(int q, uint32_t m, int X, int k0, int klim, uint32_t plane, int w) const {
+    const uint32_t adv = plane + (KC ? (uint32_t)k0 * 2u : (uint32_t)k0 * (uint32_t)X * 2u);
+    dma16(r, m + (uint32_t)(w + NW * q) * 1024u, k0 + kl + KQ * q < klim ? v[q] : OOB, (uint32_t)ufl((int)adv));
   }
 };
 
@@ -192,7 +227,7 @@ struct Frag {
 enum Epi { FWD = 0, PLAIN = 1, PART = 2 };
 
 // A BM x BN tile by WM x WN wavefronts, each (BM / WM) x (BN / WN) in 16 x 16 blocks.
-template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, int EPI>
+template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, int EPI, bool F32>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
   constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;
   constexpr int OPA = BM * 128, STG = OPA + BN * 128;
@@ -210,25 +245,41 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
   const int s = t / nT, tt = t - s * nT;
   const int gsz = 8 * a.nN, gr = tt / gsz, gm = min(8, a.nM - 8 * gr), in = tt - gr * gsz;
   const int m0 = (8 * gr + in % gm) * BM, n0 = (in / gm) * BN;
-  const int steps = (a.K + BK - 1) / BK;
-  const int k_lo = (int)((long long)steps * s / a.S), nk = (int)((long long)steps * (s + 1) / a.S) - k_lo;
+  constexpr int TERMS = F32 ? 6 : 1, PLANES = F32 ? 3 : 1;
+  const int steps = (a.K + BK - 1) / BK;  // of one term
+  const int k_lo = (int)((long long)TERMS * steps * s / a.S);
+  const int nk = (int)((long long)TERMS * steps * (s + 1) / a.S) - k_lo;
 
   Op<BM, NW, AKC> oa;
   Op<BN, NW, BKC> ob;
-  oa.setup(a.A, a.M, a.K, m0, w, L);
-  ob.setup(a.B, a.N, a.K, n0, w, L);
+  oa.setup(a.A, a.M, a.K, PLANES, m0, w, L);
+  ob.setup(a.B, a.N, a.K, PLANES, n0, w, L);
   Frag<BM, AKC> fra;
   Frag<BN, BKC> frb;
   fra.init(L);
   frb.init(L);
   const uint32_t ring = lds_addr(s_ring);
-  const int kend = min(a.K, (k_lo + nk) * BK);
   constexpr int NIA = Op<BM, NW, AKC>::NI, NI = NIA + Op<BN, NW, BKC>::NI;
-  // load instruction q of step kt into stage st (a step past the last one is all masked)
-  auto issue = [&](int q, int kt, int st) __attribute__((always_inline)) {
+  // the next step to load: its number, k and term (all wavefront-uniform)
+  int lc = 0, lt = F32 ? k_lo / steps : 0, lk = (k_lo - lt * steps) * BK;
+  const uint32_t planeA = (uint32_t)a.M * (uint32_t)a.K * 2u, planeB = (uint32_t)a.N * (uint32_t)a.K * 2u;
+  // its load instruction q into stage st (a step past the last one is all masked)
+  auto issue = [&](int q, int st) __attribute__((always_inline)) {
     const uint32_t m = ring + (uint32_t)st * STG;
-    if (q < NIA) oa.issue(q, m, a.M, (k_lo + kt) * BK, kend, w);
-    else ob.issue(q - NIA, m + OPA, a.N, (k_lo + kt) * BK, kend, w);
+    const bool live = lc < nk;
+    const int k0 = live ? lk : 0, klim = live ? a.K : 0;
+    uint32_t pa = 0u, pb = 0u;
+    if constexpr (F32) {  // digits of the terms' parts, A: 0 0 1 1 0 2, B: 0 1 0 1 2 0
+      pa = live ? ((0x201100u >> (4 * lt)) & 3u) * planeA : 0u;
+      pb = live ? ((0x021010u >> (4 * lt)) & 3u) * planeB : 0u;
+    }
+    if (q < NIA) oa.issue(q, m, a.M, k0, klim, pa, w);
+    else ob.issue(q - NIA, m + OPA, a.N, k0, klim, pb, w);
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
+    ++lc;
+    lk += BK;
+    if (F32 && lk >= a.K) lk = 0, ++lt;
   };
   auto frag_a = [&](int i, int st, int sub) __attribute__((always_inline)) {
     return fra.get(s_ring + st * STG, wm * (BM / WM) + 16 * i, sub);
@@ -251,9 +302,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
   // still be in flight).
   bf16x8 fa[MB], fb[2][NB];
 #pragma unroll
-  for (int g = 0; g < NST; ++g)
+  for (int g = 0; g < NST; ++g) {
 #pragma unroll
-    for (int q = 0; q < NI; ++q) issue(q, g, g);
+    for (int q = 0; q < NI; ++q) issue(q, g);
+    advance();
+  }
   vm_wait_barrier<(NST - 1) * NI>();
 #pragma unroll
   for (int j = 0; j < NB; ++j) fb[0][j] = frag_b(j, 0, 0);
@@ -285,7 +338,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
       for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[1][j], fa[i], acc[i][j]);
       if (i >= BR) {
 #pragma unroll
-        for (int q = (i - BR) * LP; q < (i - BR + 1) * LP && q < NI; ++q) issue(q, kt + NST, st);
+        for (int q = (i - BR) * LP; q < (i - BR + 1) * LP && q < NI; ++q) issue(q, st);
         // B's fragments first, then A's in order, each after its row block's MFMAs (past the last
         // step they are read and never used)
 #pragma unroll
@@ -297,32 +350,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
       __builtin_amdgcn_sched_barrier(0);
     }
     st3 = sn;
+    advance();
   }
   vm_drain();  // (the masked loads past the last step write zeros into the ring)
   lds_barrier();  // the ring is free: it stages the epilogue
 
   // acc[i][j][v] = C[wm.. + 16 i + (L & 15)][wn.. + 16 j + 4 (L >> 4) + v]; through LDS a lane gets
   // columns 8 (L & 7) .. + 7 of row 8 p + (L >> 3), so eight lanes cover a row's 128-byte line.  The
-  // residual of the whole 64-column strip is in flight before the first block needs it.
+  // residual of the whole 64-column strip is in flight before the first block needs it (bf16; in fp32
+  // it would take twice the registers, and is read block by block).
+  typedef typename std::conditional<F32, float, bf16_t>::type T;
   char* sg = s_ring + w * 4096;
 #pragma unroll
   for (int h = 0; h < NB / 4; ++h) {
     const int n = n0 + wn * (BN / WN) + 64 * h + 8 * (L & 7), mr = m0 + wm * (BM / WM) + (L >> 3);
-    u32x4 res[MB][2];
+    Res8<T> res[F32 ? 1 : MB][2];
     f32x4 bv[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     if constexpr (EPI == FWD) {
       if (a.bias && n < a.N) {
         bv[0] = *reinterpret_cast<const f32x4*>(a.bias + n);
         bv[1] = *reinterpret_cast<const f32x4*>(a.bias + n + 4);
       }
-      if (a.res) {
+      if (!F32 && a.res) {
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const int m = mr + 16 * i + 8 * p;
-            if (m < a.M && n < a.N)
-              res[i][p] = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(a.res) + (size_t)m * a.N + n);
+            if (m < a.M && n < a.N) load_res(a.res, (size_t)m * a.N + n, res[F32 ? 0 : i][p]);
           }
       }
     }
@@ -347,9 +402,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
         const size_t o = (size_t)m * a.N + n;
         if (m < a.M && n < a.N) {
           if constexpr (EPI == FWD) {
-            finish8(a, o, v, bv, res[i][p]);
+            if (F32 && a.res) load_res(a.res, o, res[0][p]);
+            finish8<T>(a, o, v, bv, res[F32 ? 0 : i][p]);
           } else {
-            *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.out) + o) = pack8(v);
+            store8<T>(a.out, o, v);
           }
         }
       }
@@ -358,16 +414,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
 }
 
 // Split K: the slices' partial sums added in slice order, then the epilogue.
-template <int EPI>
+template <typename T, int EPI>
 __global__ __launch_bounds__(256) void k_linear_sum(Args a) {
   const size_t nv = (size_t)a.M * a.N / 8, slice = (size_t)a.M * a.N;
   const int cpr = a.N / 8;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nv; i += (size_t)gridDim.x * 256) {
     const int n = (int)(i % cpr) * 8;
-    u32x4 r = {0u, 0u, 0u, 0u};
+    Res8<T> r;
     f32x4 b[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     if constexpr (EPI == FWD) {
-      if (a.res) r = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(a.res) + 8 * i);
+      if (a.res) load_res(a.res, 8 * i, r);
       if (a.bias) {
         b[0] = *reinterpret_cast<const f32x4*>(a.bias + n);
         b[1] = *reinterpret_cast<const f32x4*>(a.bias + n + 4);
@@ -380,47 +436,59 @@ __global__ __launch_bounds__(256) void k_linear_sum(Args a) {
       v[0] += *reinterpret_cast<const f32x4*>(p);
       v[1] += *reinterpret_cast<const f32x4*>(p + 4);
     }
-    if constexpr (EPI == FWD) finish8(a, 8 * i, v, b, r);
-    else *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(a.out) + 8 * i) = pack8(v);
+    if constexpr (EPI == FWD) finish8<T>(a, 8 * i, v, b, r);
+    else store8<T>(a.out, 8 * i, v);
   }
 }
 
 // Few tokens (M <= 16 NT): the product is one pass over W, so it streams W straight into registers.
-// A workgroup owns 16 outputs; its KW wavefronts take 64-wide k-steps in turn (each lane 2 x 16 bytes
-// of a W row: a row's 128-byte line), with the 16-token blocks of x as the other operand, and their
-// sums meet in LDS in wavefront order.  U k-steps' loads are in flight.
-template <int NT, int KW, int U>
+// A workgroup owns 16 outputs; its KW wavefronts take k-steps of 128 bytes a W row in turn (lane
+// (g, r) the 16 bytes g and g + 4 of row r), with the 16-token blocks of x as the other operand, and
+// their sums meet in LDS in wavefront order.  U k-steps' loads are in flight.  fp32 runs on the fp32
+// matrix instruction, which takes one k per lane group: the four k of a lane's 16 bytes are four
+// instructions, the same four of both operands.
+template <typename T, int NT, int KW, int U>
 __global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
   __shared__ f32x4 s_sum[KW][NT][64];
+  constexpr int EPC = 16 / (int)sizeof(T), SK = 8 * EPC;  // values of 16 bytes, k of a step
   const int L = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int o0 = blockIdx.x * 16, K = a.K;
   const int r = L & 15, g = L >> 4;
-  const bf16_t* wp = static_cast<const bf16_t*>(a.B) + (size_t)min(o0 + r, a.N - 1) * K;
-  const bf16_t* xp[NT];
+  const T* wp = static_cast<const T*>(a.B) + (size_t)min(o0 + r, a.N - 1) * K;
+  const T* xp[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xp[i] = static_cast<const bf16_t*>(a.A) + (size_t)min(16 * i + r, a.M - 1) * K;
+  for (int i = 0; i < NT; ++i) xp[i] = static_cast<const T*>(a.A) + (size_t)min(16 * i + r, a.M - 1) * K;
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
-  for (int k0 = w * 64; k0 < K; k0 += U * KW * 64) {
-    bf16x8 fw[U][2], fx[U][NT][2];
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  for (int k0 = w * SK; k0 < K; k0 += U * KW * SK) {
+    u32x4 fw[U][2], fx[U][NT][2];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = k0 + u * KW * 64 + 32 * h + 8 * g;
+        const int k = k0 + u * KW * SK + 4 * EPC * h + EPC * g;
         const bool in = k < K;  // K is a multiple of 8
-        fw[u][h] = in ? *reinterpret_cast<const bf16x8*>(wp + k) : zero;
+        fw[u][h] = in ? *reinterpret_cast<const u32x4*>(wp + k) : zero;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) fx[u][i][h] = in ? *reinterpret_cast<const bf16x8*>(xp[i] + k) : zero;
+        for (int i = 0; i < NT; ++i) fx[u][i][h] = in ? *reinterpret_cast<const u32x4*>(xp[i] + k) : zero;
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = mma(fw[u][h], fx[u][i][h], acc[i]);
+        for (int i = 0; i < NT; ++i) {
+          if constexpr (sizeof(T) == 2) {
+            acc[i] = mma(__builtin_bit_cast(bf16x8, fw[u][h]), __builtin_bit_cast(bf16x8, fx[u][i][h]), acc[i]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fw[u][h][j]),
+                                                            __uint_as_float(fx[u][i][h][j]), acc[i], 0, 0, 0);
+          }
+        }
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) s_sum[w][i][L] = acc[i];
@@ -434,8 +502,8 @@ __global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
       const size_t o = (size_t)m * a.N + n;
       f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
       f32x4 b[2] = {v[0], v[0]};
-      u32x4 res = {0u, 0u, 0u, 0u};
-      if (a.res) res = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(a.res) + o);
+      Res8<T> res;
+      if (a.res) load_res(a.res, o, res);
       if (a.bias) {
         b[0] = *reinterpret_cast<const f32x4*>(a.bias + n);
         b[1] = *reinterpret_cast<const f32x4*>(a.bias + n + 4);
@@ -445,7 +513,7 @@ __global__ __launch_bounds__(64 * KW) void k_linear_few(Args a) {
         v[0] += s_sum[q][i][32 * g + r];
         v[1] += s_sum[q][i][32 * g + 16 + r];
       }
-      finish8(a, o, v, b, res);
+      finish8<T>(a, o, v, b, res);
     }
   }
 }
@@ -456,11 +524,46 @@ __device__ __forceinline__ void times_slope(float (&d)[8], const float (&v)[8]) 
   for (int j = 0; j < 8; ++j) d[j] *= act_bwd1<ACT>(v[j]);
 }
 
-// dz = dout act'(z) in bf16 (dz NULL: not written; z NULL: dz is dout) and the column sums of the
-// unrounded dz over this workgroup's rows (part NULL: not wanted).  A workgroup owns 512 columns
-// (64 threads of 8) and the rows g, g + 4 gridDim.y, ... (four at a time).
-__global__ __launch_bounds__(256) void k_linear_dz(const bf16_t* __restrict__ dout, const bf16_t* __restrict__ z, int N,
-                                                   int O, int act, bf16_t* __restrict__ dz, float* __restrict__ part) {
+// eight fp32 values as their three bf16 parts, part p at dst + p plane (elements)
+__device__ __forceinline__ void store_parts(bf16_t* dst, size_t plane, const float (&v)[8]) {
+  float h[8], m[8], l[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[j] = bf16_to_f32(f32_to_bf16(v[j]));
+    const float r = v[j] - h[j];  // exact
+    m[j] = bf16_to_f32(f32_to_bf16(r));
+    l[j] = r - m[j];
+  }
+  auto pk = [](const float (&p)[8]) { return make_uint4(pk2(p[0], p[1]), pk2(p[2], p[3]), pk2(p[4], p[5]), pk2(p[6], p[7])); };
+  *reinterpret_cast<uint4*>(dst) = pk(h);
+  *reinterpret_cast<uint4*>(dst + plane) = pk(m);
+  *reinterpret_cast<uint4*>(dst + 2 * plane) = pk(l);
+}
+__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
+  load4(p, v[0], v[1], v[2], v[3]);
+  load4(p + 4, v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  load4(p, v[0], v[1], v[2], v[3]);
+  load4(p + 4, v[4], v[5], v[6], v[7]);
+}
+
+// src (n values, a multiple of 8) -> its three parts, planes of n values
+__global__ __launch_bounds__(256) void k_linear_split(const float* __restrict__ src, size_t n, bf16_t* __restrict__ dst) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n / 8; i += (size_t)gridDim.x * 256) {
+    float v[8];
+    load8(src + 8 * i, v);
+    store_parts(dst + 8 * i, n, v);
+  }
+}
+
+// dz = dout act'(z) as the products take it: rounded to bf16, or in fp32 its three parts (dz NULL: not
+// written; act NONE: dz is dout), and the column sums of the unrounded dz over this workgroup's rows
+// (part NULL: not wanted).  A workgroup owns 512 columns (64 threads of 8) and the rows g, g + 4
+// gridDim.y, ... (four at a time).
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dout, const T* __restrict__ z, int N, int O,
+                                                   int act, bf16_t* __restrict__ dz, float* __restrict__ part) {
   __shared__ float s[3][64][8];
   const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
   const int col = blockIdx.x * 512 + 8 * c;
@@ -470,17 +573,8 @@ __global__ __launch_bounds__(256) void k_linear_dz(const bf16_t* __restrict__ do
     for (int t = blockIdx.y * 4 + g; t < N; t += 4 * gridDim.y) {
       const size_t o = (size_t)t * O + col;
       float d[8], v[8];
-      const uint4 ud = *reinterpret_cast<const uint4*>(dout + o);
-      uint4 uz = make_uint4(0u, 0u, 0u, 0u);
-      if (z) uz = *reinterpret_cast<const uint4*>(z + o);
-      const uint32_t wd[4] = {ud.x, ud.y, ud.z, ud.w}, wz[4] = {uz.x, uz.y, uz.z, uz.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[2 * j] = __uint_as_float(wd[j] << 16);
-        d[2 * j + 1] = __uint_as_float(wd[j] & 0xFFFF0000u);
-        v[2 * j] = __uint_as_float(wz[j] << 16);
-        v[2 * j + 1] = __uint_as_float(wz[j] & 0xFFFF0000u);
-      }
+      load8(dout + o, d);
+      if (act != NONE) load8(z + o, v);
       switch (act) {
         case RELU: times_slope<RELU>(d, v); break;
         case SILU: times_slope<SILU>(d, v); break;
@@ -490,8 +584,12 @@ __global__ __launch_bounds__(256) void k_linear_dz(const bf16_t* __restrict__ do
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += d[j];
-      if (dz)
-        *reinterpret_cast<uint4*>(dz + o) = make_uint4(pk2(d[0], d[1]), pk2(d[2], d[3]), pk2(d[4], d[5]), pk2(d[6], d[7]));
+      if (dz) {
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint4*>(dz + o) = make_uint4(pk2(d[0], d[1]), pk2(d[2], d[3]), pk2(d[4], d[5]), pk2(d[6], d[7]));
+        else
+          store_parts(dz + o, (size_t)N * O, d);
+      }
     }
   }
   if (!part) return;
@@ -519,8 +617,8 @@ struct Shape { int big, S; };  // big: 2 = 256 x 256, 1 = 128 x 128, 0 = 64 x 64
 // in us.  The constants are fitted to 110 random shapes (65 <= N <= 16384, 64 <= K, O <= 8192) with
 // every tile and slice count timed: the choice is on average 0.7 % slower than the best one
 // measured, at worst 17 %.
-Shape choose(Kind kind, int M, int N, int K) {
-  const int steps = (K + BK - 1) / BK;
+Shape choose(Kind kind, int M, int N, int K, int terms) {
+  const int steps = terms * ((K + BK - 1) / BK);
   struct C { int bm, bn, occ; double fix, lat, thr; };
   const C cs[3] = {kind == K_FWD ? C{64, 64, 3, 3.0, 0.23, 0.26} : C{64, 128, 2, 3.0, 0.32, 0.47},
                    {128, 128, 2, 3.1, 0.75, 0.49}, {256, 256, 1, 6.4, 0.40, 1.20}};
@@ -542,12 +640,12 @@ Shape choose(Kind kind, int M, int N, int K) {
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
-size_t part_bytes(Kind kind, int M, int N, int K) {
-  const Shape c = choose(kind, M, N, K);
+size_t part_bytes(Kind kind, int M, int N, int K, int terms) {
+  const Shape c = choose(kind, M, N, K, terms);
   return c.S > 1 ? up((size_t)c.S * M * N * 4) : 0;
 }
 
-template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC>
+template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, bool F32>
 void launch(Args& a, int S, hipStream_t s) {
   a.nM = (a.M + BM - 1) / BM;
   a.nN = (a.N + BN - 1) / BN;
@@ -556,39 +654,48 @@ void launch(Args& a, int S, hipStream_t s) {
   a.per = (int)((T + 7) / 8);
   const dim3 g((unsigned)(8 * a.per)), b(64 * WM * WN);
   if (S > 1)
-    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, NST, AKC, BKC, PART>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, NST, AKC, BKC, PART, F32>), g, b, 0, s, a);
   else  // (both operands K-contiguous: the forward)
-    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, NST, AKC, BKC, AKC && BKC ? FWD : PLAIN>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_linear<BM, BN, WM, WN, NST, AKC, BKC, AKC && BKC ? FWD : PLAIN, F32>), g, b, 0, s, a);
 }
 
+// the product; bf16 operands, or (T float) three-part planes of them
+template <typename T>
 hipError_t product(Kind kind, Args a, void* ws, hipStream_t s) {
-  const Shape c = choose(kind, a.M, a.N, a.K);
+  constexpr bool F = sizeof(T) == 4;
+  const Shape c = choose(kind, a.M, a.N, a.K, F ? 6 : 1);
   a.part = static_cast<float*>(ws);
   if (kind == K_FWD) {
-    if (c.big == 2) launch<256, 256, 2, 4, 2, true, true>(a, c.S, s);
-    else if (c.big == 1) launch<128, 128, 2, 2, 2, true, true>(a, c.S, s);
-    else launch<64, 64, 4, 1, 3, true, true>(a, c.S, s);
+    if (c.big == 2) launch<256, 256, 2, 4, 2, true, true, F>(a, c.S, s);
+    else if (c.big == 1) launch<128, 128, 2, 2, 2, true, true, F>(a, c.S, s);
+    else launch<64, 64, 4, 1, 3, true, true, F>(a, c.S, s);
   } else if (kind == K_DX) {
-    if (c.big == 2) launch<256, 256, 2, 4, 2, true, false>(a, c.S, s);
-    else if (c.big == 1) launch<128, 128, 2, 2, 2, true, false>(a, c.S, s);
-    else launch<64, 128, 2, 2, 3, true, false>(a, c.S, s);
+    if (c.big == 2) launch<256, 256, 2, 4, 2, true, false, F>(a, c.S, s);
+    else if (c.big == 1) launch<128, 128, 2, 2, 2, true, false, F>(a, c.S, s);
+    else launch<64, 128, 2, 2, 3, true, false, F>(a, c.S, s);
   } else {
-    if (c.big == 2) launch<256, 256, 2, 4, 2, false, false>(a, c.S, s);
-    else launch<128, 128, 2, 2, 2, false, false>(a, c.S, s);
+    if (c.big == 2) launch<256, 256, 2, 4, 2, false, false, F>(a, c.S, s);
+    else launch<128, 128, 2, 2, 2, false, false, F>(a, c.S, s);
   }
   if (c.S > 1) {
-    const size_t nv = (size_t)a.M * a.N / 4;
+    const size_t nv = (size_t)a.M * a.N / 8;
     const unsigned g = (unsigned)((nv + 255) / 256 < 2048 ? (nv + 255) / 256 : 2048);
-    if (kind == K_FWD) hipLaunchKernelGGL(k_linear_sum<FWD>, dim3(g), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(k_linear_sum<PLAIN>, dim3(g), dim3(256), 0, s, a);
+    if (kind == K_FWD) hipLaunchKernelGGL((k_linear_sum<T, FWD>), dim3(g), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_sum<T, PLAIN>), dim3(g), dim3(256), 0, s, a);
   }
   return hipGetLastError();
+}
+
+void split(const void* src, size_t n, bf16_t* dst, hipStream_t s) {
+  const size_t b = (n / 8 + 255) / 256;
+  hipLaunchKernelGGL(k_linear_split, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), 0, s, (const float*)src, n, dst);
 }
 
 // Calls whose W is streamed into registers (k_linear_few) rather than tiled.  Measured, us (few /
 // tiles): K = O = 2048: N = 1 5.5 / 7.8, 16 6.9 / 8.4, 32 8.9 / 8.8; K = O = 4096: N = 1 8.6 / 13.5,
 // 16 11.6 / 10.7, 32 14.6 / 10.9; K = 512, O = 4096: N = 32 4.4 / 5.5.
-bool few_tokens(int N, int K) { return N <= 16 || (N <= 32 && K <= 2048); }
+// (fp32 tiles would first split all of W.)
+bool few_tokens(bool f32, int N, int K) { return N <= 16 || (N <= 32 && (f32 || K <= 2048)); }
 
 // row groups of the dz kernel: one (its column sums are dbias) for few rows
 int dz_groups(int N) { return N <= 64 ? 1 : (N >= 2048 ? 128 : (N + 15) / 16); }
@@ -600,67 +707,116 @@ __global__ __launch_bounds__(256) void k_zero16(uint4* __restrict__ p, size_t n)
 
 }  // namespace ln
 
-size_t linear_fwd_ws_bytes(int N, int K, int O) {
-  return 256 + (ln::few_tokens(N, K) ? 0 : ln::part_bytes(ln::K_FWD, N, O, K));
+size_t linear_fwd_ws_bytes(moe_dtype dt, int N, int K, int O) {
+  using namespace ln;
+  const bool f = dt == MOE_F32;
+  if (few_tokens(f, N, K)) return 256;
+  const size_t planes = f ? up((size_t)N * K * 6) + up((size_t)O * K * 6) : 0;
+  return 256 + planes + part_bytes(K_FWD, N, O, K, f ? 6 : 1);
 }
 
-hipError_t launch_linear_fwd(const void* x, const void* w, const float* bias, int act, const void* res, int N, int K,
-                             int O, void* out, void* z, void* ws, hipStream_t s) {
-  using namespace ln;
-  if (N == 0) return hipSuccess;
-  Args a{};
-  a.A = x; a.B = w; a.M = N; a.N = O; a.K = K;
-  a.out = out; a.z = z; a.bias = bias; a.res = res; a.act = act;
-  if (few_tokens(N, K)) {
-    const dim3 g((unsigned)((O + 15) / 16));
-    if (N <= 16) hipLaunchKernelGGL((k_linear_few<1, 8, 4>), g, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((k_linear_few<2, 8, 2>), g, dim3(512), 0, s, a);
-    return hipGetLastError();
-  }
-  return product(K_FWD, a, ws, s);
-}
+namespace ln {
 
-size_t linear_bwd_ws_bytes(int N, int K, int O) {
-  using namespace ln;
-  const size_t dx = part_bytes(K_DX, N, K, O), dw = part_bytes(K_DW, O, K, N);
-  return 256 + up((size_t)N * O * 2) + up((size_t)dz_groups(N) * O * 4) + (dx > dw ? dx : dw);
-}
-
-hipError_t launch_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int act, int N, int K,
-                             int O, void* dx, void* dw, float* db, void* ws, hipStream_t s) {
-  using namespace ln;
-  if (N == 0) {  // the parameters' gradients are zero (a fill kernel, so that the call can be captured)
-    if (dw) hipLaunchKernelGGL(k_zero16, dim3(1024), dim3(256), 0, s, (uint4*)dw, (size_t)O * K / 8);
-    if (db) hipLaunchKernelGGL(k_zero16, dim3(16), dim3(256), 0, s, (uint4*)db, (size_t)O / 4);
+template <typename T>
+hipError_t fwd(Args a, void* ws, hipStream_t s) {
+  if (few_tokens(sizeof(T) == 4, a.M, a.K)) {
+    const dim3 g((unsigned)((a.N + 15) / 16));
+    if (a.M <= 16) hipLaunchKernelGGL((k_linear_few<T, 1, 8, 4>), g, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_few<T, 2, 8, 2>), g, dim3(512), 0, s, a);
     return hipGetLastError();
   }
   char* p = static_cast<char*>(ws);
+  if constexpr (sizeof(T) == 4) {
+    const size_t nx = (size_t)a.M * a.K, nw = (size_t)a.N * a.K;
+    bf16_t* xp = reinterpret_cast<bf16_t*>(p);
+    bf16_t* wp = reinterpret_cast<bf16_t*>(p + up(nx * 6));
+    p += up(nx * 6) + up(nw * 6);
+    split(a.A, nx, xp, s);
+    split(a.B, nw, wp, s);
+    a.A = xp;
+    a.B = wp;
+  }
+  return product<T>(K_FWD, a, p, s);
+}
+
+// the backward's workspace: dz, the column sums, x's and W's parts (fp32), partial sums
+struct BwdWs {
+  size_t dz, dbp, xp, wp, part;
+  BwdWs(bool f, int N, int K, int O) {
+    const int terms = f ? 6 : 1;
+    dz = up((size_t)N * O * (f ? 6 : 2));
+    dbp = up((size_t)dz_groups(N) * O * 4);
+    xp = f ? up((size_t)N * K * 6) : 0;
+    wp = f ? up((size_t)O * K * 6) : 0;
+    const size_t dx = part_bytes(K_DX, N, K, O, terms), dw = part_bytes(K_DW, O, K, N, terms);
+    part = dx > dw ? dx : dw;
+  }
+  size_t total() const { return 256 + dz + dbp + xp + wp + part; }
+};
+
+template <typename T>
+hipError_t bwd(const T* dout, const T* x, const T* w, const T* z, int act, int N, int K, int O, void* dx, void* dw,
+               float* db, void* ws, hipStream_t s) {
+  constexpr bool F = sizeof(T) == 4;
+  const BwdWs b(F, N, K, O);
+  char* p = static_cast<char*>(ws);
   bf16_t* dz = reinterpret_cast<bf16_t*>(p);
-  p += up((size_t)N * O * 2);
-  float* dbp = reinterpret_cast<float*>(p);
-  p += up((size_t)dz_groups(N) * O * 4);
-  const bool make = act != NONE && (dx || dw);
+  float* dbp = reinterpret_cast<float*>(p + b.dz);
+  bf16_t* xp = reinterpret_cast<bf16_t*>(p + b.dz + b.dbp);
+  bf16_t* wp = reinterpret_cast<bf16_t*>(p + b.dz + b.dbp + b.xp);
+  void* part = p + b.dz + b.dbp + b.xp + b.wp;
+  const bool make = (F || act != NONE) && (dx || dw);  // (bf16 without an activation: dz is dout)
   if (make || db) {
     const int G = dz_groups(N);
-    float* part = db ? (G == 1 ? db : dbp) : nullptr;
-    hipLaunchKernelGGL(k_linear_dz, dim3((O + 511) / 512, G), dim3(256), 0, s, (const bf16_t*)dout,
-                       act != NONE ? (const bf16_t*)z : nullptr, N, O, act, make ? dz : nullptr, part);
+    float* sums = db ? (G == 1 ? db : dbp) : nullptr;
+    hipLaunchKernelGGL(k_linear_dz<T>, dim3((O + 511) / 512, G), dim3(256), 0, s, dout, z, N, O, act,
+                       make ? dz : nullptr, sums);
     if (db && G > 1) launch_sum_rows(dbp, G, O, db, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   Args a{};
-  const void* d = make ? dz : dout;
+  const void* d = make ? static_cast<const void*>(dz) : dout;
   if (dx) {
-    a.A = d; a.B = w; a.M = N; a.N = K; a.K = O; a.out = dx;
-    hipError_t e = product(K_DX, a, p, s);
+    if (F) split(w, (size_t)O * K, wp, s);
+    a.A = d; a.B = F ? static_cast<const void*>(wp) : w; a.M = N; a.N = K; a.K = O; a.out = dx;
+    hipError_t e = product<T>(K_DX, a, part, s);
     if (e != hipSuccess) return e;
   }
   if (dw) {
-    a.A = d; a.B = x; a.M = O; a.N = K; a.K = N; a.out = dw;
-    return product(K_DW, a, p, s);
+    if (F) split(x, (size_t)N * K, xp, s);
+    a.A = d; a.B = F ? static_cast<const void*>(xp) : x; a.M = O; a.N = K; a.K = N; a.out = dw;
+    return product<T>(K_DW, a, part, s);
   }
   return hipSuccess;
+}
+
+}  // namespace ln
+
+hipError_t launch_linear_fwd(moe_dtype dt, const void* x, const void* w, const float* bias, int act, const void* res,
+                             int N, int K, int O, void* out, void* z, void* ws, hipStream_t s) {
+  using namespace ln;
+  if (N == 0) return hipSuccess;
+  Args a{};
+  a.A = x; a.B = w; a.M = N; a.N = O; a.K = K;
+  a.out = out; a.z = z; a.bias = bias; a.res = res; a.act = act;
+  return dt == MOE_F32 ? fwd<float>(a, ws, s) : fwd<bf16_t>(a, ws, s);
+}
+
+size_t linear_bwd_ws_bytes(moe_dtype dt, int N, int K, int O) { return ln::BwdWs(dt == MOE_F32, N, K, O).total(); }
+
+hipError_t launch_linear_bwd(moe_dtype dt, const void* dout, const void* x, const void* w, const void* z, int act,
+                             int N, int K, int O, void* dx, void* dw, float* db, void* ws, hipStream_t s) {
+  using namespace ln;
+  if (N == 0) {  // the parameters' gradients are zero (a fill kernel, so that the call can be captured)
+    const size_t nw = (size_t)O * K / (dt == MOE_F32 ? 4 : 8);
+    if (dw) hipLaunchKernelGGL(k_zero16, dim3(1024), dim3(256), 0, s, (uint4*)dw, nw);
+    if (db) hipLaunchKernelGGL(k_zero16, dim3(16), dim3(256), 0, s, (uint4*)db, (size_t)O / 4);
+    return hipGetLastError();
+  }
+  if (dt == MOE_F32)
+    return bwd((const float*)dout, (const float*)x, (const float*)w, (const float*)z, act, N, K, O, dx, dw, db, ws, s);
+  return bwd((const bf16_t*)dout, (const bf16_t*)x, (const bf16_t*)w, (const bf16_t*)z, act, N, K, O, dx, dw, db, ws, s);
 }
 
 }  // namespace moe

@@ -471,27 +471,31 @@ moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, cons
 
 /*
  * Dense product with bias, activation and residual (the projection in front of the layer, a dense
- * MLP beside the experts), for bf16:
+ * MLP beside the experts):
  *   z[t,o]   = sum_k x[t,k] w[o,k] + bias[o]       (fp32 accumulation; bias fp32 [O] or NULL)
  *   out[t,o] = act(z[t,o]) + res[t,o]              (act: moe_act; res NULL: none)
- * x [N,K], w [O,K] (an nn.Linear weight), res, out, z [N,O], all bf16; z (the rounded z, what the
+ * x [N,K], w [O,K] (an nn.Linear weight), res, out, z [N,O], all of dt; z (as stored, what the
  * backward takes) is written unless NULL.  out may be res (in place), z is neither.  Bias, activation
  * and residual are applied in fp32 and out is rounded once.  K and O are multiples of 8, tensors
- * and workspace 16-byte aligned, and x, w, out each smaller than 2 GiB.  N <= 16 reads w once,
- * straight into registers (a decoding step).
- * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_FWD, MOE_BF16, N, 1, 1, K, O, 0).
+ * and workspace 16-byte aligned, and x, w, out each smaller than 2 GiB (MOE_F32: 2 GiB / 6
+ * elements).  N <= 16 reads w once, straight into registers (a decoding step).
+ * MOE_F32 runs on the bf16 matrix instructions with each operand split exactly into three bf16
+ * parts, as moe_router_logits does (fp32 accuracy; values of magnitude 3.38e38 and above, and
+ * infinities, make their sums NaN), and for few tokens on the fp32 ones.
+ * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_FWD, dt, N, 1, 1, K, O, 0).
  *
  * moe_linear_bwd, given dout = the gradient of out (which is res's gradient as it stands):
  *   dz = dout act'(z)    (z as the forward stored it; NULL for MOE_ACT_NONE)
  *   dx = dz w [N,K],  dw = dz^T x [O,K],  dbias[o] = sum_t dz[t,o] (fp32 [O])      (NULL skips each)
- * dz is rounded to bf16 for its two products; dbias sums it unrounded.  Everything is written
+ * MOE_BF16 rounds dz to bf16 for its two products; dbias sums it unrounded.  Everything is written
  * fresh, in a fixed order (bitwise reproducible); N == 0 sets dw and dbias to zero.
- * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_BWD, MOE_BF16, N, 1, 1, K, O, 0).
+ * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_BWD, dt, N, 1, 1, K, O, 0).
  */
-moe_status moe_linear_fwd(const void* x, const void* w, const float* bias, int32_t act, const void* res, int32_t N,
-                          int32_t K, int32_t O, void* out, void* z, void* ws, size_t ws_bytes, void* stream);
-moe_status moe_linear_bwd(const void* dout, const void* x, const void* w, const void* z, int32_t act, int32_t N,
-                          int32_t K, int32_t O, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+moe_status moe_linear_fwd(moe_dtype dt, const void* x, const void* w, const float* bias, int32_t act, const void* res,
+                          int32_t N, int32_t K, int32_t O, void* out, void* z, void* ws, size_t ws_bytes,
+                          void* stream);
+moe_status moe_linear_bwd(moe_dtype dt, const void* dout, const void* x, const void* w, const void* z, int32_t act,
+                          int32_t N, int32_t K, int32_t O, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
                           void* stream);
 
 /*

@@ -168,16 +168,21 @@ def test_linear_errors(L):
     ptr = lambda k: ctypes.c_void_p(FAKE + 4096 * k)  # noqa: E731
     N, K, O = 100, 64, 72
     for op in (G.OP_LINEAR_FWD, G.OP_LINEAR_BWD):
+        assert L.moe_workspace_bytes(op, G.MOE_F32, N, 1, 1, K, O, 0) > 6 * K * (N + O)   # the operands' parts
+        assert L.moe_workspace_bytes(op, 7, N, 1, 1, K, O, 0) == 0
         assert L.moe_workspace_bytes(op, G.MOE_BF16, N, 1, 1, K, O, 0) > 0
         assert L.moe_workspace_bytes(op, G.MOE_BF16, 0, 1, 1, K, O, 0) > 0
         assert L.moe_workspace_bytes(op, G.MOE_BF16, N, 1, 1, 60, O, 0) == 0
         assert L.moe_workspace_bytes(op, G.MOE_BF16, N, 1, 1, K, 0, 0) == 0
     need = L.moe_workspace_bytes(G.OP_LINEAR_FWD, G.MOE_BF16, N, 1, 1, K, O, 0)
 
-    def fwd(x=ptr(0), w=ptr(1), b=ptr(2), act=0, res=ptr(3), N=N, K=K, O=O, out=ptr(4), z=ptr(5), ws=ptr(6), nb=need):
-        return L.moe_linear_fwd(x, w, b, act, res, N, K, O, out, z, ws, nb, None)
+    def fwd(dt=G.MOE_BF16, x=ptr(0), w=ptr(1), b=ptr(2), act=0, res=ptr(3), N=N, K=K, O=O, out=ptr(4), z=ptr(5), ws=ptr(6), nb=need):
+        return L.moe_linear_fwd(dt, x, w, b, act, res, N, K, O, out, z, ws, nb, None)
     assert fwd(nb=need - 1) == G.MOE_EWORKSPACE
     assert fwd(ws=None) == G.MOE_EINVAL
+    assert fwd(dt=2) == G.MOE_EUNSUPPORTED
+    assert fwd(dt=G.MOE_F32) == G.MOE_EWORKSPACE              # bf16's workspace is too small
+    assert fwd(dt=G.MOE_F32, N=1 << 19, K=1024) == G.MOE_EUNSUPPORTED   # x's parts of more than 2 GiB
     assert fwd(act=5) == G.MOE_EINVAL
     assert fwd(act=-1) == G.MOE_EINVAL
     assert fwd(K=60) == G.MOE_EUNSUPPORTED
@@ -197,9 +202,9 @@ def test_linear_errors(L):
     assert fwd(x=None, out=None, N=0) == G.MOE_OK
     need = L.moe_workspace_bytes(G.OP_LINEAR_BWD, G.MOE_BF16, N, 1, 1, K, O, 0)
 
-    def bwd(d=ptr(0), x=ptr(1), w=ptr(2), z=ptr(3), act=2, N=N, K=K, O=O, dx=ptr(4), dw=ptr(5), db=ptr(6), ws=ptr(7),
+    def bwd(dt=G.MOE_BF16, d=ptr(0), x=ptr(1), w=ptr(2), z=ptr(3), act=2, N=N, K=K, O=O, dx=ptr(4), dw=ptr(5), db=ptr(6), ws=ptr(7),
             nb=need):
-        return L.moe_linear_bwd(d, x, w, z, act, N, K, O, dx, dw, db, ws, nb, None)
+        return L.moe_linear_bwd(dt, d, x, w, z, act, N, K, O, dx, dw, db, ws, nb, None)
     assert bwd(nb=need - 1) == G.MOE_EWORKSPACE
     assert bwd(z=None) == G.MOE_EINVAL
     assert bwd(dx=None, dw=None, db=None) == G.MOE_EINVAL
@@ -219,6 +224,8 @@ def test_linear_bindings():
         G.linear_fwd(x, w, bias=torch.zeros(24), residual=d, act="silu")
     with pytest.raises(TypeError):
         G.linear_fwd(x.float(), w)
+    with pytest.raises(TypeError):
+        G.linear_fwd(x.half(), w.half())
     with pytest.raises(TypeError):
         G.linear_fwd(x, w, bias=torch.zeros(24, dtype=b))
     with pytest.raises(ValueError, match="shape"):

@@ -1,10 +1,12 @@
 """moe_linear_fwd and moe_linear_bwd through the C ABI, every buffer guarded.
 
 Most cases take small whole numbers: every product and sum is then exact in fp32 (K 4 + bias stays
-below 2^24), so the outputs must equal the exact results rounded once to bf16, element for element,
-in every tile shape, slice count and layout.  With random inputs the tolerances follow the
-arithmetic (u = 2^-24, 2^-8 half a step of bf16): a sum of K products in any order is off by at most
-K u sum |x w|; the activations (their slope is at most 1.13) pass that on and add at most 16 u of
+below 2^24), so the outputs must equal the exact results rounded once to their type, element for
+element, in every tile shape, slice count and layout.  With random inputs the tolerances follow the
+arithmetic (u = 2^-24, half: 2^-8 for bf16, u for fp32): a sum of K products in any order is off by at
+most K u sum |x w|, fp32's dropped part products by 4 u sum |x w| more, and as errors of either sign
+mostly cancel, by 2e-6 in the 2-norm for K <= 4096 in fp32 (about 0.6 u sqrt(6 K / 32) of the partial
+sums' size); the activations (their slope is at most 1.13) pass that on and add at most 16 u of
 their own value and argument each; dz is one rounding of at most 2^-8 |dz| on each term of dx and
 dw; dbias sums at most 64 + 64 + 128 values in a row."""
 import numpy as np
@@ -16,8 +18,17 @@ from harness import Guards
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
-H = 2.0 ** -8
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = pytest.mark.parametrize("ty", [BF, F32], ids=["bf16", "f32"])
+
+
+def _half(ty):
+    return torch.finfo(ty).eps / 2
+
+
+def _code(ty):
+    import grouped_gemm_top_amd as G
+    return G.MOE_BF16 if ty == BF else G.MOE_F32
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -32,8 +43,8 @@ def _ints(shape, lo, hi, seed):
     return torch.randint(lo, hi + 1, shape, generator=torch.Generator().manual_seed(seed)).float()
 
 
-def _rand(shape, seed, scale=1.0):
-    return (scale * torch.randn(*shape, generator=torch.Generator().manual_seed(seed))).to(BF)
+def _rand(shape, seed, scale=1.0, ty=BF):
+    return (scale * torch.randn(*shape, generator=torch.Generator().manual_seed(seed))).to(ty)
 
 
 def _up(g, name, t):
@@ -56,45 +67,47 @@ SHAPES = [  # N, K, O
 ]
 
 
+@TYPES
 @pytest.mark.parametrize("act", ["none", "relu"])
 @pytest.mark.parametrize("N,K,O", SHAPES)
-def test_forward_exact(N, K, O, act):
+def test_forward_exact(N, K, O, act, ty):
     import grouped_gemm_top_amd as G
     x, w = _ints((N, K), -2, 2, 1), _ints((O, K), -2, 2, 2)
     b, r = _ints((O,), -50, 50, 3), _ints((N, O), -9, 9, 4)
     g = Guards()
-    dx, dw, db, dr = _up(g, "x", x.to(BF)), _up(g, "w", w.to(BF)), _up(g, "b", b), _up(g, "r", r.to(BF))
-    out, z = g.alloc("out", (N, O), BF), g.alloc("z", (N, O), BF)
-    ws = g.alloc("ws", (G.workspace_bytes(G.OP_LINEAR_FWD, G.MOE_BF16, N, 1, 1, K, O),), torch.uint8)
+    dx, dw, db, dr = _up(g, "x", x.to(ty)), _up(g, "w", w.to(ty)), _up(g, "b", b), _up(g, "r", r.to(ty))
+    out, z = g.alloc("out", (N, O), ty), g.alloc("z", (N, O), ty)
+    ws = g.alloc("ws", (G.workspace_bytes(G.OP_LINEAR_FWD, _code(ty), N, 1, 1, K, O),), torch.uint8)
     G.linear_fwd(dx, dw, bias=db, act=act, residual=dr, out=out, z=z, ws=ws)
     g.check("linear_fwd")
     zr = _mm(x, w.t()) + b
     f = (lambda v: v.clamp(min=0)) if act == "relu" else (lambda v: v)
-    assert torch.equal(z.cpu(), zr.to(BF)) and torch.equal(out.cpu(), (f(zr) + r).to(BF))
+    assert torch.equal(z.cpu(), zr.to(ty)) and torch.equal(out.cpu(), (f(zr) + r).to(ty))
     # no bias, no residual, no z; then in place over the residual
     o2, z2 = G.linear_fwd(dx, dw, act=act)
-    assert z2 is None and torch.equal(o2.cpu(), f(_mm(x, w.t())).to(BF))
+    assert z2 is None and torch.equal(o2.cpu(), f(_mm(x, w.t())).to(ty))
     o3, _ = G.linear_fwd(dx, dw, bias=db, act=act, residual=dr, out=dr, ws=ws)
     g.check("linear_fwd in place")
     assert o3.data_ptr() == dr.data_ptr() and torch.equal(o3, out)
 
 
+@TYPES
 @pytest.mark.parametrize("act", ["none", "relu"])
 @pytest.mark.parametrize("N,K,O", SHAPES)
-def test_backward_exact(N, K, O, act):
+def test_backward_exact(N, K, O, act, ty):
     import grouped_gemm_top_amd as G
     x, w = _ints((N, K), -2, 2, 5), _ints((O, K), -2, 2, 6)
     d, z = _ints((N, O), -3, 3, 7), _ints((N, O), -1, 1, 8)
     g = Guards()
-    D = {n: _up(g, n, t.to(BF)) for n, t in (("d", d), ("x", x), ("w", w), ("z", z))}
-    dx, dw, db = g.alloc("dx", (N, K), BF), g.alloc("dw", (O, K), BF), g.alloc("db", (O,), torch.float32)
-    ws = g.alloc("ws", (G.workspace_bytes(G.OP_LINEAR_BWD, G.MOE_BF16, N, 1, 1, K, O),), torch.uint8)
+    D = {n: _up(g, n, t.to(ty)) for n, t in (("d", d), ("x", x), ("w", w), ("z", z))}
+    dx, dw, db = g.alloc("dx", (N, K), ty), g.alloc("dw", (O, K), ty), g.alloc("db", (O,), torch.float32)
+    ws = g.alloc("ws", (G.workspace_bytes(G.OP_LINEAR_BWD, _code(ty), N, 1, 1, K, O),), torch.uint8)
     zz = D["z"] if act == "relu" else None
     G.linear_bwd(D["d"], D["x"], D["w"], z=zz, act=act, dx=dx, dw=dw, dbias=db, ws=ws)
     g.check("linear_bwd")
     dz = d * (z > 0) if act == "relu" else d
-    assert torch.equal(dx.cpu(), _mm(dz, w).to(BF)), "dx"
-    assert torch.equal(dw.cpu(), _mm(dz.t(), x).to(BF)), "dw"
+    assert torch.equal(dx.cpu(), _mm(dz, w).to(ty)), "dx"
+    assert torch.equal(dw.cpu(), _mm(dz.t(), x).to(ty)), "dw"
     assert torch.equal(db.cpu(), dz.sum(0)), "dbias"
     # each alone
     for n, ref in (("dx", dx), ("dw", dw), ("dbias", db)):
@@ -109,26 +122,34 @@ def _act64(v, act):
             "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh")}[act](v)
 
 
+@TYPES
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
-@pytest.mark.parametrize("N,K,O", [(5, 264, 136), (200, 520, 328), (1030, 256, 1032)])
-def test_forward_activations(N, K, O, act):
+@pytest.mark.parametrize("N,K,O", [(5, 264, 136), (30, 200, 72), (200, 520, 328), (1030, 256, 1032), (300, 4096, 264)])
+def test_forward_activations(N, K, O, act, ty):
     import grouped_gemm_top_amd as G
-    x, w, b, r = _rand((N, K), 9), _rand((O, K), 10, K ** -0.5), _rand((O,), 11).float(), _rand((N, O), 12)
+    x, w, b, r = _rand((N, K), 9, ty=ty), _rand((O, K), 10, K ** -0.5, ty), _rand((O,), 11).float(), \
+        _rand((N, O), 12, ty=ty)
+    H = _half(ty)
     x[0] *= 30  # saturated activations too
     out, z = G.linear_fwd(x.cuda(), w.cuda(), bias=b.cuda(), act=act, residual=r.cuda(), want_z=True)
     z64 = x.double() @ w.double().t() + b.double()
-    ez = K * U * (x.double().abs() @ w.double().abs().t()) + U * z64.abs()
+    ez = (K + 4) * U * (x.double().abs() @ w.double().abs().t()) + U * z64.abs()
     assert bool(((z.cpu().double() - z64).abs() <= ez + H * z64.abs()).all())
+    if ty == F32:
+        assert float((z.cpu().double() - z64).norm()) <= 2e-6 * float(z64.norm())
     ref = _act64(z64, act) + r.double()
     tol = 1.13 * ez + 16 * U * (z64.abs() + 1) + U * ref.abs() + H * ref.abs()
     assert bool(((out.cpu().double() - ref).abs() <= tol).all())
 
 
-@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
-@pytest.mark.parametrize("N,K,O", [(1, 264, 136), (200, 520, 328), (1030, 256, 1032)])
-def test_backward_activations(N, K, O, act):
+@TYPES
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("N,K,O", [(1, 264, 136), (200, 520, 328), (1030, 256, 1032), (3000, 136, 264)])
+def test_backward_activations(N, K, O, act, ty):
     import grouped_gemm_top_amd as G
-    x, w, d, z = _rand((N, K), 13), _rand((O, K), 14, K ** -0.5), _rand((N, O), 15), _rand((N, O), 16, 1.5)
+    x, w, d, z = _rand((N, K), 13, ty=ty), _rand((O, K), 14, K ** -0.5, ty), _rand((N, O), 15, ty=ty), \
+        _rand((N, O), 16, 1.5, ty)
+    H = _half(ty)
     z[0, :4] = torch.tensor([40.0, -40.0, 0.0, 3e4])
     r = G.linear_bwd(d.cuda(), x.cuda(), w.cuda(), z=z.cuda(), act=act)
     z64 = z.double().requires_grad_(True)
@@ -137,10 +158,12 @@ def test_backward_activations(N, K, O, act):
     e = 32 * U * d.double().abs()  # the slope's own error (it is at most 1.13)
     each = H * dz.abs() + e * (1 + H)
     x64, w64 = x.double(), w.double()
-    for n, ref, err, K_ in (("dx", dz @ w64, each @ w64.abs() + O * U * (dz.abs() @ w64.abs()), O),
-                            ("dw", dz.t() @ x64, each.t() @ x64.abs() + N * U * (dz.abs().t() @ x64.abs()), N)):
+    for n, ref, err in (("dx", dz @ w64, each @ w64.abs() + (O + 4) * U * (dz.abs() @ w64.abs())),
+                        ("dw", dz.t() @ x64, each.t() @ x64.abs() + (N + 4) * U * (dz.abs().t() @ x64.abs()))):
         got = r[n].cpu().double()
         assert bool(((got - ref).abs() <= err * 1.01 + H * ref.abs() + 2.0 ** -126).all()), n
+        if ty == F32:  # (and the slopes' few u, of either sign)
+            assert float((got - ref).norm()) <= 2e-6 * float(ref.norm()), n
     tol = e.sum(0) + 256 * U * dz.abs().sum(0)
     assert bool(((r["dbias"].cpu().double() - dz.sum(0)).abs() <= tol).all())
 
@@ -169,11 +192,12 @@ def test_gradient_against_differences():
             assert abs(float((r[n] * e).sum()) - num) <= 0.1 * 2.0 ** -7 * float(terms), n
 
 
-def test_bad_rows_stay_alone():
+@TYPES
+def test_bad_rows_stay_alone(ty):
     """A NaN or infinity in one token's x reaches that token's outputs only, in every path."""
     import grouped_gemm_top_amd as G
     for N, K, O in ((5, 136, 72), (90, 200, 264), (700, 136, 520)):
-        x, w = _rand((N, K), 21), _rand((O, K), 22)
+        x, w = _rand((N, K), 21, ty=ty), _rand((O, K), 22, ty=ty)
         clean, _ = G.linear_fwd(x.cuda(), w.cuda())
         x[2, K - 1] = float("nan")
         x[4, 0] = float("inf")
@@ -182,22 +206,24 @@ def test_bad_rows_stay_alone():
         assert torch.equal(got[keep], clean[keep]) and bool(got[2].isnan().all())
 
 
-def test_empty_input():
+@TYPES
+def test_empty_input(ty):
     import grouped_gemm_top_amd as G
-    x, w = torch.empty((0, 64), dtype=BF, device="cuda"), _rand((24, 64), 23).cuda()
+    x, w = torch.empty((0, 64), dtype=ty, device="cuda"), _rand((24, 64), 23, ty=ty).cuda()
     out, z = G.linear_fwd(x, w, want_z=True)
     assert out.shape == (0, 24) and z.shape == (0, 24)
-    dw, db = torch.full((24, 64), 7.0, dtype=BF, device="cuda"), torch.full((24,), 7.0, device="cuda")
+    dw, db = torch.full((24, 64), 7.0, dtype=ty, device="cuda"), torch.full((24,), 7.0, device="cuda")
     r = G.linear_bwd(out, x, w, dw=dw, dbias=db)
     torch.cuda.synchronize()
     assert r["dx"].shape == (0, 64) and float(dw.abs().max()) == 0.0 and float(db.abs().max()) == 0.0
 
 
+@TYPES
 @pytest.mark.parametrize("N,K,O", [(3, 512, 264), (300, 2880, 512), (2050, 264, 1544)])
-def test_stream_and_graph(N, K, O):
+def test_stream_and_graph(N, K, O, ty):
     import grouped_gemm_top_amd as G
-    x, w, b, d = _rand((N, K), 24).cuda(), _rand((O, K), 25, K ** -0.5).cuda(), _rand((O,), 26).float().cuda(), \
-        _rand((N, O), 27).cuda()
+    x, w, b, d = _rand((N, K), 24, ty=ty).cuda(), _rand((O, K), 25, K ** -0.5, ty).cuda(), \
+        _rand((O,), 26).float().cuda(), _rand((N, O), 27, ty=ty).cuda()
 
     def both(**s):
         out, z = G.linear_fwd(x, w, bias=b, act="gelu_tanh", residual=d, want_z=True, **s)
@@ -215,7 +241,7 @@ def test_stream_and_graph(N, K, O):
     with torch.cuda.graph(graph2):
         got2 = both()
     for seed in range(3):
-        x.copy_(_rand((N, K), 60 + seed))
+        x.copy_(_rand((N, K), 60 + seed, ty=ty))
         graph.replay()
         graph2.replay()
         torch.cuda.synchronize()
