@@ -30,8 +30,7 @@ __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
 }
 struct Add { __device__ static __forceinline__ float op(float a, float b) { return a + b; } };
-// (a NaN stays one, unlike with fmaxf)
-struct Max { __device__ static __forceinline__ float op(float a, float b) { return __builtin_elementwise_maximum(a, b); } };
+struct Max { __device__ static __forceinline__ float op(float a, float b) { return fmaxf(a, b); } };
 template <int LP, class O>
 __device__ __forceinline__ float group(float v) {
   if constexpr (LP >= 2) v = O::op(v, dpp<0xB1>(v));    // lane ^ 1
@@ -56,18 +55,9 @@ __device__ __forceinline__ float across(float v) {
   return v;
 }
 
-// e^x for x <= 0 as 2^(x log2 e), the product's rounding error carried as a first-order factor
-// (v_exp_f32 of the rounded product alone would lose about |x| 2^-24; log2 e's own rounding costs
-// |x| 2^-26).  Below -200, at -infinity too, it is 0.  A NaN counts as -200: softmax() adds it
-// back for the whole token.
-__device__ __forceinline__ float exp_neg(float x) {
-  x = fmaxf(x, -200.f);
-  const float c = 1.44269504088896340736f;  // log2 e
-  const float t = x * c;
-  const float e = __builtin_fmaf(x, c, -t);
-  const float r = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(r, e * 0.6931471805599453f, r);
-}
+// e^x for x <= 0, 0 at -infinity.  The rounded product loses |x| 2^-24, which weighs little where it
+// is large: there e^x is small.
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
 // The logits of one token, LP lanes: element (q LP + l) VW + v.  Positions past E hold -inf.
 template <int VW, int LP, int Q>
@@ -87,7 +77,7 @@ __device__ __forceinline__ void load_row(const float* __restrict__ p, int E, int
 
 // z -> e^(z - max) in place; the caller gets 1 / sum and the token's log sum exp (hardware
 // reciprocal and logarithm, one unit in the last place each).  A token whose logits are all -inf has
-// 1 / sum = 0 and lse = 0; one with a NaN or +inf has NaN for both.
+// 1 / sum = 0 and lse = 0; one with a NaN or +inf has NaN for both (some z - max is NaN, so the sum is).
 template <int VW, int LP, int Q>
 __device__ __forceinline__ float2 softmax(float (&z)[Q][VW], const float (&b)[Q][VW]) {
   float m = -__builtin_inff();
@@ -96,7 +86,7 @@ __device__ __forceinline__ float2 softmax(float (&z)[Q][VW], const float (&b)[Q]
 #pragma unroll
     for (int v = 0; v < VW; ++v) {
       z[q][v] += b[q][v];
-      m = __builtin_elementwise_maximum(m, z[q][v]);
+      m = fmaxf(m, z[q][v]);
     }
   m = group<LP, Max>(m);
   m = m == -__builtin_inff() ? 0.f : m;
@@ -109,10 +99,9 @@ __device__ __forceinline__ float2 softmax(float (&z)[Q][VW], const float (&b)[Q]
       s += z[q][v];
     }
   s = group<LP, Add>(s);
-  const float nan = m - m;  // 0, or NaN where m is NaN or infinite
   const bool none = s == 0.f;
-  return make_float2((none ? 0.f : __builtin_amdgcn_rcpf(s)) + nan,
-                     (none ? 0.f : __builtin_fmaf(__builtin_amdgcn_logf(s), 0.6931471805599453f, m)) + nan);
+  return make_float2(none ? 0.f : __builtin_amdgcn_rcpf(s),
+                     none ? 0.f : __builtin_fmaf(__builtin_amdgcn_logf(s), 0.6931471805599453f, m));
 }
 
 // The first sequence b in [0, B) that ends behind token t (ptr[b+1] > t), or B: 64 probes a round.
@@ -529,9 +518,9 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
     else if (E <= 16) F(4, 4, 1); \
     else if (E <= 32) F(4, 8, 1); \
     else if (E <= 64) F(4, 16, 1); \
-    else if (E <= 128) F(4, 32, 1); \
-    else if (E <= 256) F(4, 64, 1); \
-    else if (E <= 512) F(4, 64, 2); \
+    else if (E <= 128) F(4, 16, 2); \
+    else if (E <= 256) F(4, 32, 2); \
+    else if (E <= 512) F(4, 32, 4); \
     else F(4, 64, 4); \
   } else { \
     if (E <= 8) F(1, 8, 1); \

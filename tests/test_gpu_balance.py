@@ -2,11 +2,12 @@
 C ABI, every buffer guarded.
 
 Counts are equal.  Tolerances of the rest, from the arithmetic (u = 2^-24, zm the largest |z|):
-* p: z = logits + bias is off by u zm, which e^z takes as a relative error, numerator and sum; the
+* p: z = logits + bias is off by u zm, which e^z takes as a relative error, numerator and sum; so is
+  x = z - max (at most 2 zm in size) with u |x|, rounded itself and in its product with log2 e; the
   exponential, at most 16 + 6 additions, the reciprocal and the product add less than 40 u:
-  (2 zm + 40) u relative;
+  (4 zm + 40) u relative;
 * loss[0], a sum of positive terms: p's error, then at most 128 additions in a row (tokens of one
-  slot, lane exchanges, slots, experts): (2 zm + 256) u relative;
+  slot, lane exchanges, slots, experts): (4 zm + 168) u relative, below (2 zm + 256) u for zm <= 44;
 * lse = max + log(sum): (zm + 40) u absolute; loss[1] takes it times 2 |lse|, and 256 u for its sum;
 * saved: three divisions and a product from a rounded constant: 8 u relative;
 * dlogits: the two errors above on each of its terms p g, p sum(g p) and p lse, at most 64 u for the
