@@ -59,6 +59,7 @@ __device__ __forceinline__ float act_bwd1(float v) {
     return 0.5f * (1.0f + erff(0.70710678118654752f * v)) +
            v * 0.3989422804014327f * __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (v * v));
   } else if constexpr (ACT == GELU_TANH) {
+    if (fabsf(v) > 16.f) return v > 0.f ? 1.f : 0.f;  // exact there, and v^2 may overflow further out
     const float s = sig_scaled(v * (2.0f * kG * kLog2e + (2.0f * kG * kG3 * kLog2e) * (v * v)));
     return s + v * s * (1.0f - s) * (2.0f * kG + (6.0f * kG * kG3) * (v * v));
   } else {
