@@ -536,20 +536,25 @@ def _first_use():
 def _on_stream(fn):
     """Run a binding on its first tensor's device and, if `stream` is given, with that stream as
     the current one: what the call allocates then belongs to the stream that uses it."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         torch = _torch or _first_use()
+        first = args[0] if args else kw.get(name)
+        if first is None:
+            raise TypeError(f"{fn.__name__}() needs {name}")
         # (a host tensor is refused by the binding)
         if stream is None and (first.get_device() == torch._C._cuda_getDevice() if first.is_cuda else True):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         _on_gpu(first)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
         with torch.cuda.device(first.device):
             if stream is None:
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
     return call
 
 

@@ -242,3 +242,17 @@ def test_linear_bindings():
         G.linear_bwd(d[:3], x, w)
     with pytest.raises(ValueError, match="GPU"):
         G.linear_bwd(d, x, w)
+
+
+def test_bindings_take_every_argument_by_name():
+    """The documented names work for the first argument too (a host tensor reaches the binding's own refusal)."""
+    b, f = torch.bfloat16, torch.float32
+    x, w = torch.zeros(4, 64, dtype=b), torch.zeros(32, 64, dtype=b)
+    lg, ix, sv = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(9, dtype=f)
+    for call in (lambda: G.add_rmsnorm(x=x), lambda: G.add_rmsnorm_bwd(dy=x, h=x), lambda: G.linear_fwd(w=w, x=x),
+                 lambda: G.linear_bwd(dout=torch.zeros(4, 32, dtype=b), x=x, w=w),
+                 lambda: G.balance_loss(logits=lg, topk_idx=ix, alpha=0.1), lambda: G.balance_loss_bwd(logits=lg, saved=sv)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(TypeError):
+        G.linear_fwd()
