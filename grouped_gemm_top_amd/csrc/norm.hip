@@ -382,11 +382,20 @@ size_t add_rmsnorm_bwd_ws_bytes(int N, int H) { return (size_t)nm::bwd_groups(N)
 hipError_t launch_add_rmsnorm(moe_dtype dt, moe_dtype rdt, const void* x, const void* res, const float* w, float eps,
                               int N, int H, void* h, void* y, uint8_t* q, uint8_t* scales, hipStream_t s) {
   if (N == 0) return hipSuccess;
-  const nm::FwdArgs a{x, res, w, h, y, q, scales, N, H, eps};
-  if (dt == MOE_F32) nm::fwd<float, float>(a, s);
-  else if (rdt == MOE_F32) nm::fwd<bf16_t, float>(a, s);
-  else nm::fwd<bf16_t, bf16_t>(a, s);
-  return hipGetLastError();
+  // at most 2^21 rows a launch: 1024 threads a row stay below the 2^32 threads that one may have
+  const long long slab = 1 << 21;
+  const size_t xs = dt == MOE_F32 ? 4 : 2, rs = rdt == MOE_F32 ? 4 : 2, KS = 4 * ((H + 127) / 128);
+  for (long long r0 = 0; r0 < N; r0 += slab) {
+    auto at = [&](auto* p, size_t row_bytes) { return p ? (decltype(p))((uintptr_t)p + r0 * row_bytes) : p; };
+    const nm::FwdArgs a{at(x, H * xs), at(res, H * rs), w, at(h, H * rs), at(y, H * xs), at(q, H), at(scales, KS),
+                        N - r0 < slab ? N - r0 : slab, H, eps};
+    if (dt == MOE_F32) nm::fwd<float, float>(a, s);
+    else if (rdt == MOE_F32) nm::fwd<bf16_t, float>(a, s);
+    else nm::fwd<bf16_t, bf16_t>(a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, const void* h, const void* dh_in,

@@ -281,3 +281,23 @@ def test_offsets_past_32_bits():
     terms = h64 * h64 * rr
     # (rows of zeros add nothing, but the tail's rows may meet in one workgroup's sum)
     _check_close(b["dw"], terms.sum(0), 128 * U * terms.abs().sum(0), "dw")
+
+
+@pytest.mark.parametrize("N,H,quant", [((1 << 21) + 3, 32, True), ((1 << 22) + 1, 8, False), ((1 << 26) + 5, 8, False)])
+def test_more_rows_than_one_launch_takes(N, H, quant):
+    """Rows are independent: the rows around 2^21, 2^22 and at the end equal those of a call of their own."""
+    import torch
+    import grouped_gemm_top_amd as G
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(N, H, device="cuda", generator=gen, dtype=torch.bfloat16)
+    w = torch.rand(H, device="cuda", generator=gen) + 0.5
+    r = G.add_rmsnorm(x, w, residual=x, want_h=quant, quantize=quant)
+    for lo in (0, (1 << 21) - 5, (1 << 22) - 5, N - 9):
+        hi = min(N, lo + 9)
+        if lo >= N:
+            continue
+        one = G.add_rmsnorm(x[lo:hi].contiguous(), w, residual=x[lo:hi].contiguous(), want_h=quant, quantize=quant)
+        for key, v in one.items():
+            assert (v is None) == (r[key] is None)
+            if v is not None:
+                assert torch.equal(v, r[key][lo:hi]), (key, lo)
