@@ -422,6 +422,7 @@ struct BwdArgs {
   const float* din;    // NULL: zeros (may be dz)
   float* dz;
   int N, E, B;
+  long long first;  // this launch's first token
 };
 
 template <int VW, int LP, int Q>
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(NT) void k_balance_bwd(BwdArgs a) {
   constexpr int U = Q * VW >= 16 ? 1 : (Q * VW >= 8 ? 2 : 4);
   const int slot = threadIdx.x / LP, l = threadIdx.x % LP;
   const int E = a.E, N = a.N;
-  const long long tb = (long long)blockIdx.x * (SL * U);
+  const long long tb = a.first + (long long)blockIdx.x * (SL * U);
   const int tl = (int)min(tb + SL * U, (long long)N) - 1;  // the workgroup's last token
   float bias[Q][VW];
 #pragma unroll
@@ -594,16 +595,23 @@ hipError_t launch_balance_loss_bwd(const float* logits, const float* bias, const
                                    float* dz, hipStream_t s) {
   using namespace bl;
   if (N == 0) return hipSuccess;
-  const BwdArgs a{logits, bias, mask, ptr, saved, dloss, din, dz, N, E, B};
+  BwdArgs a{logits, bias, mask, ptr, saved, dloss, din, dz, N, E, B, 0};
   const bool vec = E % 4 == 0 && al16(logits) && al16(saved) && al16(din) && al16(dz);
 #define BL_BWD(VW, LP, Q)                                                                                  \
   do {                                                                                                     \
     constexpr int per = (NT / LP) * (Q * VW >= 16 ? 1 : (Q * VW >= 8 ? 2 : 4));                             \
-    hipLaunchKernelGGL((k_balance_bwd<VW, LP, Q>), dim3((unsigned)(((long long)N + per - 1) / per)), dim3(NT), 0, s, a); \
+    hipLaunchKernelGGL((k_balance_bwd<VW, LP, Q>), dim3((unsigned)((n + per - 1) / per)), dim3(NT), 0, s, a); \
   } while (0)
-  BL_SHAPES(vec, E, BL_BWD)
+  // at most 2^22 tokens a launch (a multiple of every `per`): 64 threads a token stay below the 2^32
+  // threads that one may have
+  for (; a.first < N; a.first += 1 << 22) {
+    const long long n = N - a.first < (1 << 22) ? N - a.first : 1 << 22;
+    BL_SHAPES(vec, E, BL_BWD)
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
 #undef BL_BWD
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace moe

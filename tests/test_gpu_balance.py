@@ -290,3 +290,22 @@ def test_router_backward_takes_the_gradient():
     c = G.router_bwd(lg, idx, plan, ds, x, wr, bias=bias, dlogits_in=mine, dlogits=mine)
     torch.cuda.synchronize()
     assert all(torch.equal(b[n], c[n]) for n in b)
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (9, 1)])
+def test_gradient_of_more_tokens_than_one_launch_takes(E, k):
+    """With `saved` given a token's gradient depends on its own row and sequence alone: the rows around
+    2^22 and at the end equal those of a call with these tokens only."""
+    import grouped_gemm_top_amd as G
+    N = (1 << 22) + 37
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    lg = torch.randn(N, E, device="cuda", generator=gen)
+    mask = (torch.rand(N, device="cuda", generator=gen) > 0.2).to(torch.uint8)
+    ptr = torch.tensor([3, 1000, 1 << 21, (1 << 22) - 7, (1 << 22) + 11, N - 2], dtype=torch.int32, device="cuda")
+    saved = torch.rand(5 * E + 1, device="cuda", generator=gen)
+    dz = G.balance_loss_bwd(lg, saved, mask=mask, seq_ptr=ptr)
+    for lo in (0, (1 << 22) - 40, N - 30):
+        hi = min(N, lo + 70)
+        sub = (ptr - lo).clamp(0, hi - lo).int()
+        one = G.balance_loss_bwd(lg[lo:hi].clone(), saved, mask=mask[lo:hi].clone(), seq_ptr=sub)
+        assert torch.equal(one, dz[lo:hi]), lo
