@@ -68,8 +68,11 @@ moe_status check_plan(const moe_plan* p) {
 
 constexpr int32_t kMaxSeqs = 1 << 20;
 
-moe_status check_seqs(int32_t B, const int32_t* seq_ptr) {
+// (1024 threads per sequence and 64 experts: a launch takes fewer than 2^32)
+moe_status check_seqs(int32_t B, int32_t E, const int32_t* seq_ptr) {
   REQUIRE(B >= 1 && B <= kMaxSeqs, MOE_EINVAL, "B must be in [1, %d] (got %d)", kMaxSeqs, B);
+  REQUIRE((int64_t)B * ((E + 63) / 64) < 1 << 22, MOE_EUNSUPPORTED, "B * ceil(E / 64) must be below 2^22 (got B=%d, E=%d)",
+          B, E);
   REQUIRE(seq_ptr || B == 1, MOE_EINVAL, "B > 1 needs seq_ptr");
   return MOE_OK;
 }
@@ -204,7 +207,7 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
       if (H < 32 || I < 32 || H % 32 || I % 32 || M_cap < 0) return 0;
       return moe::layer_bwd_mxfp8_ws_bytes(N, M_cap, H, I);
     case MOE_OP_BALANCE_LOSS:  // I: the sequences
-      if (I < 1 || I > kMaxSeqs) return 0;
+      if (check_seqs(I, E, &I) != MOE_OK) return 0;
       return moe::balance_loss_ws_bytes(N, E, I);
     case MOE_OP_LINEAR_FWD:
       if (check_linear(dt, N, H, I) != MOE_OK) return 0;
@@ -582,7 +585,7 @@ moe_status moe_balance_loss(const float* logits, const float* bias, const int32_
   g_err[0] = 0;
   moe_status st = check_dims(N, E, k);
   if (st != MOE_OK) return st;
-  if ((st = check_seqs(B, seq_ptr)) != MOE_OK) return st;
+  if ((st = check_seqs(B, E, seq_ptr)) != MOE_OK) return st;
   REQUIRE(alpha - alpha == 0.f && beta - beta == 0.f, MOE_EINVAL, "alpha and beta must be finite");
   REQUIRE(N == 0 || (logits && topk_idx), MOE_EINVAL, "NULL logits/topk_idx");
   REQUIRE(loss && counts && saved, MOE_EINVAL, "NULL loss/counts/saved");
@@ -603,7 +606,7 @@ moe_status moe_balance_loss_bwd(const float* logits, const float* bias, const ui
   g_err[0] = 0;
   moe_status st = check_dims(N, E, 1);
   if (st != MOE_OK) return st;
-  if ((st = check_seqs(B, seq_ptr)) != MOE_OK) return st;
+  if ((st = check_seqs(B, E, seq_ptr)) != MOE_OK) return st;
   REQUIRE(N == 0 || (logits && saved && dlogits), MOE_EINVAL, "NULL logits/saved/dlogits");
   REQUIRE(N == 0 || (dlogits != logits && dlogits != saved), MOE_EINVAL, "dlogits must not be logits or saved");
   moe::kernel_event(MOE_K_BALANCE_BWD, 0, (hipStream_t)stream);

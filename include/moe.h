@@ -411,7 +411,7 @@ moe_status moe_router_bwd(moe_dtype dt, const float* logits, const float* bias, 
  *                                  + dloss[1] saved[B*E] lse_t p_m
  * (dlogits_in NULL: zeros; tokens that take no part get dlogits_in; dlogits may be dlogits_in).
  * moe_router_bwd_acc takes the result on.  logits, dlogits fp32 [N,E]; counts int32 [B,E].
- * 1 <= E <= 1024, 1 <= k <= E, 1 <= B <= 2^20.  Everything is summed in fp32 in a fixed order (bitwise
+ * 1 <= E <= 1024, 1 <= k <= E, 1 <= B <= 2^20, B ceil(E / 64) < 2^22.  Everything is summed in fp32 in a fixed order (bitwise
  * reproducible).  A seq_ptr that does not ascend gives wrong sums but touches no other memory.
  * Workspace of moe_balance_loss: moe_workspace_bytes(MOE_OP_BALANCE_LOSS, MOE_F32, N, E, k, 0, B, 0).
  */

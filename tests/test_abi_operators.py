@@ -256,3 +256,13 @@ def test_bindings_take_every_argument_by_name():
             call()
     with pytest.raises(TypeError):
         G.linear_fwd()
+
+
+def test_balance_loss_sequences_times_experts(L):
+    """B ceil(E / 64) workgroups of 1024 threads are one launch: refused from 2^32 threads on."""
+    big = 1 << 20
+    ok = L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 64, 192, 2, 0, big, 0)
+    assert ok > 0
+    assert L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 64, 193, 2, 0, big, 0) == 0
+    assert L.moe_balance_loss(F, None, F, None, F, big, 64, 256, 2, 0.1, 0.1, F, F, F, F, 1 << 62, None) == G.MOE_EUNSUPPORTED
+    assert L.moe_balance_loss_bwd(F, None, None, F, big, 64, 256, F, None, None, F, None) == G.MOE_EUNSUPPORTED
