@@ -119,6 +119,8 @@ moe_status check_linear(moe_dtype dt, int32_t N, int32_t K, int32_t O) {
   REQUIRE(N >= 0, MOE_EINVAL, "N must be >= 0 (got %d)", N);
   REQUIRE(K >= 8 && O >= 8, MOE_EINVAL, "K and O must be >= 8 (got K=%d, O=%d)", K, O);
   REQUIRE(K % 8 == 0 && O % 8 == 0, MOE_EUNSUPPORTED, "K and O must be multiples of 8 (got K=%d, O=%d)", K, O);
+  // (512 threads per 16 outputs, 1024 per 32 columns of dbias: a launch takes fewer than 2^32)
+  REQUIRE(O <= 1 << 26, MOE_EUNSUPPORTED, "O must be at most 2^26 (got %d)", O);
   const int64_t es = dt == MOE_F32 ? 6 : 2;
   REQUIRE((int64_t)N * K * es <= kDescBytes && (int64_t)N * O * es <= kDescBytes && (int64_t)O * K * es <= kDescBytes,
           MOE_EUNSUPPORTED, "x [N=%d, K=%d], w [O=%d, K] and out [N, O] must each be < 2 GiB (bf16; fp32: a third of it "

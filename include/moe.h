@@ -477,8 +477,8 @@ moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, cons
  * x [N,K], w [O,K] (an nn.Linear weight), res, out, z [N,O], all of dt; z (as stored, what the
  * backward takes) is written unless NULL.  out may be res (in place), z is neither.  Bias, activation
  * and residual are applied in fp32 and out is rounded once.  K and O are multiples of 8, tensors
- * and workspace 16-byte aligned, and x, w, out each smaller than 2 GiB (MOE_F32: 2 GiB / 6
- * elements).  N <= 16 reads w once, straight into registers (a decoding step).
+ * and workspace 16-byte aligned, x, w, out each smaller than 2 GiB (MOE_F32: 2 GiB / 6
+ * elements) and O at most 2^26.  N <= 16 reads w once, straight into registers (a decoding step).
  * MOE_F32 runs on the bf16 matrix instructions with each operand split exactly into three bf16
  * parts, as moe_router_logits does (fp32 accuracy; values of magnitude 3.38e38 and above, and
  * infinities, make their sums NaN), and for few tokens on the fp32 ones.

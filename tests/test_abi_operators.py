@@ -266,3 +266,12 @@ def test_balance_loss_sequences_times_experts(L):
     assert L.moe_workspace_bytes(G.OP_BALANCE_LOSS, G.MOE_F32, 64, 193, 2, 0, big, 0) == 0
     assert L.moe_balance_loss(F, None, F, None, F, big, 64, 256, 2, 0.1, 0.1, F, F, F, F, 1 << 62, None) == G.MOE_EUNSUPPORTED
     assert L.moe_balance_loss_bwd(F, None, None, F, big, 64, 256, F, None, None, F, None) == G.MOE_EUNSUPPORTED
+
+
+def test_linear_widest_output(L):
+    """ceil(O / 16) workgroups of 512 threads are one launch: an O near 2^27 is refused, for both directions."""
+    for op in (G.OP_LINEAR_FWD, G.OP_LINEAR_BWD):
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, 1, 1, 1, 8, 1 << 26, 0) > 0
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, 1, 1, 1, 8, (1 << 27) - 8, 0) == 0
+    assert L.moe_linear_fwd(G.MOE_BF16, F, F, None, 0, None, 1, 8, (1 << 27) - 8, ctypes.c_void_p(FAKE + 4096), None, F,
+                            1 << 62, None) == G.MOE_EUNSUPPORTED
