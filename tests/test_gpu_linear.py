@@ -248,3 +248,20 @@ def test_stream_and_graph(N, K, O, ty):
         eager = both()
         torch.cuda.synchronize()
         assert all(torch.equal(eager[n], got[n]) and torch.equal(eager[n], got2[n]) for n in eager)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slope_far_from_zero(act, dt):
+    """Far out the slope is 1 or 0, also where z^2 or z^3 overflow fp32: dbias is the sum of dout or 0, exactly
+    (small integers; silu's slope is within e^-100 of its limit from |z| = 128 on)."""
+    import grouped_gemm_top_amd as G
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[dt]
+    z = torch.tensor([128.0, -128.0, 1e6, -1e6, 1e20, -1e20, 3e38, -3e38], dtype=t, device="cuda").repeat(5, 1)
+    dout = torch.arange(1, 41, device="cuda").reshape(5, 8).to(t)
+    x, w = torch.ones(5, 8, dtype=t, device="cuda"), torch.eye(8, dtype=t, device="cuda")
+    r = G.linear_bwd(dout, x, w, z, act=act)
+    want = dout.float() * (z > 0)
+    assert torch.equal(r["dbias"], want.sum(0))
+    assert torch.equal(r["dx"].float(), want)
+    assert torch.equal(r["dw"].float(), want.sum(0)[:, None].expand(8, 8))
