@@ -51,11 +51,41 @@ __device__ __forceinline__ float sig_scaled(float t) {
 constexpr float kLog2e = 1.44269504088896340736f;
 // gelu_tanh: (1 + tanh u) / 2 = sigmoid(2u), u = kG (v + kG3 v^3), kG = sqrt(2 / pi)
 constexpr float kG = 0.7978845608028654f, kG3 = 0.044715f;
+// gelu: Phi(v) = (1 + erf(v / sqrt 2)) / 2, with e = e^(-v^2 / 2), which the slope takes as well.
+// 1 + erf would cancel for v < 0 (no digit left at v = -5.5), so the smaller tail is computed itself:
+//   |v| < 1:  Phi = 1/2 + v Q(v^2)
+//   else:     Phi(-|v|) = e w P(w), w = 1 / (1 + 0.4 |v|);  Phi(|v|) = 1 - Phi(-|v|)
+// P and Q are least-maximum fits of relative error 2^-27 and below (P on 1 <= |v| <= 13.4, past which e is 0
+// in fp32).  Relative error: 5 units of 2^-24 and, of e, what v^2 / 2 loses in its roundings, 1.5 v^2
+// units.  8192 x 4096 x 4096 with its full epilogue: 247 us (253 with erff; without an activation 236).
+struct Gauss { float cdf, e; };
+__device__ __forceinline__ Gauss gauss(float v) {
+  const float a = fabsf(v), s = v * v;
+  const float e = __builtin_amdgcn_exp2f((-0.5f * kLog2e) * s);
+  const float w = __builtin_amdgcn_rcpf(__builtin_fmaf(0.4f, a, 1.0f));
+  float p = -0.056554921f;
+  p = __builtin_fmaf(p, w, 0.189746842f);
+  p = __builtin_fmaf(p, w, -0.201070011f);
+  p = __builtin_fmaf(p, w, 0.0237784851f);
+  p = __builtin_fmaf(p, w, 0.00688937446f);
+  p = __builtin_fmaf(p, w, 0.0837814957f);
+  p = __builtin_fmaf(p, w, 0.134175435f);
+  p = __builtin_fmaf(p, w, 0.159548461f);
+  p = __builtin_fmaf(p, w, 0.159578457f);
+  const float t = p * w * e;
+  float q = -7.65420828e-06f;
+  q = __builtin_fmaf(q, s, 0.000113486371f);
+  q = __builtin_fmaf(q, s, -0.00118632999f);
+  q = __builtin_fmaf(q, s, 0.00997332297f);
+  q = __builtin_fmaf(q, s, -0.0664903596f);
+  q = __builtin_fmaf(q, s, 0.398942292f);
+  return Gauss{a < 1.0f ? __builtin_fmaf(v, q, 0.5f) : (v < 0.f ? t : 1.0f - t), e};
+}
 template <int ACT>
 __device__ __forceinline__ float act_fwd1(float v) {
   if constexpr (ACT == RELU) return v > 0.f ? v : (v != v ? v : 0.f);
   else if constexpr (ACT == SILU) return v * sig_scaled(kLog2e * v);
-  else if constexpr (ACT == GELU) return 0.5f * v * (1.0f + erff(0.70710678118654752f * v));
+  else if constexpr (ACT == GELU) return v * gauss(v).cdf;
   else if constexpr (ACT == GELU_TANH)
     return v * sig_scaled(v * (2.0f * kG * kLog2e + (2.0f * kG * kG3 * kLog2e) * (v * v)));
   else return v;
@@ -68,8 +98,8 @@ __device__ __forceinline__ float act_bwd1(float v) {
     const float s = sig_scaled(kLog2e * v);
     return s * (1.0f + v * (1.0f - s));
   } else if constexpr (ACT == GELU) {
-    return 0.5f * (1.0f + erff(0.70710678118654752f * v)) +
-           v * 0.3989422804014327f * __builtin_amdgcn_exp2f((-0.5f * kLog2e) * (v * v));
+    const Gauss g = gauss(v);
+    return g.cdf + v * 0.3989422804014327f * g.e;
   } else if constexpr (ACT == GELU_TANH) {
     if (fabsf(v) > 16.f) return v > 0.f ? 1.f : 0.f;  // exact there, and v^2 may overflow further out
     const float s = sig_scaled(v * (2.0f * kG * kLog2e + (2.0f * kG * kG3 * kLog2e) * (v * v)));

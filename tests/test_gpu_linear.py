@@ -265,3 +265,36 @@ def test_slope_far_from_zero(act, dt):
     assert torch.equal(r["dbias"], want.sum(0))
     assert torch.equal(r["dx"].float(), want)
     assert torch.equal(r["dw"].float(), want.sum(0)[:, None].expand(8, 8))
+
+
+@TYPES
+@pytest.mark.parametrize("N", [10, 60])
+def test_gelu_in_its_tail(N, ty):
+    """The erf GELU and its slope keep their relative accuracy down to z = -12.5, where 1 + erf would be
+    a difference of nearly equal numbers (few tokens and tiles).  Phi(z) for z < 0 is e^(-z^2 / 2) times a
+    function of size 1 / |z|: the exponent carries three roundings of z^2 / 2 (the square, the constant, the
+    product), 1.5 z^2 u of the result, the function and the products at most 40 u: (2 z^2 + 40) u of
+    Phi.  The slope's second term z phi(z) has the same exponent and six more operations: (1.5 z^2 + 12) u
+    of it; the sum and the store 2 u.  W is the identity, so z is x exactly."""
+    import grouped_gemm_top_amd as G
+    H = _half(ty)
+    z = torch.linspace(-12.5, 6.0, 8 * N).reshape(N, 8).to(ty)
+    out, zz = G.linear_fwd(z.cuda(), torch.eye(8, dtype=ty, device="cuda"), act="gelu", want_z=True)
+    assert torch.equal(zz.cpu(), z)
+    z64 = z.double()
+    phi_c = 0.5 * torch.special.erfc(-z64 * 0.5 ** 0.5)
+    tol = (2 * z64 ** 2 + 40) * U * (z64 * phi_c).abs() + H * (z64 * phi_c).abs() + 2.0 ** -125
+    err = (out.cpu().double() - z64 * phi_c).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    # the slope: dbias of one row of ones
+    zr = z.reshape(1, -1)
+    O = zr.shape[1]
+    one = torch.ones(1, O, dtype=ty, device="cuda")
+    r = G.linear_bwd(one, torch.ones(1, 8, dtype=ty, device="cuda"), torch.ones(O, 8, dtype=ty, device="cuda"),
+                     z=zr.cuda(), act="gelu", want_dx=False, want_dw=False)
+    z64, phi_c = z64.reshape(-1), phi_c.reshape(-1)
+    zpdf = z64 * torch.exp(-0.5 * z64 ** 2) * (2 * np.pi) ** -0.5
+    ref = phi_c + zpdf
+    tol = (2 * z64 ** 2 + 40) * U * phi_c + (1.5 * z64 ** 2 + 12) * U * zpdf.abs() + 2 * U * ref.abs() + 2.0 ** -122
+    err = (r["dbias"].cpu().double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
