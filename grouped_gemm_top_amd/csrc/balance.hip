@@ -58,9 +58,18 @@ __device__ __forceinline__ float across(float v) {
   return v;
 }
 
-// e^x for x <= 0, 0 at -infinity.  The rounded product loses |x| 2^-24, which weighs little where it
-// is large: there e^x is small.
-__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+// e^x for x <= 0 as 2^(x log2 e), the part that the rounded product loses (its own rounding and log2 e's,
+// up to |x| 2^-24) carried as a first-order factor: 5 units of 2^-24 at any x, where the product alone is off
+// by up to 44 at x = -64.  Below -200, at -infinity too, it is 0; a NaN stays one.  Forward and gradient at
+// N = 65536, E = 256 take 29.9 + 23.7 us, with the product alone 29.1 + 23.1.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = __builtin_elementwise_maximum(x, -200.f);
+  const float c = 1.44269502162933349609f, c_lo = 1.92596299e-8f;  // log2 e = c + c_lo
+  const float t = x * c;
+  const float e = __builtin_fmaf(x, c_lo, __builtin_fmaf(x, c, -t));
+  const float r = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(r, e * 0.6931471805599453f, r);
+}
 
 // The logits of one token, LP lanes: element (q LP + l) VW + v.  Positions past E hold -inf.
 template <int VW, int LP, int Q>

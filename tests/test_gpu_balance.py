@@ -309,3 +309,25 @@ def test_gradient_of_more_tokens_than_one_launch_takes(E, k):
         sub = (ptr - lo).clamp(0, hi - lo).int()
         one = G.balance_loss_bwd(lg[lo:hi].clone(), saved, mask=mask[lo:hi].clone(), seq_ptr=sub)
         assert torch.equal(one, dz[lo:hi]), lo
+
+
+@pytest.mark.parametrize("E,hot", [(32, 0), (33, 32), (200, 77)])
+def test_small_probabilities(E, hot):
+    """A probability far below the largest keeps its relative accuracy.  Every token chooses expert
+    `hot`, whose logit is 0; the others' are between -64 and -44, so x = z - max is exact, the sum of the
+    exponentials is 1 within 1 u and, with beta 0, dlogits[t,m] = -p_m g p_hot for m != hot.  Of that,
+    relative: the exponential 2 u from the instruction and 3 u from its argument's and its
+    correction's roundings; 1 / sum 4 u, twice (in p_m and in the dot product); products and the
+    addition 6 u: 20 u covers the 19.  (x log2 e rounded once would alone be off by up to 44 u.)"""
+    import grouped_gemm_top_amd as G
+    N = 500
+    lg = -44 - 20 * torch.rand(N, E, generator=torch.Generator().manual_seed(12))
+    lg[:, hot] = 0.0
+    idx = torch.full((N, 1), hot, dtype=torch.int32, device="cuda")
+    r = G.balance_loss(lg.cuda(), idx, 0.5)
+    d = G.balance_loss_bwd(lg.cuda(), r["saved"]).cpu().double()
+    p, g = torch.softmax(lg.double(), 1), float(r["saved"][hot])
+    ref = -p * g * p[:, hot:hot + 1]
+    err = (d - ref).abs() / (20 * U * ref.abs())
+    err[:, hot] = 0.0
+    assert float(err.max()) <= 1, float(err.max())
