@@ -186,6 +186,10 @@ int64_t moe_plan_rows_cap(int32_t kind, int32_t N, int32_t E, int32_t k, int32_t
 
 size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_t k, int32_t H, int32_t I,
                            int32_t M_cap) {
+  if (op == MOE_OP_ADD_RMSNORM_BWD) {  // (the limit on N k is the router's)
+    if (check_norm(dt, dt, N, H) != MOE_OK) return 0;
+    return moe::add_rmsnorm_bwd_ws_bytes(N, H);
+  }
   if (check_dims(N, E, k) != MOE_OK) return 0;
   switch (op) {
     case MOE_OP_PERMUTE: return moe::permute_ws_bytes(N, E);
@@ -217,9 +221,7 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_LINEAR_BWD:
       if (check_linear(dt, N, H, I) != MOE_OK) return 0;
       return moe::linear_bwd_ws_bytes(dt, N, H, I);
-    case MOE_OP_ADD_RMSNORM_BWD:
-      if (check_norm(dt, dt, N, H) != MOE_OK) return 0;
-      return moe::add_rmsnorm_bwd_ws_bytes(N, H);
+    case MOE_OP_ADD_RMSNORM_BWD: break;  // above
   }
   return 0;
 }

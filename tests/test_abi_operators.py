@@ -275,3 +275,15 @@ def test_linear_widest_output(L):
         assert L.moe_workspace_bytes(op, G.MOE_BF16, 1, 1, 1, 8, (1 << 27) - 8, 0) == 0
     assert L.moe_linear_fwd(G.MOE_BF16, F, F, None, 0, None, 1, 8, (1 << 27) - 8, ctypes.c_void_p(FAKE + 4096), None, F,
                             1 << 62, None) == G.MOE_EUNSUPPORTED
+
+
+def test_norm_backward_workspace_for_as_many_rows_as_the_call_takes(L):
+    """N H below 2^40 is what bounds the norm: the workspace query answers wherever the call accepts the sizes."""
+    for N, H in ((1 << 30, 8), ((1 << 31) - 1, 8), ((1 << 31) - 1, 504), (1 << 26, 16376)):
+        need = L.moe_workspace_bytes(G.OP_ADD_RMSNORM_BWD, G.MOE_BF16, N, 1, 1, H, 0, 0)
+        assert need >= H * 4, (N, H)
+        st = L.moe_add_rmsnorm_bwd(G.MOE_BF16, G.MOE_BF16, F, ctypes.c_void_p(FAKE + 4096), None, None, 1e-6, N, H,
+                                   ctypes.c_void_p(FAKE + 8192), None, F, F, need - 1, None)
+        assert st == G.MOE_EWORKSPACE
+    assert L.moe_workspace_bytes(G.OP_ADD_RMSNORM_BWD, G.MOE_BF16, 1 << 27, 1, 1, 8192, 0, 0) == 0   # N H = 2^40
+    assert L.moe_workspace_bytes(G.OP_ADD_RMSNORM_BWD, G.MOE_BF16, -1, 1, 1, 64, 0, 0) == 0
