@@ -534,8 +534,9 @@ def _first_use():
 
 
 def _on_stream(fn):
-    """Run a binding on its first tensor's device and, if `stream` is given, with that stream as
-    the current one: what the call allocates then belongs to the stream that uses it."""
+    """Run a binding on its first tensor's device and, if `stream` (a torch stream, or any object
+    whose cuda_stream is the handle of one of that device) is given, with that stream as the current
+    one: what the call allocates then belongs to the stream that uses it."""
     name = fn.__code__.co_varnames[0]
 
     @functools.wraps(fn)
@@ -548,8 +549,11 @@ def _on_stream(fn):
         if stream is None and (first.get_device() == torch._C._cuda_getDevice() if first.is_cuda else True):
             return fn(*args, **kw)
         _on_gpu(first)
-        if stream is not None and stream.device != first.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        if stream is not None:
+            if getattr(stream, "device", first.device) != first.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+            if not isinstance(stream, torch.cuda.Stream):  # a handle of a stream made elsewhere
+                stream = torch.cuda.ExternalStream(stream.cuda_stream, device=first.device)
         with torch.cuda.device(first.device):
             if stream is None:
                 return fn(*args, **kw)

@@ -175,3 +175,37 @@ def test_block_in_a_graph():
         for n in eager:
             assert torch.equal(eager[n].view(torch.uint8) if eager[n].dtype == BF else eager[n],
                                got[n].view(torch.uint8) if got[n].dtype == BF else got[n]), (seed, n)
+
+
+def test_stream_handles():
+    """`stream` may be any object with a cuda_stream handle, as the layer's own calls take it, a torch external
+    stream among them; the results are those of the current stream."""
+    import grouped_gemm_top_amd as G
+    t = _inputs(4)
+    D = {n: x.cuda() for n, x in t.items()}
+    lg = torch.randn(N, E, device="cuda")
+    idx = lg.topk(K, dim=1).indices.int()
+
+    def calls(**kw):
+        n = G.add_rmsnorm(D["res"], D["wn"], quantize=True, **kw)
+        b = G.add_rmsnorm_bwd(D["dout"], D["res"], D["wn"], **kw)
+        r = G.balance_loss(lg, idx, ALPHA, BETA, **kw)
+        p, z = G.linear_fwd(D["a"], D["wo"], bias=D["bo"], act="silu", want_z=True, **kw)
+        q = G.linear_bwd(D["dout"], D["a"], D["wo"], z=z, act="silu", **kw)
+        return [n["y"], n["q"].float(), b["dh"], b["dw"], r["loss"], G.balance_loss_bwd(lg, r["saved"], **kw), p, q["dx"],
+                q["dw"], q["dbias"]]
+
+    want = calls()
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+
+    class Default:
+        cuda_stream = torch.cuda.default_stream().cuda_stream
+
+    for stream in (side, Handle, Handle(), torch.cuda.ExternalStream(side.cuda_stream), Default()):
+        torch.cuda.synchronize()
+        got = calls(stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), stream
