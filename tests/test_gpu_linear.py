@@ -298,3 +298,32 @@ def test_gelu_in_its_tail(N, ty):
     tol = (2 * z64 ** 2 + 40) * U * phi_c + (1.5 * z64 ** 2 + 12) * U * zpdf.abs() + 2 * U * ref.abs() + 2.0 ** -122
     err = (r["dbias"].cpu().double() - ref).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_slope_where_the_sigmoid_is_near_one(act):
+    """fp32 slopes s (1 + v q c) with s = 1 / (1 + E), q = E / (1 + E), c the inner derivative (1 for silu): q
+    must come from E, not from 1 - s, whose error of 1 u counts v c times.  Relative errors in u: E from its
+    exponent g (silu g = |v|, two roundings and the constant's; tanh gelu g = 2 u(v), four) and the
+    instruction: a = 1.25 g + 2 and 4 g + 2; s: (1 - s) a + 3 (an addition, the reciprocal's 2); q: that
+    and a and 1, at most 2 a + 4; c and the products 10.  So s ((1 - s) a + 3) + |v s q c| (3 a + 17)
+    and 2 for the sum and the store.  A sigmoid below 2^-126 is flushed to 0, which costs 2^-126 (1 + |v c|)
+    (|v c| is 230 at z = -10, where the tanh gelu's gets there), and so may be the sum.  dbias of a single
+    row of ones is the slope itself."""
+    import grouped_gemm_top_amd as G
+    z = torch.linspace(-12.0, 60.0, 20000)[None]
+    O = z.shape[1]
+    r = G.linear_bwd(torch.ones(1, O, device="cuda"), torch.ones(1, 8, device="cuda"), torch.ones(O, 8, device="cuda"),
+                     z=z.cuda(), act=act, want_dx=False, want_dw=False)
+    v = z[0].double()
+    kg, k3 = (2 / np.pi) ** 0.5, 0.044715
+    if act == "silu":
+        t, c, a = v, torch.ones_like(v), 1.25 * v.abs() + 2
+    else:
+        t, c = 2 * kg * (v + k3 * v ** 3), 2 * kg * (1 + 3 * k3 * v ** 2)
+        a = 4 * t.abs() + 2
+    s, q = torch.sigmoid(t), torch.sigmoid(-t)
+    ref = s + v * s * q * c
+    tol = U * (s * (q * a + 3) + (v * s * q * c).abs() * (3 * a + 17) + 2 * ref.abs()) + 2.0 ** -126 * (2 + (v * c).abs())
+    err = (r["dbias"].cpu().double() - ref).abs()
+    assert bool((err <= tol).all()), (float((err / tol).max()), float(v[(err / tol).argmax()]))
