@@ -301,3 +301,11 @@ def test_more_rows_than_one_launch_takes(N, H, quant):
             assert (v is None) == (r[key] is None)
             if v is not None:
                 assert torch.equal(v, r[key][lo:hi]), (key, lo)
+
+
+@pytest.mark.parametrize("dt,rdt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("N,H", [(4099, 96), (4099, 1024), (2051, 2048), (1101, 2880), (1101, 8192), (1101, 8224)])
+def test_backward_of_many_rows(N, H, dt, rdt):
+    """More rows than one turn of the backward's 512 workgroups takes, with a ragged last turn, at each of its
+    six widths: every row of dh and dx, and dw across the turns."""
+    test_backward(N, H, dt, rdt)
