@@ -331,3 +331,41 @@ def test_small_probabilities(E, hot):
     err = (d - ref).abs() / (20 * U * ref.abs())
     err[:, hot] = 0.0
     assert float(err.max()) <= 1, float(err.max())
+
+
+def test_offsets_past_32_bits():
+    """N E beyond 2^31 elements: counts and loss of the whole batch, and the last sequence's gradient is that of
+    its tokens alone."""
+    import grouped_gemm_top_amd as G
+    N, E, k = (1 << 21) + 37, 1024, 2
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    lg = torch.empty(N, E, device="cuda")
+    idx = torch.empty(N, k, dtype=torch.int32, device="cuda")
+    ptr = torch.tensor([5, 1 << 20, N - 30, N], dtype=torch.int32, device="cuda")
+    psum = torch.zeros(3, E, dtype=torch.float64, device="cuda")
+    lse2, zm, rows = 0.0, 0.0, 1 << 16
+    for lo in range(0, N, rows):
+        z = torch.randn(min(rows, N - lo), E, generator=gen, device="cuda")
+        lg[lo:lo + rows], idx[lo:lo + rows] = z, z.topk(k, dim=1).indices.int()
+        z64, zm = z.double(), max(zm, float(z.abs().max()))
+        lse = torch.logsumexp(z64, 1, keepdim=True)
+        p = torch.exp(z64 - lse)
+        for b in range(3):
+            a, e = max(int(ptr[b]) - lo, 0), min(int(ptr[b + 1]) - lo, len(z))
+            if a < e:
+                psum[b] += p[a:e].sum(0)
+                lse2 += float(lse[a:e].square().sum())
+    r = G.balance_loss(lg, idx, ALPHA, BETA, seq_ptr=ptr)
+    d = G.balance_loss_bwd(lg, r["saved"], seq_ptr=ptr)
+    l0 = 0.0
+    for b in range(3):
+        a, e = int(ptr[b]), int(ptr[b + 1])
+        counts = torch.bincount(idx[a:e].reshape(-1).long(), minlength=E)
+        assert torch.equal(r["counts"][b].long(), counts)
+        l0 += float(ALPHA / 3 * E / (k * (e - a) ** 2) * (counts * psum[b]).sum())
+    l1 = BETA * lse2 / (N - 5)
+    # a slot adds up to T / SL = 2064 / 4 tokens in a row, then lane exchanges and at most 1024 / 16 + 16 partial rows
+    assert abs(float(r["loss"][0]) - l0) <= (4 * zm + 40 + 516 + 16 + 80) * U * l0
+    assert abs(float(r["loss"][1]) - l1) <= (2 * zm + 80 + 516 + 16 + 80) * U * l1
+    one = G.balance_loss_bwd(lg[-30:].clone(), torch.cat([r["saved"][2 * E:3 * E], r["saved"][-1:]]))
+    assert torch.equal(one, d[-30:]) and float(d[:5].abs().max()) == 0.0
