@@ -481,14 +481,17 @@ moe_status moe_add_rmsnorm_bwd(moe_dtype dt, moe_dtype rdt, const void* dy, cons
  * elements) and O at most 2^26.  N <= 16 reads w once, straight into registers (a decoding step).
  * MOE_F32 runs on the bf16 matrix instructions with each operand split exactly into three bf16
  * parts, as moe_router_logits does (fp32 accuracy; values of magnitude 3.38e38 and above, and
- * infinities, make their sums NaN), and for few tokens on the fp32 ones.
+ * infinities, make their sums NaN; a value below 2^-109 is taken with an error of up to 2^-134); a
+ * forward of few tokens (N <= 32) runs on the fp32 ones, which have neither limit.
  * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_FWD, dt, N, 1, 1, K, O, 0).
  *
  * moe_linear_bwd, given dout = the gradient of out (which is res's gradient as it stands):
  *   dz = dout act'(z)    (z as the forward stored it; NULL for MOE_ACT_NONE)
  *   dx = dz w [N,K],  dw = dz^T x [O,K],  dbias[o] = sum_t dz[t,o] (fp32 [O])      (NULL skips each)
- * MOE_BF16 rounds dz to bf16 for its two products; dbias sums it unrounded.  Everything is written
- * fresh, in a fixed order (bitwise reproducible); N == 0 sets dw and dbias to zero.
+ * With an activation MOE_BF16 rounds dz to bf16 for its two products, once (by at most 2^-8 of
+ * each value: a third operand of the matrix instructions' type beside x and w); dbias sums it unrounded.
+ * A caller that needs dz in fp32 there has it by the MOE_F32 call on fp32 copies of its tensors.
+ * Everything is written fresh, in a fixed order (bitwise reproducible); N == 0 sets dw and dbias to zero.
  * Workspace: moe_workspace_bytes(MOE_OP_LINEAR_BWD, dt, N, 1, 1, K, O, 0).
  */
 moe_status moe_linear_fwd(moe_dtype dt, const void* x, const void* w, const float* bias, int32_t act, const void* res,

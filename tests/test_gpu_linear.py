@@ -327,3 +327,23 @@ def test_slope_where_the_sigmoid_is_near_one(act):
     tol = U * (s * (q * a + 3) + (v * s * q * c).abs() * (3 * a + 17) + 2 * ref.abs()) + 2.0 ** -126 * (2 + (v * c).abs())
     err = (r["dbias"].cpu().double() - ref).abs()
     assert bool((err <= tol).all()), (float((err / tol).max()), float(v[(err / tol).argmax()]))
+
+
+@pytest.mark.parametrize("e", [-100, -116, -126])
+def test_fp32_parts_of_tiny_values(e):
+    """Where the third bf16 part of an fp32 value falls below bf16's smallest step, 2^-133, it is rounded to
+    that step: the value is off by at most 2^-134 (nothing from 2^-109 on), which the product passes on."""
+    import grouped_gemm_top_amd as G
+    N, s = 64, 60
+    x = (1 + torch.rand(N, 8, generator=torch.Generator().manual_seed(27))) * 2.0 ** e
+    w = torch.eye(8) * 2.0 ** s
+    out, _ = G.linear_fwd(x.cuda(), w.cuda())
+    r = G.linear_bwd(x.cuda(), w.repeat(8, 1).cuda(), w.cuda(), want_dbias=False)
+    ref = x.double() * 2.0 ** s
+    tol = (2.0 ** (s - 134) if e < -109 else 0.0) + U * ref
+    assert bool(((out.cpu().double() - ref).abs() <= tol).all())
+    assert bool(((r["dx"].cpu().double() - ref).abs() <= tol).all())
+    # dw[o, i] = sum_t x[t, o] 2^s [t mod 8 == i]: eight terms
+    ref = ref.reshape(8, 8, 8).sum(0).t()
+    tol = (8 * 2.0 ** (s - 134) if e < -109 else 0.0) + 16 * U * ref
+    assert bool(((r["dw"].cpu().double() - ref).abs() <= tol).all())
