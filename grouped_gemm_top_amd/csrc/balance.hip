@@ -8,16 +8,16 @@
 //   dz[t,m] = d0 p_m (g[b,m] - sum_e g[b,e] p_e) + d1 (2 beta / n) lse_t p_m
 //
 // Both directions read the logits once and are bound by that stream, small calls by launches.
-// Measured on one MI355X (a copy of 1 GiB moves 5.2 TB/s there): N = 65536, E = 256, k = 8, ragged and masked,
-// forward 21 us + 6 us in k_balance_sum for 69 MB, gradient 26.5 us for 134 MB (5.1 TB/s); N = 4096, E = 128:
-// 6.7 + 5.6 and 4.8 us, chains of a few dependent trips to memory; N = 64, E = 8: 5.0 and 2.6 us.
+// Measured on one MI355X (a copy moves 5.1 - 5.3 TB/s there): N = 65536, E = 256, k = 8, ragged and masked,
+// forward 23.6 us + 5.8 us in k_balance_sum for 69 MB, gradient 27.4 us for 134 MB (4.9 TB/s); N = 4096, E = 128:
+// 6.8 + 5.6 and 5.1 us, chains of a few dependent trips to memory; N = 64, E = 8: 5.1 and 2.5 us.
 // A group of LP lanes holds one token's logits in registers (VW consecutive values per lane, Q
 // times), so maximum, sum and dot product are a few lane exchanges and no LDS.
 //
 // Forward: workgroup i takes the tokens i T .. (i + 1) T - 1, whatever sequences they belong to,
 // so ragged batches are balanced by construction.  It leaves one partial row of sums and counts
-// per (workgroup i, sequence b) it meets, in slot i + b: along the batch i and b only ever grow, one
-// of them at each new pair, so slots are distinct.  k_balance_sum adds a sequence's slots in
+// per (workgroup i, sequence b) it meets, in slot i + b: along the batch neither i nor b decreases and
+// at each new pair one of them or both grow, so slots are distinct.  k_balance_sum adds a sequence's slots in
 // order (no floating-point atomics: bitwise reproducible), and its last workgroup, known by a
 // ticket, adds the loss.  A call small enough for one workgroup finishes in one launch.
 #include "common.h"
@@ -61,7 +61,8 @@ __device__ __forceinline__ float across(float v) {
 // e^x for x <= 0 as 2^(x log2 e), the part that the rounded product loses (its own rounding and log2 e's,
 // up to |x| 2^-24) carried as a first-order factor: 5 units of 2^-24 at any x, where the product alone is off
 // by up to 44 at x = -64.  Below -200, at -infinity too, it is 0; a NaN stays one.  Forward and gradient at
-// N = 65536, E = 256 take 29.9 + 23.7 us, with the product alone 29.1 + 23.1.
+// N = 65536, E = 256 (one sequence, the same tensors again and again) take 29.9 + 23.7 us, with the product
+// alone 29.1 + 23.1.
 __device__ __forceinline__ float exp_neg(float x) {
   x = __builtin_elementwise_maximum(x, -200.f);
   const float c = 1.44269502162933349609f, c_lo = 1.92596299e-8f;  // log2 e = c + c_lo
@@ -519,8 +520,9 @@ __global__ __launch_bounds__(NT) void k_balance_bwd(BwdArgs a) {
 // N E up to here: one workgroup and one launch (N = 64, E = 8, one sequence: 5.6 us, 11.0 by two launches;
 // N = 64, E = 128, four: 15.1 and 16.7; at N E = 32768, N = 256, four: 23.6 and 14.0)
 constexpr int ONE_MAX = 1 << 13;
-// Tokens per workgroup of the forward, for about 1024 workgroups, four a CU (N = 65536, E = 256: 256
-// of them 36.4 us, 512 26.8, 1024 25.6, 2048 28.2, 4096 31.8; N = 16384: 19.9, 17.7, 18.7, 18.7, 18.6)
+// Tokens per workgroup of the forward, for about 1024 workgroups, four a CU (N = 65536, E = 256, 37 ragged masked
+// sequences: 256 of them 37.9 us, 512 29.4, 1024 28.2, 2048 31.4, 4096 36.6; one sequence, where k_balance_sum
+// adds all rows in few workgroups: 32.6, 28.4, 30.4, 37.3, 52.4; N = 16384 ragged: 22.7, 20.4, 20.7, 20.7, 20.8)
 int chunk_tokens(int N) {
   const int t = (int)(((long long)N + 1023) / 1024);
   return t < 16 ? 16 : (t + 15) / 16 * 16;
@@ -529,7 +531,8 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 // f(VW, LP, Q) for E experts; vec: rows of 16-byte vectors.  Fewer lanes a token share each lane
 // exchange among more tokens, more lanes leave fewer values in each.  Forward and gradient at N = 65536,
-// E = 256: 64 lanes 27.1 + 31.6 us, 32 25.6 + 28.6, 16 27.3 + 28.9; E = 128: 32 lanes 22.3 + 15.9, 16 21.9 + 13.8.
+// E = 256, ragged: 64 lanes 30.4 + 31.6 us, 32 28.2 + 28.5, 16 31.2 + 30.9; E = 128, one sequence: 32 lanes 25.3 + 16.4,
+// 16 25.0 + 14.7.
 #define BL_SHAPES(vec, E, F) \
   if (vec) {                 \
     if (E <= 8) F(4, 2, 1); \

@@ -6,11 +6,14 @@
 //
 // The three products are one kernel, C[m][n] = sum_k A(m,k) B(n,k), in three layouts: forward with
 // both operands K-contiguous, dx with B K-strided (W read along its rows), dW with both K-strided.
-// Accumulation, bias, activation and residual are fp32; each output is rounded once.  In bf16 dz is
-// rounded to bf16 before its two products (the matrix cores take bf16), db sums it unrounded.
+// Accumulation, bias, activation and residual are fp32; each output is rounded once.  In bf16, where
+// there is an activation, dz is rounded to bf16 before its two products, as an operand of the matrix
+// cores, and db sums it unrounded.  dx and dW are then off by 0.0023 in the 2-norm, where their own rounding
+// alone makes 0.0017; a second bf16 part of dz would save the difference and double both products, 240 of
+// 264 us at N = 8192, K = 2048, O = 4096.  The fp32 call keeps dz whole.
 //
-// fp32 operands are split exactly into three bf16 parts, v = v0 + v1 + v2 (8 significant bits
-// each), and the product is the sum of the part products (0,0) (0,1) (1,0) (1,1) (0,2) (2,0); the
+// fp32 operands are split into three bf16 parts, v = v0 + v1 + v2 (8 significant bits each; exact from
+// 2^-109 on, below to 2^-134), and the product is the sum of the part products (0,0) (0,1) (1,0) (1,1) (0,2) (2,0); the
 // others are below 2^-24 of the leading one.  The kernel walks those six terms as one contraction
 // six times as long: a term only moves the two operands' plane offsets.  The matrix cores' fp32
 // instructions would take 16 times as long as one bf16 term, these six take 6 times.
@@ -20,12 +23,13 @@
 //  * large products: a 64-wide step of the 256 x 256 tile takes 1.38 - 1.48 us, 1450 - 1560 TFLOP/s over
 //    the chip while the loop runs.  The loop without its loads takes 1.19 us, without its LDS
 //    reads too 1.11; without its LDS reads but with the loads 1.42.  So it is the 64 KB a CU loads in a
-//    step.  N = 8192, K = O = 4096: forward 213 - 222 us, dx 215, dW 211 (library in the same runs 193 -
-//    219, 214 - 243, 235 - 268); with bias, gelu, residual and z, 201 MB more, 247 - 254.
-//  * products of few tiles: one CU's loads and the launch, 17.5 us for N = 333, K = 2880, O = 2056.
+//    step.  N = 8192, K = O = 4096: forward 210 - 222 us, dx 206 - 215, dW 204 - 211 (library in the same runs 180 -
+//    219, 204 - 243, 225 - 268); with bias, tanh gelu, residual and z, 134 MB more, 237 - 244.
+//  * products of few tiles: one CU's loads and the launch, 17.7 us for N = 333, K = 2880, O = 2056.
 //  * few tokens: W's stream, 8.7 us for 34 MB (N = 1, K = O = 4096; library 12.5).
-//  * fp32: six bf16 terms, 1278 us for N = 8192, K = O = 4096 (library 1835), 113 for 2048^3 (128); the split's
-//    own pass costs most where the product is small, 46 us for 1000^3 (25).
+//  * fp32: six bf16 terms, 1234 - 1282 us for N = 8192, K = O = 4096 (library 1813 - 1835), dx 1242, dW 1293 (1826,
+//    1805), 116 - 122 for 2048^3 (126 - 130); the split's own pass costs most where the product is small, 46 us
+//    for 1000^3 (24).
 #include <type_traits>
 
 #include "gemm_lds.h"
@@ -743,7 +747,9 @@ void split(const void* src, size_t n, bf16_t* dst, hipStream_t s) {
 // Calls whose W is streamed into registers (k_linear_few) rather than tiled.  Measured, us (few /
 // tiles): K = O = 2048: N = 1 5.5 / 7.8, 16 6.9 / 8.4, 32 8.9 / 8.8; K = O = 4096: N = 1 8.6 / 13.5,
 // 16 11.6 / 10.7, 32 14.6 / 10.9; K = 512, O = 4096: N = 32 4.4 / 5.5.
-// (fp32 tiles would first split all of W.)
+// (fp32 tiles would first split all of W.)  The rule does not look at O, and a narrow, deep W pays for it:
+// K = 16384, O = 128 runs on 8 workgroups, 20 us at N = 1 and 31 at N = 16, where tiles with K slices take
+// 10.6 at N = 17.
 bool few_tokens(bool f32, int N, int K) { return N <= 16 || (N <= 32 && (f32 || K <= 2048)); }
 
 // row groups of the dz kernel: one (its column sums are dbias) for few rows

@@ -12,11 +12,13 @@
 //   nothing has to be kept from the forward and the gradient is that of the norm at the stored h)
 //
 // Both are streaming kernels bound by HBM: each input is read once and each output written once,
-// a row stays in registers between the reduction and the result.  Measured on one MI355X (a copy
-// of 1 GiB moves 5.2 TB/s there): forward with codes 95 us for 520 MB (N = 16383, H = 2880, fp32 stream) and
-// 14.1 us for 76 MB (N = 4096, H = 2048), 5.5 and 5.4 TB/s; backward 169 + 5 us for 940 MB (N = 16384, H =
-// 4096, fp32 stream), 5.4 TB/s, and 14.8 + 4 us for 67 MB (N = 4096, H = 2048); the second launch adds dw's
-// partial rows.  One row (N = 1, H = 2048) is 3 us: a launch and two trips to memory.
+// a row stays in registers between the reduction and the result.  Measured on one MI355X, beside a copy
+// that moves as many bytes: forward with codes 95 us (copy 98) for 520 MB (N = 16383, H = 2880, fp32 stream) and
+// 14.1 us (10.9: part of it stays in the 256 MB cache) for 76 MB (N = 4096, H = 2048); backward 170 + 5 us (177)
+// for 940 MB (N = 16384, H = 4096, fp32 stream) and 15.0 + 4 us (9.9) for 67 MB (N = 4096, H = 2048); the second
+// launch adds dw's partial rows.  One row (N = 1, H = 2048) is 3 us: a launch and two trips to memory.
+// Narrow rows leave lanes idle, a wavefront holds one row: N = 131072, H = 128 forward 51, backward 69 us (26.5);
+// N = 32768, H = 64 11 and 19 us (4.0); from H = 512 on all lanes work (N = 32768: 24.4 and 25.4 us, 26.6).
 //
 // Lane l of the WR wavefronts that share a row holds the 8-value chunks l, l + 64 WR, ... (V of
 // them): 16-byte accesses in bf16, two in fp32, and an MX-FP8 block is four neighbouring lanes.
