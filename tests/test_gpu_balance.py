@@ -369,3 +369,23 @@ def test_offsets_past_32_bits():
     assert abs(float(r["loss"][1]) - l1) <= (2 * zm + 80 + 516 + 16 + 80) * U * l1
     one = G.balance_loss_bwd(lg[-30:].clone(), torch.cat([r["saved"][2 * E:3 * E], r["saved"][-1:]]))
     assert torch.equal(one, d[-30:]) and float(d[:5].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("E", [8, 32, 33, 200])
+def test_a_bad_token_spoils_the_losses_and_its_own_gradient_alone(E):
+    """A counted token with a NaN or +inf logit: NaN losses and a NaN row; other tokens' gradients, which depend on
+    the counts alone, are those of the clean call, bit for bit."""
+    import grouped_gemm_top_amd as G
+    N, k = 70, 2
+    lg, _, idx, _, _ = _inputs(N, E, k, 1, False, False, seed=14)
+    bad = {3: float("nan"), 7: float("inf"), 64: -float("nan")}
+    hurt = lg.clone()
+    for t, v in bad.items():
+        hurt[t, (5 * t) % E] = v
+    a = G.balance_loss(lg.cuda(), idx.cuda(), ALPHA, BETA)
+    b = G.balance_loss(hurt.cuda(), idx.cuda(), ALPHA, BETA)
+    da, db = (G.balance_loss_bwd(x.cuda(), a["saved"]).cpu() for x in (lg, hurt))
+    assert torch.equal(a["counts"], b["counts"]) and torch.equal(a["saved"], b["saved"])
+    assert bool(b["loss"].isnan().all())
+    keep = [t for t in range(N) if t not in bad]
+    assert torch.equal(da[keep], db[keep]) and bool(db[list(bad)].isnan().all())
