@@ -32,15 +32,10 @@
 //    for 1000^3 (24).
 #include <type_traits>
 
-#include "gemm_lds.h"
+#include "linear_tile.h"
 
 namespace moe {
 namespace ln {
-
-using namespace gk;
-using gg::OOB;
-
-constexpr int BK = 64;  // k per LDS stage: a K-contiguous row of a stage is one 128-byte line
 
 enum Act { NONE = MOE_ACT_NONE, RELU = MOE_ACT_RELU, SILU = MOE_ACT_SILU, GELU = MOE_ACT_GELU,
            GELU_TANH = MOE_ACT_GELU_TANH };
@@ -147,32 +142,6 @@ struct Args {
   int act;
 };
 
-// 16 rows x 64 columns of fp32 staged as rows of 256 bytes, 16-byte chunk q of row r at q ^ r
-__device__ __forceinline__ void stage_write(char* st, const f32x4* blk, int L) {
-  const int c = L & 15, g = L >> 4;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(st + c * 256 + (((4 * j + g) ^ c) << 4)) = blk[j];
-}
-// columns 8 (L & 7) .. + 7 of row 8 p + (L >> 3)
-__device__ __forceinline__ void stage_read(const char* st, int p, int L, f32x4 (&v)[2]) {
-  const int r = 8 * p + (L >> 3), q = 2 * (L & 7);
-  v[0] = *reinterpret_cast<const f32x4*>(st + r * 256 + ((q ^ r) << 4));
-  v[1] = *reinterpret_cast<const f32x4*>(st + r * 256 + (((q + 1) ^ r) << 4));
-}
-__device__ __forceinline__ u32x4 pack8(const f32x4 (&v)[2]) {
-  return u32x4{pk2(v[0][0], v[0][1]), pk2(v[0][2], v[0][3]), pk2(v[1][0], v[1][1]), pk2(v[1][2], v[1][3])};
-}
-
-// eight values from element o of p on, in type T
-template <typename T>
-__device__ __forceinline__ void store8(void* p, size_t o, const f32x4 (&v)[2]) {
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<u32x4*>(static_cast<T*>(p) + o) = pack8(v);
-  } else {
-    *reinterpret_cast<f32x4*>(static_cast<T*>(p) + o) = v[0];
-    *reinterpret_cast<f32x4*>(static_cast<T*>(p) + o + 4) = v[1];
-  }
-}
 template <typename T> struct Res8 { u32x4 r; };           // eight values as they are stored
 template <> struct Res8<float> { f32x4 r[2]; };
 __device__ __forceinline__ void load_res(const void* p, size_t o, Res8<bf16_t>& r) {
@@ -206,207 +175,30 @@ __device__ __forceinline__ void finish8(const Args& a, size_t o, f32x4 (&v)[2], 
   if (a.res) add_res(v, r);
   store8<T>(a.out, o, v);
 }
-// One operand's loads: R rows (K-contiguous) or R columns (K-strided) of a 64-wide k-step, as R / 8
-// kilobytes; instruction q of wavefront w fills kilobyte w + NW q, lane L its bytes 16 L .. 16 L + 15.
-//  K-contiguous: kilobyte b holds rows 8b .. 8b + 7 of 128 bytes, k-chunk c of row r at c ^ ((r >> 1) & 7)
-//  K-strided: k-rows of 2R bytes, column chunk c of k-row k at c ^ mn_f(k)
-template <int R, int NW, bool KC>
-struct Op {
-  static constexpr int NI = R / 8 / NW;
-  static_assert(R % (8 * NW) == 0 && NW % 2 == 0 && (KC || R >= 128), "whole kilobytes per wavefront");
-  i32x4 r;
-  uint32_t v[NI];  // this lane's byte offset at k = 0 (OOB when masked)
-  int kl;          // k of this lane inside a step (K-strided: instruction 0's)
-  static constexpr int KQ = KC ? 0 : 512 * NW / R;  // and how much further each instruction's is
-
-  // rows or columns x0 .. x0 + R - 1 of X; ld: row length in elements
-  __device__ __forceinline__ void setup(const void* p, int X, int K, int planes, int x0, int w, int L) {
-    r = sgpr4(dmadesc(p, (long long)planes * X * K * 2));
-#pragma unroll
-    for (int q = 0; q < NI; ++q) {
-      const int b = w + NW * q;
-      if constexpr (KC) {
-        const int row = x0 + 8 * b + (L >> 3);
-        const int c = (L & 7) ^ ((4 * (w & 1) + (L >> 4)) & 7);
-        kl = 8 * c;  // (the same for every q: NW is even)
-        v[q] = row < X ? ((uint32_t)row * (uint32_t)K + 8u * c) * 2u : OOB;
-      } else {
-        constexpr int CPR = R / 8;  // chunks per k-row
-        const int k = b * (64 / CPR) + L / CPR;
-        const int col = x0 + 8 * ((L % CPR) ^ mn_f(k));
-        if (q == 0) kl = k;
-        v[q] = col < X ? ((uint32_t)k * (uint32_t)X + (uint32_t)col) * 2u : OOB;
-      }
-    }
-  }
-  // Load instruction q of the step at k0 of the plane at byte offset `plane` into the stage area at
-  // LDS address m; k >= klim (K; 0 for a step past the last) is masked per lane (K is a multiple of 8
-  // where a chunk runs along k).  The uniform advance stays below 2^31, so a masked lane's offset is
-  // past the descriptor's range with and without it.
-  __device__ __forceinline__ void issue(int q, uint32_t m, int X, int k0, int klim, uint32_t plane, int w) const {
-    const uint32_t adv = plane + (KC ? (uint32_t)k0 * 2u : (uint32_t)k0 * (uint32_t)X * 2u);
-    dma16(r, m + (uint32_t)(w + NW * q) * 1024u, k0 + kl + KQ * q < klim ? v[q] : OOB, (uint32_t)ufl((int)adv));
-  }
-};
-
-// fragment of 16 rows (or columns) from x0 on, k-half sub of a stage (layouts: Op)
-template <int R, bool KC>
-struct Frag {
-  int o0, ff, bb;
-  __device__ __forceinline__ void init(int L) {
-    if constexpr (KC) {
-      o0 = (L & 15) * 128 + ((((L >> 4) ^ ((L >> 1) & 7)) & 7) << 4);
-    } else {
-      const int m = L & 15, g = L >> 4;
-      o0 = (8 * g + (m >> 2)) * (2 * R) + 8 * (m & 1);
-      ff = 2 * ((m >> 2) | ((g & 1) << 2));
-      bb = (m >> 1) & 1;
-    }
-  }
-  __device__ __forceinline__ bf16x8 get(const char* op, int x0, int sub) const {
-    if constexpr (KC) {
-      return *reinterpret_cast<const bf16x8*>(op + x0 * 128 + (o0 ^ (64 * sub)));
-    } else {
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const char* p = op + o0 + sub * (32 * 2 * R) + ((((x0 >> 3) ^ ff) | bb) << 4);
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 2 * R));
-      struct P { s16x4 a, b; } pr{lo, hi};
-      return __builtin_bit_cast(bf16x8, pr);
-    }
-  }
-};
-
 enum Epi { FWD = 0, PLAIN = 1, PART = 2 };
 
-// A BM x BN tile by WM x WN wavefronts, each (BM / WM) x (BN / WN) in 16 x 16 blocks.
 template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, int EPI, bool F32>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
-  constexpr int NW = WM * WN, MB = BM / WM / 16, NB = BN / WN / 16;
-  constexpr int OPA = BM * 128, STG = OPA + BN * 128;
-  static_assert(NB % 4 == 0, "the epilogue stages 64 columns at a time");
-  static_assert(NST * STG >= NW * 4096, "the epilogue's staging");
-  static_assert(MB > 1 || NB == 4, "shapes below");
-  __shared__ __attribute__((aligned(1024))) char s_ring[NST * STG];
+  using C = Core<BM, BN, WM, WN, NST, AKC, BKC, F32>;
+  constexpr int MB = C::MB, NB = C::NB;
+  __shared__ __attribute__((aligned(1024))) char s_ring[NST * C::STG];
   const int L = threadIdx.x & 63, w = ufl(threadIdx.x >> 6);
   const int wm = w % WM, wn = w / WM;
-  // XCD x gets the tiles x per .. (x + 1) per - 1 (workgroups go to XCDs round robin), in groups of
-  // eight M-tiles so that what one L2 serves at a time is a compact block of C
   const int t = (blockIdx.x & 7) * a.per + (blockIdx.x >> 3);
   const int nT = a.nM * a.nN;
   if ((int)(blockIdx.x >> 3) >= a.per || t >= nT * a.S) return;
-  const int s = t / nT, tt = t - s * nT;
-  const int gsz = 8 * a.nN, gr = tt / gsz, gm = min(8, a.nM - 8 * gr), in = tt - gr * gsz;
-  const int m0 = (8 * gr + in % gm) * BM, n0 = (in / gm) * BN;
-  constexpr int TERMS = F32 ? 6 : 1, PLANES = F32 ? 3 : 1;
+  const int s = t / nT;
+  int mt, nt;
+  tile_at(t - s * nT, a.nM, a.nN, mt, nt);
+  const int m0 = mt * BM, n0 = nt * BN;
   const int steps = (a.K + BK - 1) / BK;  // of one term
-  const int k_lo = (int)((long long)TERMS * steps * s / a.S);
-  const int nk = (int)((long long)TERMS * steps * (s + 1) / a.S) - k_lo;
-
-  Op<BM, NW, AKC> oa;
-  Op<BN, NW, BKC> ob;
-  oa.setup(a.A, a.M, a.K, PLANES, m0, w, L);
-  ob.setup(a.B, a.N, a.K, PLANES, n0, w, L);
-  Frag<BM, AKC> fra;
-  Frag<BN, BKC> frb;
-  fra.init(L);
-  frb.init(L);
-  const uint32_t ring = lds_addr(s_ring);
-  constexpr int NIA = Op<BM, NW, AKC>::NI, NI = NIA + Op<BN, NW, BKC>::NI;
-  // the next step to load: its number, k and term (all wavefront-uniform)
-  int lc = 0, lt = F32 ? k_lo / steps : 0, lk = (k_lo - lt * steps) * BK;
-  const uint32_t planeA = (uint32_t)a.M * (uint32_t)a.K * 2u, planeB = (uint32_t)a.N * (uint32_t)a.K * 2u;
-  // its load instruction q into stage st (a step past the last one is all masked)
-  auto issue = [&](int q, int st) __attribute__((always_inline)) {
-    const uint32_t m = ring + (uint32_t)st * STG;
-    const bool live = lc < nk;
-    const int k0 = live ? lk : 0, klim = live ? a.K : 0;
-    uint32_t pa = 0u, pb = 0u;
-    if constexpr (F32) {  // digits of the terms' parts, A: 0 0 1 1 0 2, B: 0 1 0 1 2 0
-      pa = live ? ((0x201100u >> (4 * lt)) & 3u) * planeA : 0u;
-      pb = live ? ((0x021010u >> (4 * lt)) & 3u) * planeB : 0u;
-    }
-    if (q < NIA) oa.issue(q, m, a.M, k0, klim, pa, w);
-    else ob.issue(q - NIA, m + OPA, a.N, k0, klim, pb, w);
-  };
-  auto advance = [&]() __attribute__((always_inline)) {
-    ++lc;
-    lk += BK;
-    if (F32 && lk >= a.K) lk = 0, ++lt;
-  };
-  auto frag_a = [&](int i, int st, int sub) __attribute__((always_inline)) {
-    return fra.get(s_ring + st * STG, wm * (BM / WM) + 16 * i, sub);
-  };
-  auto frag_b = [&](int j, int st, int sub) __attribute__((always_inline)) {
-    return frb.get(s_ring + st * STG + OPA, wn * (BN / WN) + 16 * j, sub);
-  };
-
+  const int k_lo = (int)((long long)C::TERMS * steps * s / a.S);
+  const int nk = (int)((long long)C::TERMS * steps * (s + 1) / a.S) - k_lo;
+  const uint32_t pa = (uint32_t)a.M * (uint32_t)a.K * 2u, pb = (uint32_t)a.N * (uint32_t)a.K * 2u;
+  const Opnd A{a.A, a.M, AKC ? a.K : a.M, (long long)C::PLANES * a.M * a.K * 2, pa, nullptr};
+  const Opnd B{a.B, a.N, BKC ? a.K : a.N, (long long)C::PLANES * a.N * a.K * 2, pb, nullptr};
   f32x4 acc[MB][NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // A k-step is two half-steps of k = 32.  During a half-step's MFMAs the next one's fragments are
-  // read: a row block's A fragment is replaced as soon as its MFMAs are issued, B's have a second
-  // set.  The step's barrier sits inside its second half-step: by then every wavefront holds all of
-  // step kt in registers, so its stage takes the loads of step kt + NST, and step kt + 1 has landed
-  // for the reads that follow (its loads had NST - 1 steps; those of the NST - 2 steps after it may
-  // still be in flight).
-  bf16x8 fa[MB], fb[2][NB];
-#pragma unroll
-  for (int g = 0; g < NST; ++g) {
-#pragma unroll
-    for (int q = 0; q < NI; ++q) issue(q, g);
-    advance();
-  }
-  vm_wait_barrier<(NST - 1) * NI>();
-#pragma unroll
-  for (int j = 0; j < NB; ++j) fb[0][j] = frag_b(j, 0, 0);
-#pragma unroll
-  for (int i = 0; i < MB; ++i) fa[i] = frag_a(i, 0, 0);
-  constexpr int BR = MB > 4 ? 2 : MB > 1 ? 1 : 0;  // row blocks of the second half-step before the barrier
-  constexpr int RP = (NB + MB + MB - BR - 1) / (MB - BR);  // fragment reads per row block after it
-  constexpr int LP = (NI + MB - BR - 1) / (MB - BR);       // and load instructions
-  // (sched_barrier keeps the compiler from gathering the reads at the end of a half-step)
-  int st3 = 0;
-#pragma unroll 1
-  for (int kt = 0; kt < nk; ++kt) {
-    // this step's stage and the next one's
-    const int st = NST == 2 ? kt & 1 : st3, sn = NST == 2 ? st ^ 1 : (st + 1 == NST ? 0 : st + 1);
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[0][j], fa[i], acc[i][j]);
-      fa[i] = frag_a(i, st, 1);
-#pragma unroll
-      for (int j = i; j < NB; j += MB) fb[1][j] = frag_b(j, st, 1);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      if (i == BR)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NST - 2) * NI) : "memory");
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = mma(fb[1][j], fa[i], acc[i][j]);
-      if (i >= BR) {
-#pragma unroll
-        for (int q = (i - BR) * LP; q < (i - BR + 1) * LP && q < NI; ++q) issue(q, st);
-        // B's fragments first, then A's in order, each after its row block's MFMAs (past the last
-        // step they are read and never used)
-#pragma unroll
-        for (int q = (i - BR) * RP; q < (i - BR + 1) * RP && q < NB + MB; ++q) {
-          if (q < NB) fb[0][q] = frag_b(q, sn, 0);
-          else fa[q - NB] = frag_a(q - NB, sn, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    st3 = sn;
-    advance();
-  }
-  vm_drain();  // (the masked loads past the last step write zeros into the ring)
-  lds_barrier();  // the ring is free: it stages the epilogue
+  C::run(s_ring, A, B, m0, n0, a.K, steps, k_lo, nk, w, L, acc);
 
   // acc[i][j][v] = C[wm.. + 16 i + (L & 15)][wn.. + 16 j + 4 (L >> 4) + v]; through LDS a lane gets
   // columns 8 (L & 7) .. + 7 of row 8 p + (L >> 3), so eight lanes cover a row's 128-byte line.  The
@@ -577,30 +369,6 @@ __device__ __forceinline__ void times_slope(float (&d)[8], const float (&v)[8]) 
   for (int j = 0; j < 8; ++j) d[j] *= act_bwd1<ACT>(v[j]);
 }
 
-// eight fp32 values as their three bf16 parts, part p at dst + p plane (elements)
-__device__ __forceinline__ void store_parts(bf16_t* dst, size_t plane, const float (&v)[8]) {
-  float h[8], m[8], l[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    h[j] = bf16_to_f32(f32_to_bf16(v[j]));
-    const float r = v[j] - h[j];  // exact
-    m[j] = bf16_to_f32(f32_to_bf16(r));
-    l[j] = r - m[j];
-  }
-  auto pk = [](const float (&p)[8]) { return make_uint4(pk2(p[0], p[1]), pk2(p[2], p[3]), pk2(p[4], p[5]), pk2(p[6], p[7])); };
-  *reinterpret_cast<uint4*>(dst) = pk(h);
-  *reinterpret_cast<uint4*>(dst + plane) = pk(m);
-  *reinterpret_cast<uint4*>(dst + 2 * plane) = pk(l);
-}
-__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
-  load4(p, v[0], v[1], v[2], v[3]);
-  load4(p + 4, v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  load4(p, v[0], v[1], v[2], v[3]);
-  load4(p + 4, v[4], v[5], v[6], v[7]);
-}
-
 // src (n values, a multiple of 8) -> its three parts, planes of n values
 __global__ __launch_bounds__(256) void k_linear_split(const float* __restrict__ src, size_t n, bf16_t* __restrict__ dst) {
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n / 8; i += (size_t)gridDim.x * 256) {
@@ -661,38 +429,6 @@ __global__ __launch_bounds__(256) void k_linear_dz(const T* __restrict__ dout, c
 }
 
 // ------------------------------------------------------------------ host side
-enum Kind { K_FWD, K_DX, K_DW };
-struct Shape { int big, S; };  // big: 2 = 256 x 256, 1 = 128 x 128, 0 = 64 x 64 (64 x 128 for dx)
-
-// Tile and K slices of a product: the choice with the least estimated time,
-//   launch + rounds x (start and epilogue) + steps x max(latency of a step alone, tiles a CU x
-//   time of a step when the CU is full) (+ the partial sums' way to memory and back)
-// in us.  The constants are fitted to 110 random shapes (65 <= N <= 16384, 64 <= K, O <= 8192) with
-// every tile and slice count timed: the choice is on average 0.7 % slower than the best one
-// measured, at worst 17 %.
-Shape choose(Kind kind, int M, int N, int K, int terms) {
-  const int steps = terms * ((K + BK - 1) / BK);
-  struct C { int bm, bn, occ; double fix, lat, thr; };
-  const C cs[3] = {kind == K_FWD ? C{64, 64, 3, 3.0, 0.23, 0.26} : C{64, 128, 2, 3.0, 0.32, 0.47},
-                   {128, 128, 2, 3.1, 0.75, 0.49}, {256, 256, 1, 6.4, 0.40, 1.20}};
-  Shape best{1, 1};
-  double tb = 1e30;
-  for (int b = kind == K_DW ? 1 : 0; b < 3; ++b) {
-    const long long tiles = (long long)((M + cs[b].bm - 1) / cs[b].bm) * ((N + cs[b].bn - 1) / cs[b].bn);
-    for (int S = 1; S <= 16 && S <= steps; S *= 2) {
-      const double elems = (double)S * M * N;
-      if (S > 1 && elems > 64e6) break;  // at most 256 MB of partial sums
-      const long long tpc = (tiles * S + 255) / 256, rounds = (tpc + cs[b].occ - 1) / cs[b].occ;
-      const double step = cs[b].thr * tpc > cs[b].lat ? cs[b].thr * tpc : cs[b].lat;
-      double t = 2.5 + rounds * cs[b].fix + (steps + S - 1) / S * step;
-      if (S > 1) t += 2.2 + 2.3e-6 * elems;
-      if (t < tb) tb = t, best = Shape{b, S};
-    }
-  }
-  return best;
-}
-
-size_t up(size_t n) { return (n + 255) / 256 * 256; }
 size_t part_bytes(Kind kind, int M, int N, int K, int terms) {
   const Shape c = choose(kind, M, N, K, terms);
   return c.S > 1 ? up((size_t)c.S * M * N * 4) : 0;
