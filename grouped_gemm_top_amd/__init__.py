@@ -21,7 +21,7 @@ __all__ = [
     "OP_ROUTER_LOGITS", "PLAN_TOPK", "PLAN_TR", "PLAN_CAP", "CAP_POSITION", "CAP_PROBS",
     "EXPORTED_SYMBOLS", "KERNEL_IDS", "set_kernel_events", "add_rmsnorm", "add_rmsnorm_bwd", "OP_ADD_RMSNORM_BWD",
     "balance_loss", "balance_loss_bwd", "OP_BALANCE_LOSS", "linear_fwd", "linear_bwd", "OP_LINEAR_FWD", "OP_LINEAR_BWD",
-    "ACTIVATIONS",
+    "ACTIVATIONS", "linear_ce_fwd", "linear_ce_bwd", "OP_LINEAR_CE_FWD", "OP_LINEAR_CE_BWD",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
@@ -34,6 +34,7 @@ OP_LAYER_BWD_MXFP8 = 7
 OP_ADD_RMSNORM_BWD = 8
 OP_BALANCE_LOSS = 9
 OP_LINEAR_FWD, OP_LINEAR_BWD = 10, 11
+OP_LINEAR_CE_FWD, OP_LINEAR_CE_BWD = 12, 13
 # activations of linear_fwd (moe_act in include/moe.h)
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -45,7 +46,7 @@ EXPORTED_SYMBOLS = (
     "moe_router_logits", "moe_router_bwd", "moe_set_kernel_events", "moe_quantize_mxfp8",
     "moe_grouped_gemm_fwd_mxfp8", "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8",
     "moe_add_rmsnorm", "moe_add_rmsnorm_bwd", "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
-    "moe_linear_fwd", "moe_linear_bwd",
+    "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd",
 )
 
 # kernel ids of the measurement hook (moe_kernel_id in include/moe.h)
@@ -53,7 +54,7 @@ KERNEL_IDS = {"gateup": 0, "down": 1, "dh": 2, "dx": 3, "dwd": 4, "dw1": 5, "com
               "route": 8, "permute": 9, "route_tr_plan": 10, "dswiglu": 11, "router_logits": 12,
               "router_dz": 13, "router_dx": 14, "router_dw": 15, "gateup_fp8": 16, "down_fp8": 17, "quant": 18,
               "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21, "balance": 22,
-              "balance_bwd": 23, "linear": 24, "linear_bwd": 25}
+              "balance_bwd": 23, "linear": 24, "linear_bwd": 25, "linear_ce": 26, "linear_ce_bwd": 27}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -129,6 +130,8 @@ def load_library(path: str):
     L.moe_router_bwd_acc.argtypes = [ctypes.c_int, vp, vp, vp, pp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.moe_linear_fwd.argtypes = [ctypes.c_int, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, sz, vp]
     L.moe_linear_bwd.argtypes = [ctypes.c_int, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.moe_linear_ce_fwd.argtypes = [ctypes.c_int, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    L.moe_linear_ce_bwd.argtypes = [ctypes.c_int, vp, vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
@@ -136,7 +139,7 @@ def load_library(path: str):
                "moe_set_kernel_events", "moe_quantize_mxfp8", "moe_grouped_gemm_fwd_mxfp8",
                "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
                "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
-               "moe_linear_fwd", "moe_linear_bwd"):
+               "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -780,3 +783,57 @@ def linear_bwd(dout, x, w, z=None, act="none", want_dx=True, want_dw=True, want_
         _check(lib().moe_linear_bwd(dt, _addr(dout), _addr(x), _addr(w), _addr(z), code, N, K, O, _addr(dx), _addr(dw),
                                     _addr(dbias), _addr(ws), nb, _cur(dev)))
     return dict(dx=dx, dw=dw, dbias=dbias)
+
+
+def _ce_args(x, w, targets):
+    """The checks that linear_ce_fwd and its backward share -> (N, H, V, dtype code, device)."""
+    torch = _torch
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [N, H] and w [V, H]")
+    N, H = x.shape
+    V = w.shape[0]
+    dev = x.get_device()
+    _want("x", x, (N, H), x.dtype, dev)
+    _want("w", w, (V, H), x.dtype, dev)
+    _want("targets", targets, (N,), torch.int32, dev)
+    return N, H, V, _dtype_code(x), dev
+
+
+@_on_stream
+def linear_ce_fwd(x, w, targets, z_coef: float = 0.0, loss=None, lse=None, ws=None):
+    """Softmax cross entropy of the logits x w^T, which are never kept, with a z-loss: x [N,H] and w [V,H]
+    bf16 or fp32, targets int32 [N] (outside [0, V), -100 say: the token takes no part).
+    -> dict(loss fp32 [N]: lse - z_target + z_coef lse^2, lse fp32 [N]: log sum exp of the logits, for
+    linear_ce_bwd); both 0 for tokens that take no part.  stream: a torch stream to run on."""
+    torch = _torch
+    N, H, V, dt, dev = _ce_args(x, w, targets)
+    _on_gpu(x)
+    loss = _out("loss", loss, (N,), torch.float32, x, dev)
+    lse = _out("lse", lse, (N,), torch.float32, x, dev)
+    nb = _op_bytes(OP_LINEAR_CE_FWD, dt, N, 1, 1, H, V, 0)
+    ws = _op_ws(nb, x, ws, dev)
+    _check(lib().moe_linear_ce_fwd(dt, _addr(x), _addr(w), _addr(targets), N, H, V, z_coef, _addr(loss), _addr(lse),
+                                   _addr(ws), nb, _cur(dev)))
+    return dict(loss=loss, lse=lse)
+
+
+@_on_stream
+def linear_ce_bwd(dloss, x, w, targets, lse, z_coef: float = 0.0, want_dx=True, want_dw=True, dx=None, dw=None, ws=None):
+    """Backward of linear_ce_fwd at the same x, w, targets and z_coef, from its lse and dloss fp32 [N], the
+    gradients of the losses -> dict(dx [N,H] (zero for tokens that take no part), dw [V,H]); what is not
+    wanted is None."""
+    torch = _torch
+    N, H, V, dt, dev = _ce_args(x, w, targets)
+    _want("dloss", dloss, (N,), torch.float32, dev)
+    _want("lse", lse, (N,), torch.float32, dev)
+    _on_gpu(x)
+    if want_dx or dx is not None:
+        dx = _out("dx", dx, (N, H), x.dtype, x, dev)
+    if want_dw or dw is not None:
+        dw = _out("dw", dw, (V, H), x.dtype, x, dev)
+    nb = _op_bytes(OP_LINEAR_CE_BWD, dt, N, 1, 1, H, V, 0)
+    ws = _op_ws(nb, x, ws, dev)
+    if N or dw is not None:
+        _check(lib().moe_linear_ce_bwd(dt, _addr(dloss), _addr(x), _addr(w), _addr(targets), _addr(lse), N, H, V, z_coef,
+                                       _addr(dx), _addr(dw), _addr(ws), nb, _cur(dev)))
+    return dict(dx=dx, dw=dw)

@@ -26,6 +26,7 @@ moe_status hip_status(hipError_t e, const char* where) {
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 #define REQUIRE(cond, st, ...) \
   do {                         \
@@ -128,6 +129,22 @@ moe_status check_linear(moe_dtype dt, int32_t N, int32_t K, int32_t O) {
   return MOE_OK;
 }
 
+// type and sizes of the cross entropy: descriptors of 32-bit byte offsets over x and over a piece (256
+// columns at least) of dz and of w; launches of fewer than 2^32 threads
+moe_status check_ce(moe_dtype dt, int32_t N, int32_t H, int32_t V) {
+  moe_status st;
+  if ((st = check_dtype(dt)) != MOE_OK) return st;
+  REQUIRE(N >= 0, MOE_EINVAL, "N must be >= 0 (got %d)", N);
+  REQUIRE(H >= 8 && V >= 1, MOE_EINVAL, "H must be >= 8 and V >= 1 (got H=%d, V=%d)", H, V);
+  REQUIRE(H % 8 == 0, MOE_EUNSUPPORTED, "H must be a multiple of 8 (got %d)", H);
+  const int64_t es = dt == MOE_F32 ? 6 : 2, h = H > 256 ? H : 256;
+  REQUIRE(N * h * es <= kDescBytes && 256 * (int64_t)H * es <= kDescBytes, MOE_EUNSUPPORTED,
+          "x [N=%d, max(H=%d, 256)] must be < 2 GiB (bf16; fp32: a third of it in elements)", N, H);
+  REQUIRE((int64_t)N * V <= (int64_t)1 << 36 && (int64_t)V * H <= (int64_t)1 << 36, MOE_EUNSUPPORTED,
+          "N V and V H must be at most 2^36 (got N=%d, V=%d, H=%d)", N, V, H);
+  return MOE_OK;
+}
+
 }  // namespace
 
 namespace moe {
@@ -221,6 +238,12 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_LINEAR_BWD:
       if (check_linear(dt, N, H, I) != MOE_OK) return 0;
       return moe::linear_bwd_ws_bytes(dt, N, H, I);
+    case MOE_OP_LINEAR_CE_FWD:
+      if (check_ce(dt, N, H, I) != MOE_OK) return 0;
+      return moe::linear_ce_fwd_ws_bytes(dt, N, H, I);
+    case MOE_OP_LINEAR_CE_BWD:
+      if (check_ce(dt, N, H, I) != MOE_OK) return 0;
+      return moe::linear_ce_bwd_ws_bytes(dt, N, H, I);
     case MOE_OP_ADD_RMSNORM_BWD: break;  // above
   }
   return 0;
@@ -668,6 +691,54 @@ moe_status moe_linear_bwd(moe_dtype dt, const void* dout, const void* x, const v
   hipError_t e = moe::launch_linear_bwd(dt, dout, x, w, z, act, N, K, O, dx, dw, dbias, ws, (hipStream_t)stream);
   moe::kernel_event(MOE_K_LINEAR_BWD, 1, (hipStream_t)stream);
   return hip_status(e, "moe_linear_bwd");
+}
+
+moe_status moe_linear_ce_fwd(moe_dtype dt, const void* x, const void* w, const int32_t* targets, int32_t N, int32_t H,
+                             int32_t V, float z_coef, float* loss, float* lse, void* ws, size_t ws_bytes,
+                             void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_ce(dt, N, H, V)) != MOE_OK) return st;
+  REQUIRE(z_coef - z_coef == 0.f, MOE_EINVAL, "z_coef must be finite");
+  REQUIRE(w, MOE_EINVAL, "NULL w");
+  REQUIRE(N == 0 || (x && targets && loss && lse), MOE_EINVAL, "NULL x/targets/loss/lse");
+  REQUIRE(N == 0 || (loss != lse && loss != x && lse != x && (void*)loss != targets && (void*)lse != targets), MOE_EINVAL,
+          "loss and lse must be no other argument");
+  REQUIRE(aligned16(x) && aligned16(w) && aligned16(ws), MOE_EUNSUPPORTED, "x, w and workspace must be 16-byte aligned");
+  REQUIRE(aligned4(targets) && aligned4(loss) && aligned4(lse), MOE_EUNSUPPORTED,
+          "targets, loss and lse must be 4-byte aligned");
+  const size_t need = moe::linear_ce_fwd_ws_bytes(dt, N, H, V);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  moe::kernel_event(MOE_K_LINEAR_CE, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_linear_ce_fwd(dt, x, w, targets, N, H, V, z_coef, loss, lse, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_LINEAR_CE, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_linear_ce_fwd");
+}
+
+moe_status moe_linear_ce_bwd(moe_dtype dt, const float* dloss, const void* x, const void* w, const int32_t* targets,
+                             const float* lse, int32_t N, int32_t H, int32_t V, float z_coef, void* dx, void* dw,
+                             void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_ce(dt, N, H, V)) != MOE_OK) return st;
+  REQUIRE(z_coef - z_coef == 0.f, MOE_EINVAL, "z_coef must be finite");
+  REQUIRE(dx || dw, MOE_EINVAL, "no gradient requested");
+  REQUIRE(N == 0 || (x && w && targets && lse), MOE_EINVAL, "NULL x/w/targets/lse");
+  REQUIRE(N == 0 || ((!dx || (dx != x && dx != w && dx != dw)) && (!dw || (dw != x && dw != w))), MOE_EINVAL,
+          "dx and dw must be no other argument");
+  REQUIRE(aligned16(x) && aligned16(w) && aligned16(dx) && aligned16(dw) && aligned16(ws), MOE_EUNSUPPORTED,
+          "x, w, dx, dw and workspace must be 16-byte aligned");
+  REQUIRE(aligned4(targets) && aligned4(lse) && aligned4(dloss), MOE_EUNSUPPORTED,
+          "targets, lse and dloss must be 4-byte aligned");
+  const size_t need = moe::linear_ce_bwd_ws_bytes(dt, N, H, V);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  moe::kernel_event(MOE_K_LINEAR_CE_BWD, 0, (hipStream_t)stream);
+  hipError_t e =
+      moe::launch_linear_ce_bwd(dt, dloss, x, w, targets, lse, N, H, V, z_coef, dx, dw, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_LINEAR_CE_BWD, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_linear_ce_bwd");
 }
 
 }  // extern "C"

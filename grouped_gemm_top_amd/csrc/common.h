@@ -161,4 +161,11 @@ hipError_t launch_linear_fwd(moe_dtype dt, const void* x, const void* w, const f
                              int N, int K, int O, void* out, void* z, void* ws, hipStream_t s);
 hipError_t launch_linear_bwd(moe_dtype dt, const void* dout, const void* x, const void* w, const void* z, int act,
                              int N, int K, int O, void* dx, void* dw, float* db, void* ws, hipStream_t s);
+size_t linear_ce_fwd_ws_bytes(moe_dtype dt, int N, int H, int V);
+size_t linear_ce_bwd_ws_bytes(moe_dtype dt, int N, int H, int V);
+hipError_t launch_linear_ce_fwd(moe_dtype dt, const void* x, const void* w, const int32_t* target, int N, int H, int V,
+                                float zc, float* loss, float* lse, void* ws, hipStream_t s);
+hipError_t launch_linear_ce_bwd(moe_dtype dt, const float* dloss, const void* x, const void* w, const int32_t* target,
+                                const float* lse, int N, int H, int V, float zc, void* dx, void* dw, void* ws,
+                                hipStream_t s);
 }  // namespace moe

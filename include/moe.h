@@ -83,7 +83,9 @@ typedef enum moe_op {
   MOE_OP_ADD_RMSNORM_BWD = 8,
   MOE_OP_BALANCE_LOSS = 9,
   MOE_OP_LINEAR_FWD = 10,
-  MOE_OP_LINEAR_BWD = 11
+  MOE_OP_LINEAR_BWD = 11,
+  MOE_OP_LINEAR_CE_FWD = 12,
+  MOE_OP_LINEAR_CE_BWD = 13
 } moe_op;
 
 typedef enum moe_act {
@@ -502,6 +504,36 @@ moe_status moe_linear_bwd(moe_dtype dt, const void* dout, const void* x, const v
                           void* stream);
 
 /*
+ * Softmax cross entropy with a z-loss over a large vocabulary, straight from x and the output
+ * projection w; the logits z = x w^T are formed piece by piece and never kept.  For token t with
+ * target y = targets[t] in [0, V):
+ *   z[t,v]  = sum_h x[t,h] w[v,h]                       (fp32 accumulation)
+ *   lse[t]  = log sum_v exp z[t,v]
+ *   loss[t] = lse[t] - z[t,y] + z_coef lse[t]^2
+ * A token whose target lies outside [0, V) (-100, say) takes no part: loss and lse are 0, and whatever its x
+ * holds reaches no output.  x [N,H], w [V,H] of dt; targets int32 [N]; loss, lse fp32 [N].
+ *
+ * moe_linear_ce_bwd, with dloss fp32 [N] the gradients of the losses (NULL: ones) and lse as the
+ * forward wrote it:
+ *   dz[t,v] = dloss[t] ((1 + 2 z_coef lse[t]) exp(z[t,v] - lse[t]) - [v == y])
+ *   dx = dz w [N,H] (zero for tokens that take no part),  dw = dz^T x [V,H]      (NULL skips each)
+ * z is formed again.  dz is rounded to MOE_BF16 for its two products, once (2^-8 of each value at most); MOE_F32
+ * keeps fp32 accuracy throughout, by three bf16 parts an operand, with moe_linear_fwd's limits (infinities and
+ * magnitudes from 3.38e38 on make their sums NaN).  Its working copy of dz is a piece of the vocabulary: at most
+ * 128 MB (MOE_F32: 192 MB), or 256 columns where N is above 262144 (131072).
+ * A counted token with NaN or infinite logits spoils its own loss, lse and dx, and all of dw.
+ * H a multiple of 8, V >= 1 (any); tensors and workspace 16-byte aligned, targets, loss, lse and dloss 4-byte;
+ * N max(H, 256) elements below 2 GiB (MOE_F32: 2 GiB / 6 elements), 256 H likewise, N V at most 2^36; z_coef finite.
+ * Everything is written fresh, in a fixed order (bitwise reproducible); N == 0 sets dw to zero.  Workspaces:
+ * moe_workspace_bytes(MOE_OP_LINEAR_CE_FWD / _BWD, dt, N, 1, 1, H, V, 0).
+ */
+moe_status moe_linear_ce_fwd(moe_dtype dt, const void* x, const void* w, const int32_t* targets, int32_t N, int32_t H,
+                             int32_t V, float z_coef, float* loss, float* lse, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_linear_ce_bwd(moe_dtype dt, const float* dloss, const void* x, const void* w, const int32_t* targets,
+                             const float* lse, int32_t N, int32_t H, int32_t V, float z_coef, void* dx, void* dw,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Measurement hook (for benchmarks and profilers, not needed for computing): kernels of
  * the library, identified by moe_kernel_id.  After moe_set_kernel_events(id, start, stop)
  * with two hipEvent_t handles (passed as void*), every later launch of that kernel records
@@ -539,7 +571,9 @@ typedef enum moe_kernel_id {
   MOE_K_BALANCE_BWD = 23,     /* moe_balance_loss_bwd */
   MOE_K_LINEAR = 24,          /* moe_linear_fwd */
   MOE_K_LINEAR_BWD = 25,      /* moe_linear_bwd: dz, dx, dw, dbias */
-  MOE_K_COUNT = 26
+  MOE_K_LINEAR_CE = 26,       /* moe_linear_ce_fwd */
+  MOE_K_LINEAR_CE_BWD = 27,   /* moe_linear_ce_bwd */
+  MOE_K_COUNT = 28
 } moe_kernel_id;
 
 moe_status moe_set_kernel_events(int32_t kernel_id, void* start_event, void* stop_event);
