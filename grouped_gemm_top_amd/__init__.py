@@ -22,6 +22,7 @@ __all__ = [
     "EXPORTED_SYMBOLS", "KERNEL_IDS", "set_kernel_events", "add_rmsnorm", "add_rmsnorm_bwd", "OP_ADD_RMSNORM_BWD",
     "balance_loss", "balance_loss_bwd", "OP_BALANCE_LOSS", "linear_fwd", "linear_bwd", "OP_LINEAR_FWD", "OP_LINEAR_BWD",
     "ACTIVATIONS", "linear_ce_fwd", "linear_ce_bwd", "OP_LINEAR_CE_FWD", "OP_LINEAR_CE_BWD",
+    "dequantize_mxfp8", "grouped_gemm_fwd_ckpt8", "layer_bwd_ckpt8", "OP_LAYER_BWD_CKPT8",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
@@ -35,6 +36,7 @@ OP_ADD_RMSNORM_BWD = 8
 OP_BALANCE_LOSS = 9
 OP_LINEAR_FWD, OP_LINEAR_BWD = 10, 11
 OP_LINEAR_CE_FWD, OP_LINEAR_CE_BWD = 12, 13
+OP_LAYER_BWD_CKPT8 = 14
 # activations of linear_fwd (moe_act in include/moe.h)
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -47,6 +49,7 @@ EXPORTED_SYMBOLS = (
     "moe_grouped_gemm_fwd_mxfp8", "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8",
     "moe_add_rmsnorm", "moe_add_rmsnorm_bwd", "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
     "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd",
+    "moe_grouped_gemm_fwd_ckpt8", "moe_layer_bwd_ckpt8", "moe_dequantize_mxfp8",
 )
 
 # kernel ids of the measurement hook (moe_kernel_id in include/moe.h)
@@ -54,7 +57,8 @@ KERNEL_IDS = {"gateup": 0, "down": 1, "dh": 2, "dx": 3, "dwd": 4, "dw1": 5, "com
               "route": 8, "permute": 9, "route_tr_plan": 10, "dswiglu": 11, "router_logits": 12,
               "router_dz": 13, "router_dx": 14, "router_dw": 15, "gateup_fp8": 16, "down_fp8": 17, "quant": 18,
               "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21, "balance": 22,
-              "balance_bwd": 23, "linear": 24, "linear_bwd": 25, "linear_ce": 26, "linear_ce_bwd": 27}
+              "balance_bwd": 23, "linear": 24, "linear_bwd": 25, "linear_ce": 26, "linear_ce_bwd": 27,
+              "gateup_ckpt": 28, "dh_ckpt": 29, "dequant": 30}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -132,6 +136,9 @@ def load_library(path: str):
     L.moe_linear_bwd.argtypes = [ctypes.c_int, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     L.moe_linear_ce_fwd.argtypes = [ctypes.c_int, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
     L.moe_linear_ce_bwd.argtypes = [ctypes.c_int, vp, vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    L.moe_grouped_gemm_fwd_ckpt8.argtypes = [vp, vp, vp, vp, i32, i32, pp, vp, vp, vp, vp, sz, vp]
+    L.moe_layer_bwd_ckpt8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, pp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_dequantize_mxfp8.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, i32, vp, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
@@ -139,7 +146,8 @@ def load_library(path: str):
                "moe_set_kernel_events", "moe_quantize_mxfp8", "moe_grouped_gemm_fwd_mxfp8",
                "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
                "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
-               "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd"):
+               "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd",
+               "moe_grouped_gemm_fwd_ckpt8", "moe_layer_bwd_ckpt8", "moe_dequantize_mxfp8"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -783,6 +791,99 @@ def linear_bwd(dout, x, w, z=None, act="none", want_dx=True, want_dw=True, want_
         _check(lib().moe_linear_bwd(dt, _addr(dout), _addr(x), _addr(w), _addr(z), code, N, K, O, _addr(dx), _addr(dw),
                                     _addr(dbias), _addr(ws), nb, _cur(dev)))
     return dict(dx=dx, dw=dw, dbias=dbias)
+
+
+def _ckpt_layer(H, w_gate, w_up, w_down, plan, dev):
+    """The checks that the layer's 8-bit checkpoint calls share -> (E, I, rows of the row arrays)."""
+    bf = _torch.bfloat16
+    if w_gate.dim() != 3:
+        raise ValueError("w_gate and w_up must be [E, I, H], w_down [E, H, I]")
+    E, I = w_gate.shape[:2]
+    if E != plan.E:
+        raise ValueError(f"the plan is for {plan.E} experts, w_gate holds {E}")
+    _want("w_gate", w_gate, (E, I, H), bf, dev)
+    _want("w_up", w_up, (E, I, H), bf, dev)
+    _want("w_down", w_down, (E, H, I), bf, dev)
+    if plan.counts.get_device() != dev:
+        raise ValueError(f"tensors on different devices: the plan is on {plan.counts.device}")
+    return E, I, max(plan.M_cap, 1)
+
+
+@_on_stream
+def dequantize_mxfp8(q, scales, dtype=None, out=None):
+    """The values that MX-FP8 codes q uint8 [..., K] and their scale codes (quantize_mxfp8's) stand for
+    -> [..., K] in dtype (torch.bfloat16, the default, or torch.float32).  stream: a torch stream to run on."""
+    torch = _torch
+    K = q.shape[-1]
+    rows = q.numel() // K if K else 0
+    dev = q.get_device()
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    _want("q", q, q.shape, torch.uint8, dev)
+    _want("scales", scales, q.shape[:-1] + (mx_scale_cols(K),), torch.uint8, dev)
+    _on_gpu(q)
+    out = _out("out", out, q.shape, dtype, q, dev)
+    _check(lib().moe_dequantize_mxfp8(_dtype_code(out), _addr(q), _addr(scales), rows, K, _addr(out), _cur(dev)))
+    return out
+
+
+@_on_stream
+def grouped_gemm_fwd_ckpt8(x, w_gate, w_up, w_down, plan: Plan, hq=None, hs=None, y=None, ws=None):
+    """grouped_gemm_fwd for bf16 layers that keeps [G | U] for the backward as MX-FP8 codes
+    -> ((hq uint8 [M_cap, 2I], hs uint8 [M_cap, 2 mx_scale_cols(I)]), y [M_cap, H]); each half of a row is
+    laid out as quantize_mxfp8 lays out a row of I values.  y is bit for bit grouped_gemm_fwd's.
+    I a multiple of 32.  stream: a torch stream to run on (default: the current one)."""
+    torch = _torch
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, H] (got {tuple(x.shape)})")
+    H = x.shape[1]
+    dev = x.get_device()
+    _want("x", x, (plan.N, H), torch.bfloat16, dev)
+    _, I, mc = _ckpt_layer(H, w_gate, w_up, w_down, plan, dev)
+    _on_gpu(x)
+    hq = _out("hq", hq, (mc, 2 * I), torch.uint8, x, dev)
+    hs = _out("hs", hs, (mc, 2 * mx_scale_cols(I)), torch.uint8, x, dev)
+    y = _out("y", y, (mc, H), torch.bfloat16, x, dev)
+    nb = _op_bytes(OP_GEMM_FWD, MOE_BF16, plan.N, plan.E, plan.k, H, I, plan.M_cap)
+    ws = _op_ws(nb, x, ws, dev)
+    _check(lib().moe_grouped_gemm_fwd_ckpt8(_addr(x), _addr(w_gate), _addr(w_up), _addr(w_down), H, I, plan.c, _addr(hq),
+                                            _addr(hs), _addr(y), _addr(ws), nb, _cur(dev)))
+    return (hq, hs), y
+
+
+@_on_stream
+def layer_bwd_ckpt8(dout, x, w_gate, w_up, w_down, plan: Plan, hcache, dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                    ds=None, ws=None):
+    """layer_bwd for bf16 layers at the [G | U] that hcache = (hq, hs) of grouped_gemm_fwd_ckpt8 stands for; x is
+    bf16 [N,H], or (codes, scale codes) as add_rmsnorm and quantize_mxfp8 make them (dw_gate and dw_up are then taken
+    at the values these stand for).  -> dict(dx, dw_gate, dw_up, dw_down, ds), as layer_bwd."""
+    torch = _torch
+    bf, u8 = torch.bfloat16, torch.uint8
+    if dout.dim() != 2:
+        raise ValueError(f"dout must be [N, H] (got {tuple(dout.shape)})")
+    N, H = dout.shape
+    dev = dout.get_device()
+    _want("dout", dout, (plan.N, H), bf, dev)
+    x, xs = x if isinstance(x, (tuple, list)) else (x, None)
+    _want("x", x, (N, H), bf if xs is None else u8, dev)
+    if xs is not None:
+        _want("x's scale codes", xs, (N, mx_scale_cols(H)), u8, dev)
+    _, I, mc = _ckpt_layer(H, w_gate, w_up, w_down, plan, dev)
+    hq, hs = hcache
+    _want("hq", hq, (mc, 2 * I), u8, dev)
+    _want("hs", hs, (mc, 2 * mx_scale_cols(I)), u8, dev)
+    _on_gpu(dout)
+    dx = _out("dx", dx, (N, H), bf, dout, dev)
+    dw_gate = _out("dw_gate", dw_gate, w_gate.shape, bf, dout, dev)
+    dw_up = _out("dw_up", dw_up, w_up.shape, bf, dout, dev)
+    dw_down = _out("dw_down", dw_down, w_down.shape, bf, dout, dev)
+    ds = _out("ds", ds, (N, plan.k) if plan.kind == PLAN_TOPK else (mc,), torch.float32, dout, dev)
+    nb = _op_bytes(OP_LAYER_BWD_CKPT8, MOE_BF16, plan.N, plan.E, plan.k, H, I, plan.M_cap)
+    ws = _op_ws(nb, dout, ws, dev)
+    _check(lib().moe_layer_bwd_ckpt8(_addr(dout), _addr(x), _addr(xs), _addr(w_gate), _addr(w_up), _addr(w_down), H, I,
+                                     plan.c, _addr(hq), _addr(hs), _addr(dx), _addr(dw_gate), _addr(dw_up),
+                                     _addr(dw_down), _addr(ds), _addr(ws), nb, _cur(dev)))
+    return dict(dx=dx, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down, ds=ds)
 
 
 def _ce_args(x, w, targets):

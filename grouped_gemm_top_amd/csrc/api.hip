@@ -229,6 +229,9 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_LAYER_BWD_MXFP8:
       if (H < 32 || I < 32 || H % 32 || I % 32 || M_cap < 0) return 0;
       return moe::layer_bwd_mxfp8_ws_bytes(N, M_cap, H, I);
+    case MOE_OP_LAYER_BWD_CKPT8:
+      if (check_hi(H, I) != MOE_OK || I % 32 || M_cap < 0) return 0;
+      return moe::layer_bwd_ckpt8_ws_bytes(N, M_cap, H, I);
     case MOE_OP_BALANCE_LOSS:  // I: the sequences
       if (check_seqs(I, E, &I) != MOE_OK) return 0;
       return moe::balance_loss_ws_bytes(N, E, I);
@@ -394,6 +397,70 @@ moe_status moe_quantize_mxfp8(moe_dtype dt, const void* src, int64_t rows, int32
   hipError_t e = moe::launch_quant_mxfp8(dt, src, rows, K, q, scales, (hipStream_t)stream);
   moe::kernel_event(MOE_K_QUANT, 1, (hipStream_t)stream);
   return hip_status(e, "moe_quantize_mxfp8");
+}
+
+moe_status moe_dequantize_mxfp8(moe_dtype dt, const uint8_t* q, const uint8_t* scales, int64_t rows, int32_t K,
+                                void* out, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_dtype(dt)) != MOE_OK) return st;
+  REQUIRE(rows >= 0, MOE_EINVAL, "rows must be >= 0 (got %lld)", (long long)rows);
+  REQUIRE(K >= 32 && K % 32 == 0, MOE_EUNSUPPORTED, "K must be a positive multiple of 32 (got %d)", K);
+  REQUIRE(rows == 0 || (q && scales && out), MOE_EINVAL, "NULL q/scales/out");
+  REQUIRE(aligned16(q) && aligned16(out), MOE_EUNSUPPORTED, "q and out must be 16-byte aligned");
+  REQUIRE(rows <= ((int64_t)1 << 40) / K, MOE_EINVAL, "rows too large");
+  moe::kernel_event(MOE_K_DEQUANT, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_dequant_mxfp8(dt, q, scales, rows, K, out, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_DEQUANT, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_dequantize_mxfp8");
+}
+
+moe_status moe_grouped_gemm_fwd_ckpt8(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                                      int32_t H, int32_t I, const moe_plan* plan, uint8_t* hq, uint8_t* hs, void* y,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_hi(H, I)) != MOE_OK) return st;
+  REQUIRE(I % 32 == 0, MOE_EUNSUPPORTED, "I must be a multiple of 32 (got %d)", I);
+  if ((st = check_plan(plan)) != MOE_OK) return st;
+  REQUIRE(w_gate && w_up && w_down, MOE_EINVAL, "NULL weight argument");
+  REQUIRE(plan->M_cap == 0 || (x && hq && hs && y), MOE_EINVAL, "NULL tensor argument");
+  REQUIRE(aligned16(x) && aligned16(w_gate) && aligned16(w_up) && aligned16(w_down) && aligned16(hq) && aligned4(hs) &&
+              aligned16(y) && aligned16(ws),
+          MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned, hs 4-byte aligned");
+  if ((st = check_desc_sizes(MOE_BF16, plan->N, H, I, plan->M_cap)) != MOE_OK) return st;
+  const size_t need = moe::gemm_fwd_ws_bytes(MOE_BF16, (int)mcap_of(plan), I);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  return hip_status(moe::launch_gemm_fwd_ckpt8(x, w_gate, w_up, w_down, H, I, *plan, hq, hs, y, ws,
+                                               (hipStream_t)stream),
+                    "moe_grouped_gemm_fwd_ckpt8");
+}
+
+moe_status moe_layer_bwd_ckpt8(const void* dout, const void* x, const uint8_t* xs, const void* w_gate,
+                               const void* w_up, const void* w_down, int32_t H, int32_t I, const moe_plan* plan,
+                               const uint8_t* hq, const uint8_t* hs, void* dx, void* dw_gate, void* dw_up,
+                               void* dw_down, float* ds, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_hi(H, I)) != MOE_OK) return st;
+  REQUIRE(I % 32 == 0 && (!xs || H % 32 == 0), MOE_EUNSUPPORTED,
+          "I, and H where x comes as codes, must be a multiple of 32 (got H=%d, I=%d)", H, I);
+  if ((st = check_plan(plan)) != MOE_OK) return st;
+  REQUIRE(w_gate && w_up && w_down && dw_gate && dw_up && dw_down, MOE_EINVAL, "NULL weight/gradient argument");
+  REQUIRE(plan->N == 0 || (dout && x && dx), MOE_EINVAL, "NULL activation argument");
+  REQUIRE(plan->M_cap == 0 || (hq && hs && ds), MOE_EINVAL, "NULL hq/hs/ds argument");
+  REQUIRE(aligned16(dout) && aligned16(x) && aligned16(w_gate) && aligned16(w_up) && aligned16(w_down) &&
+              aligned16(hq) && aligned4(hs) && aligned16(dx) && aligned16(dw_gate) && aligned16(dw_up) &&
+              aligned16(dw_down) && aligned16(ws),
+          MOE_EUNSUPPORTED, "tensors and workspace must be 16-byte aligned, hs 4-byte aligned");
+  if ((st = check_desc_sizes(MOE_BF16, plan->N, H, I, plan->M_cap)) != MOE_OK) return st;
+  const size_t need = moe::layer_bwd_ckpt8_ws_bytes(plan->N, (int)mcap_of(plan), H, I);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  return hip_status(moe::launch_layer_bwd_ckpt8(dout, x, xs, w_gate, w_up, w_down, H, I, *plan, hq, hs, dx, dw_gate,
+                                                dw_up, dw_down, ds, ws, (hipStream_t)stream),
+                    "moe_layer_bwd_ckpt8");
 }
 
 moe_status moe_grouped_gemm_fwd_mxfp8(const uint8_t* x_q, const uint8_t* x_s, const uint8_t* wg_q,

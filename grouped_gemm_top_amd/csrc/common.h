@@ -168,4 +168,13 @@ hipError_t launch_linear_ce_fwd(moe_dtype dt, const void* x, const void* w, cons
 hipError_t launch_linear_ce_bwd(moe_dtype dt, const float* dloss, const void* x, const void* w, const int32_t* target,
                                 const float* lse, int N, int H, int V, float zc, void* dx, void* dw, void* ws,
                                 hipStream_t s);
+hipError_t launch_dequant_mxfp8(moe_dtype dt, const void* q, const void* scales, long long rows, int K, void* out,
+                                hipStream_t s);
+// the layer with [G | U] kept as codes (bf16 layers); xs: x is codes and these its scale codes
+hipError_t launch_gemm_fwd_ckpt8(const void* x, const void* wg, const void* wu, const void* wd, int H, int I,
+                                 const moe_plan& p, void* hq, void* hs, void* y, void* ws, hipStream_t s);
+size_t layer_bwd_ckpt8_ws_bytes(int N, int M_cap, int H, int I);
+hipError_t launch_layer_bwd_ckpt8(const void* dout, const void* x, const void* xs, const void* wg, const void* wu,
+                                  const void* wd, int H, int I, const moe_plan& p, const void* hq, const void* hs,
+                                  void* dx, void* dwg, void* dwu, void* dwd, float* ds, void* ws, hipStream_t s);
 }  // namespace moe

@@ -916,6 +916,25 @@ hipError_t launch_gemm_fwd_mxfp8(const void* xq, const void* xs, const void* wgq
   return run_gemm_bf16<gg::DOWN8>(a, mt * ((H + 255) / 256), s);
 }
 
+hipError_t launch_gemm_fwd_ckpt8(const void* x, const void* wg, const void* wu, const void* wd, int H, int I,
+                                 const moe_plan& p, void* hq, void* hs, void* y, void* ws, hipStream_t s) {
+  gg::Args a{};
+  a.x = x; a.wg = wg; a.wu = wu; a.wd = wd;
+  a.counts = p.counts; a.offsets = p.offsets; a.row_token = p.row_token; a.row_w = p.row_w;
+  a.E = p.E; a.H = H; a.I = I; a.N = p.N; a.M_cap = p.M_cap;
+  a.out0 = hq; a.out1 = ws; a.out2 = hs;
+  const long long mt = (long long)(p.M_cap + 255) / 256 + p.E;
+  hipError_t err = run_gemm_bf16<gg::GATEUP, true>(a, mt * ((I + 127) / 128), s);
+  if (err != hipSuccess) return err;
+  a.act = ws; a.out0 = y; a.out1 = nullptr; a.out2 = nullptr;
+  return run_gemm_bf16<gg::DOWN>(a, mt * ((H + 255) / 256), s);
+}
+
+// moe_layer_bwd's workspace, then x in bf16 where it comes as codes
+size_t layer_bwd_ckpt8_ws_bytes(int N, int M_cap, int H, int I) {
+  return layer_bwd_ws_bytes(MOE_BF16, N, M_cap, H, I) + align256((size_t)N * H * 2);
+}
+
 size_t layer_bwd_ws_bytes(moe_dtype dt, int N, int M_cap, int H, int I) {
   (void)N;
   const size_t es = dt == MOE_BF16 ? 2 : 4;
@@ -934,12 +953,13 @@ size_t layer_bwd_mxfp8_ws_bytes(int N, int M_cap, int H, int I) {
 }
 
 // wtq / wts: the quantized [W_gate^T | W_up^T] of every expert for a dX product on MX-FP8
-// operands (bf16 layers only), or NULL for the bf16 product.
+// operands (bf16 layers only), or NULL for the bf16 product.  hs: hcache holds codes and these their
+// scale codes (bf16 layers only; NULL: hcache is bf16).
 template <typename T>
 static hipError_t layer_bwd_t(const void* dout, const void* x, const void* wg, const void* wu, const void* wd,
                               int H, int I, const moe_plan& p, const void* hcache, void* dx, void* dwg,
                               void* dwu, void* dwd, float* ds, void* ws, hipStream_t s, const void* wtq = nullptr,
-                              const void* wts = nullptr) {
+                              const void* wts = nullptr, const void* hs = nullptr) {
   const size_t es = sizeof(T);
   constexpr bool BF = std::is_same<T, bf16_t>::value;
   const int tn = BF ? 256 : gg::BN;  // N-tile width of the dH kernel
@@ -976,7 +996,10 @@ static hipError_t layer_bwd_t(const void* dout, const void* x, const void* wg, c
   // dA' = dOut[t] W_down^T (varlen-M GEMM) with the dSwiGLU epilogue: dH = [dG | dU],
   // A' = w A and the dS partials (their ordered sum runs in the dX combine below)
   a.out0 = dh; a.out1 = aprime; a.dspart = dspart;
-  if ((err = launch(KDH{}, mt * nTN)) != hipSuccess) return err;
+  a.hs = hs;
+  if (BF && hs != nullptr) err = run_gemm_bf16<gg::DH, true>(a, mt * nTN, s);
+  else err = launch(KDH{}, mt * nTN);
+  if (err != hipSuccess) return err;
   // The two weight-gradient kernels run first and dX last.  The bf16 kernels store their dW
   // (805 MB in all at the headline shape) with the non-temporal policy, since no later kernel
   // of the step reads it; of the orders measured with those stores this one is the fastest
@@ -1018,6 +1041,20 @@ hipError_t launch_layer_bwd_mxfp8(const void* dout, const void* x, const void* w
                                   const void* hcache, void* dx, void* dwg, void* dwu, void* dwd, float* ds, void* ws,
                                   hipStream_t s) {
   return layer_bwd_t<bf16_t>(dout, x, wg, wu, wd, H, I, p, hcache, dx, dwg, dwu, dwd, ds, ws, s, wtq, wts);
+}
+
+hipError_t launch_layer_bwd_ckpt8(const void* dout, const void* x, const void* xs, const void* wg, const void* wu,
+                                  const void* wd, int H, int I, const moe_plan& p, const void* hq, const void* hs,
+                                  void* dx, void* dwg, void* dwu, void* dwd, float* ds, void* ws, hipStream_t s) {
+  if (xs != nullptr) {  // the weight gradients take x in bf16 (codes and scales stand for bf16 values)
+    void* xb = static_cast<char*>(ws) + layer_bwd_ws_bytes(MOE_BF16, p.N, p.M_cap, H, I);
+    kernel_event(MOE_K_DEQUANT, 0, s);
+    hipError_t err = launch_dequant_mxfp8(MOE_BF16, x, xs, p.N, H, xb, s);
+    kernel_event(MOE_K_DEQUANT, 1, s);
+    if (err != hipSuccess) return err;
+    x = xb;
+  }
+  return layer_bwd_t<bf16_t>(dout, x, wg, wu, wd, H, I, p, hq, dx, dwg, dwu, dwd, ds, ws, s, nullptr, nullptr, hs);
 }
 
 hipError_t launch_layer_bwd(moe_dtype dt, const void* dout, const void* x, const void* wg, const void* wu,

@@ -543,6 +543,54 @@ __device__ __forceinline__ uint4 stage_read(const char* st, int p, int L) {
 __device__ __forceinline__ void st16(rsrc_t r, uint32_t off, const uint4& v) {
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, 0);
 }
+// [G | U] kept in 8 bits (the checkpoint form of hcache): codes [M_cap, 2I] and scale codes [M_cap, 2 KS(I)], each
+// half of a row laid out and quantized by itself as moe_quantize_mxfp8 does a row of I values.
+//
+// ckpt_store: a 16-row block of a gate/up tile, 64 gate columns (blk[0..3]) and the 64 up columns they
+// belong to (blk[4..7]).  A row's block of 32 lies in the four lanes L & 15 + 16 g, eight values each, whose
+// largest magnitude gives its scale.  The codes go through LDS, rows of 128 bytes with 16-byte chunk q of row r
+// at q ^ (r & 7), and leave as 64 contiguous bytes a half; the block of columns from I on is zeros, whose scale
+// code 0 fills the scale row's padding.  Rows >= mlen lie past the descriptors' ranges.
+__device__ __forceinline__ void ckpt_store(rsrc_t rq, rsrc_t rs, char* st, const f32x4 (&blk)[8], uint32_t m16,
+                                           int i0, int I, int L) {
+  const int c = L & 15, g = L >> 4;
+  int se[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float mx = 0.f;
+#pragma unroll
+    for (int j = 2 * b; j < 2 * b + 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) mx = fmaxf(mx, fabsf(blk[j][v]));
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    se[b] = mx_scale_exp(mx);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint32_t*>(st + c * 128 + ((j ^ (c & 7)) << 4) + 4 * g) =
+        mx_pack4(blk[j][0], blk[j][1], blk[j][2], blk[j][3], se[j >> 1]);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int r = 8 * p + (L >> 3), q = L & 7, ii = i0 + 16 * (q & 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(st + r * 128 + ((q ^ (r & 7)) << 4));
+    st16(rq, ii < I ? (m16 + r) * (uint32_t)(2 * I) + (uint32_t)((q >= 4 ? I : 0) + ii) : OOB, v);
+  }
+  // the two scale codes of the gate half by lane group 0, of the up half by group 1
+  const int KS = 4 * ((I + 127) / 128);
+  const uint16_t s0 = (uint16_t)((se[0] + 127) | ((se[1] + 127) << 8));
+  const uint16_t s1 = (uint16_t)((se[2] + 127) | ((se[3] + 127) << 8));
+  __builtin_amdgcn_raw_buffer_store_b16(
+      g == 0 ? s0 : s1, rs, g < 2 ? (m16 + c) * (uint32_t)(2 * KS) + (uint32_t)(g * KS + i0 / 32) : OOB, 0, 0);
+}
+// four e4m3 codes of scale 2^e as fp32
+__device__ __forceinline__ void ckpt_val4(uint32_t w, int e, float (&v)[4]) {
+  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  v[0] = __builtin_amdgcn_ldexpf(lo.x, e);
+  v[1] = __builtin_amdgcn_ldexpf(lo.y, e);
+  v[2] = __builtin_amdgcn_ldexpf(hi.x, e);
+  v[3] = __builtin_amdgcn_ldexpf(hi.y, e);
+}
 // Non-temporal form (cache policy NT), for the weight gradients: no later kernel of the step
 // reads them, and stored normally their dirty lines drain to HBM during the next kernels
 // (the dX GEMM that follows them ran 24 us slower).
@@ -552,7 +600,8 @@ __device__ __forceinline__ void st16_nt(rsrc_t r, uint32_t off, const uint4& v) 
 
 // acc[i][j][v] = C[m = 16(4i + wm) + (L & 15)][n = wn*128 + 16j + 4(L >> 4) + v]
 // `st`: this wavefront's 4 KB of LDS staging, free for the duration of the epilogue.
-template <int KIND>
+// CK (GATEUP, DH): [G | U] is written and read as codes.
+template <int KIND, bool CK>
 __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&acc)[KT<KIND>::MI][8], int wm, int wn,
                                          int L_, int nMg, char* st) {
   // The lane's address arithmetic depends only on kernel constants; an opaque copy of the lane
@@ -564,21 +613,28 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&a
   constexpr int MI = KT<KIND>::MI;
   const long long rb = (long long)c.roff + (long long)c.mt * Geo<KIND>::BMK;
   if constexpr (KIND == GATEUP || KIND == GATEUP8) {
-    const rsrc_t rh = gg::mkr_off(a.out0, rb * 2 * I * 2, (long long)c.mlen * 2 * I * 2);
+    constexpr int HB = CK ? 1 : 2;  // bytes of a [G | U] value
+    const int KS2 = 8 * ((I + 127) / 128);
+    const rsrc_t rh = gg::mkr_off(a.out0, rb * 2 * I * HB, (long long)c.mlen * 2 * I * HB);
+    const rsrc_t rhs = gg::mkr_off(CK ? a.out2 : a.out0, CK ? rb * KS2 : 0, CK ? (long long)c.mlen * KS2 : 0);
     const rsrc_t ra = KIND == GATEUP ? gg::mkr_off(a.out1, rb * I * 2, (long long)c.mlen * I * 2)
                                      : gg::mkr_off(a.out1, rb * I, (long long)c.mlen * I);
     const int i0 = c.nt * 128 + wn * 64;  // first i of this wavefront's 64 gate and 64 up columns
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       // [G | U] block: staged columns 0..63 gate, 64..127 up, for i0 .. i0 + 63
-      stage_write(st, acc[i], L);
+      if constexpr (CK) {
+        ckpt_store(rh, rhs, st, acc[i], (uint32_t)(16 * (4 * i + wm)), i0, I, L);
+      } else {
+        stage_write(st, acc[i], L);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint4 v = stage_read(st, p, L);
-        const uint32_t m = (uint32_t)(16 * (4 * i + wm) + 4 * p + (L >> 4));  // rows >= mlen: past the range
-        const int q = L & 15, ii = i0 + (q & 7) * 8;
-        const uint32_t off = m * (uint32_t)(2 * I) * 2u + (uint32_t)((q >= 8 ? I : 0) + ii) * 2u;
-        st16(rh, ii < I ? off : OOB, v);
+        for (int p = 0; p < 4; ++p) {
+          const uint4 v = stage_read(st, p, L);
+          const uint32_t m = (uint32_t)(16 * (4 * i + wm) + 4 * p + (L >> 4));  // rows >= mlen: past the range
+          const int q = L & 15, ii = i0 + (q & 7) * 8;
+          const uint32_t off = m * (uint32_t)(2 * I) * 2u + (uint32_t)((q >= 8 ? I : 0) + ii) * 2u;
+          st16(rh, ii < I ? off : OOB, v);
+        }
       }
       if constexpr (KIND == GATEUP8) {
         // A = silu(G) * U quantized to MX-FP8 for the down GEMM: the wavefront's 64 columns are
@@ -660,7 +716,10 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&a
     // goes to dspart[r nP + q] (nP = 2 ceil(I / 256)), summed in order by the next kernel.
     // Rows >= mlen and columns >= I lie past the descriptors' ranges: their loads read zeros
     // and their stores are dropped.
-    const rsrc_t rhc = gg::mkr_off(a.hcache, rb * 2 * I * 2, (long long)c.mlen * 2 * I * 2);
+    constexpr int HB = CK ? 1 : 2;  // bytes of a [G | U] value
+    const int KS = 4 * ((I + 127) / 128);
+    const rsrc_t rhc = gg::mkr_off(a.hcache, rb * 2 * I * HB, (long long)c.mlen * 2 * I * HB);
+    const rsrc_t rhs = gg::mkr_off(CK ? a.hs : a.hcache, CK ? rb * 2 * KS : 0, CK ? (long long)c.mlen * 2 * KS : 0);
     const rsrc_t rdh = gg::mkr_off(a.out0, rb * 2 * I * 2, (long long)c.mlen * 2 * I * 2);
     const rsrc_t rap = gg::mkr_off(a.out1, rb * I * 2, (long long)c.mlen * I * 2);
     const rsrc_t rw = gg::mkr_off(a.row_w, rb * 4, (long long)c.mlen * 4);
@@ -673,9 +732,28 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&a
     const int col = c0 + 8 * q;  // the 8 columns this lane moves in row-contiguous form
     // (loading block i + 1's G and U during block i would keep 33 more registers live and
     // pushes them into scratch, which made the epilogue twice as slow)
-    uint4 gv[4], uv[4];
+    // As codes, G and U come in as rows of 128 bytes (8 lanes a row, placed as ckpt_store does), and a lane
+    // takes its 32 of each and its row's scale words into registers before dG and dU overwrite them.
+    constexpr int NV = CK ? 2 : 4;
+    uint4 gv[NV], uv[NV];
+    uint32_t gs = 0, us = 0;
     float w = 0.f;
     auto gu_load = [&](int i) __attribute__((always_inline)) {
+      if constexpr (CK) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t m = (uint32_t)(16 * (4 * i + wm) + 8 * p + (L >> 3));
+          const int cc = c0 + 16 * (L & 7);
+          const uint32_t off = m * (uint32_t)(2 * I) + (uint32_t)cc;
+          gv[p] = gg::bld16(rhc, cc < I ? off : OOB);
+          uv[p] = gg::bld16(rhc, cc < I ? off + (uint32_t)I : OOB);
+        }
+        const uint32_t so = (uint32_t)(16 * (4 * i + wm) + q) * (uint32_t)(2 * KS) + (uint32_t)(c0 / 32);
+        gs = (uint32_t)gg::bld4(rhs, c0 < I ? so : OOB);
+        us = (uint32_t)gg::bld4(rhs, c0 < I ? so + (uint32_t)KS : OOB);
+        w = __int_as_float(gg::bld4(rw, (uint32_t)(16 * (4 * i + wm) + q) * 4u));
+        return;
+      }
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const uint32_t m = (uint32_t)(16 * (4 * i + wm) + 4 * p + g4);
@@ -689,25 +767,51 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&a
     for (int i = 0; i < MI; ++i) {
       gu_load(i);
       const float wi = w;
+      uint32_t gq[CK ? 8 : 1], uq[CK ? 8 : 1];
+      if constexpr (CK) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int r = 4 * p + g4;
-        *reinterpret_cast<uint4*>(sgu + r * 256 + ((q ^ r) << 4)) = gv[p];
-        *reinterpret_cast<uint4*>(suu + r * 256 + ((q ^ r) << 4)) = uv[p];
+        for (int p = 0; p < 2; ++p) {
+          const int r = 8 * p + (L >> 3), o = r * 128 + (((L & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(sgu + o) = gv[p];
+          *reinterpret_cast<uint4*>(suu + o) = uv[p];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int o = q * 128 + ((j ^ (q & 7)) << 4) + 4 * g4;
+          gq[j] = *reinterpret_cast<const uint32_t*>(sgu + o);
+          uq[j] = *reinterpret_cast<const uint32_t*>(suu + o);
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < NV; ++p) {
+          const int r = 4 * p + g4;
+          *reinterpret_cast<uint4*>(sgu + r * 256 + ((q ^ r) << 4)) = gv[p];
+          *reinterpret_cast<uint4*>(suu + r * 256 + ((q ^ r) << 4)) = uv[p];
+        }
       }
       float ds = 0.f;
       u32x2 apk[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int o = q * 256 + (((2 * j + (g4 >> 1)) ^ q) << 4) + (g4 & 1) * 8;
-        const u32x2 G2 = *reinterpret_cast<const u32x2*>(sgu + o);
-        const u32x2 U2 = *reinterpret_cast<const u32x2*>(suu + o);
+        float G4[4], U4[4];
+        if constexpr (CK) {
+          ckpt_val4(gq[j], (int)((gs >> (8 * (j >> 1))) & 255u) - 127, G4);
+          ckpt_val4(uq[j], (int)((us >> (8 * (j >> 1))) & 255u) - 127, U4);
+        } else {
+          const u32x2 G2 = *reinterpret_cast<const u32x2*>(sgu + o);
+          const u32x2 U2 = *reinterpret_cast<const u32x2*>(suu + o);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint32_t gw = v < 2 ? G2.x : G2.y, uw = v < 2 ? U2.x : U2.y;
+            G4[v] = __uint_as_float((v & 1) ? (gw & 0xFFFF0000u) : (gw << 16));
+            U4[v] = __uint_as_float((v & 1) ? (uw & 0xFFFF0000u) : (uw << 16));
+          }
+        }
         float rg[4], ru[4], ra[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const uint32_t gw = v < 2 ? G2.x : G2.y, uw = v < 2 ? U2.x : U2.y;
-          const float gg_ = __uint_as_float((v & 1) ? (gw & 0xFFFF0000u) : (gw << 16));
-          const float u = __uint_as_float((v & 1) ? (uw & 0xFFFF0000u) : (uw << 16));
+          const float gg_ = G4[v], u = U4[v];
           const float sg = sigm(gg_);
           const float silu = gg_ * sg;
           const float act = silu * u;
@@ -887,7 +991,7 @@ __device__ __forceinline__ void mstep_wait(int later) {
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int KIND>
+template <int KIND, bool CK>
 __global__ __launch_bounds__(NT, 1) void k_gg_bf16(Args a, const int32_t* __restrict__ counts,
                                                    const int32_t* __restrict__ offsets) {
   a.counts = counts;
@@ -1214,7 +1318,7 @@ __global__ __launch_bounds__(NT, 1) void k_gg_bf16(Args a, const int32_t* __rest
           issue_step(Cn, 0, gs);
         }
       }
-      epilogue<KIND>(a, Cc, acc, wm, wn, L, S.nMg, st);
+      epilogue<KIND, CK>(a, Cc, acc, wm, wn, L, S.nMg, st);
 #pragma unroll
       for (int i = 0; i < G::MI; ++i)
 #pragma unroll
@@ -1339,27 +1443,30 @@ __global__ __launch_bounds__(NT, 1) void k_gg_bf16(Args a, const int32_t* __rest
 }  // namespace g4
 
 // ------------------------------------------------------------------ host side
-template <int KIND>
+template <int KIND, bool CK>
 hipError_t run_gemm_bf16(const gg::Args& a, long long max_tiles, hipStream_t s) {
   if (max_tiles <= 0) return hipSuccess;
+  constexpr int ID = !CK ? KIND : KIND == gg::GATEUP ? (int)MOE_K_GATEUP_CKPT : (int)MOE_K_DH_CKPT;
   const DevInfo d = dev_info();
   long long g = d.cus;
   if (max_tiles < g) g = max_tiles;
   g = (g + 7) / 8 * 8;
-  kernel_event(KIND, 0, s);
-  hipLaunchKernelGGL((g4::k_gg_bf16<KIND>), dim3((unsigned)g), dim3(g4::NT), 0, s, a, a.counts, a.offsets);
-  kernel_event(KIND, 1, s);
+  kernel_event(ID, 0, s);
+  hipLaunchKernelGGL((g4::k_gg_bf16<KIND, CK>), dim3((unsigned)g), dim3(g4::NT), 0, s, a, a.counts, a.offsets);
+  kernel_event(ID, 1, s);
   return hipGetLastError();
 }
 
-template hipError_t run_gemm_bf16<gg::GATEUP>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DOWN>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DH>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DX>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DWD>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DW1>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::GATEUP8>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DOWN8>(const gg::Args&, long long, hipStream_t);
-template hipError_t run_gemm_bf16<gg::DX8>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::GATEUP, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DOWN, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DH, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DX, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DWD, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DW1, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::GATEUP8, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DOWN8, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DX8, false>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::GATEUP, true>(const gg::Args&, long long, hipStream_t);
+template hipError_t run_gemm_bf16<gg::DH, true>(const gg::Args&, long long, hipStream_t);
 
 }  // namespace moe

@@ -35,6 +35,7 @@ struct Args {
   const void* wds;
   const void* acts;
   void* out2;
+  const void* hs;     // DH with [G | U] as codes (hcache): their scale codes; GATEUP writes them to out2
   const int32_t* counts;
   const int32_t* offsets;
   const int32_t* row_token;
@@ -68,8 +69,9 @@ __device__ __forceinline__ rsrc_t mkr_off(const void* p, long long byte_off, lon
 
 }  // namespace gg
 
-// bf16 grouped GEMM of kind KIND (gemm_bf16.hip); max_tiles bounds the tile count of the launch.
-template <int KIND>
+// bf16 grouped GEMM of kind KIND (gemm_bf16.hip); max_tiles bounds the tile count of the launch.  CK: [G | U]
+// as MX-FP8 codes (GATEUP writes, DH reads them).
+template <int KIND, bool CK = false>
 hipError_t run_gemm_bf16(const gg::Args& a, long long max_tiles, hipStream_t s);
 
 }  // namespace moe

@@ -131,4 +131,42 @@ hipError_t launch_quant_mxfp8(moe_dtype dt, const void* src, long long rows, int
   return hipGetLastError();
 }
 
+// The values that codes and scale codes stand for, in T: a thread per 16 codes (half a block).  code 2^(c - 127)
+// has 4 significant bits, so bf16 and fp32 hold it exactly from their smallest subnormal (2^-133, 2^-149) on.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc,
+                                                       long long n16, int K, int KS, T* __restrict__ out) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const int cpr = K / 16;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n16; i += (long long)gridDim.x * 256) {
+    const long long r = i / cpr;
+    const int c = (int)(i - r * cpr);
+    const uint4 u = reinterpret_cast<const uint4*>(q)[i];
+    const int e = (int)sc[r * KS + (c >> 1)] - 127;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+      const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+      store4(out + 16 * i + 4 * j, __builtin_amdgcn_ldexpf(lo.x, e), __builtin_amdgcn_ldexpf(lo.y, e),
+             __builtin_amdgcn_ldexpf(hi.x, e), __builtin_amdgcn_ldexpf(hi.y, e));
+    }
+  }
+}
+
+hipError_t launch_dequant_mxfp8(moe_dtype dt, const void* q, const void* scales, long long rows, int K, void* out,
+                                hipStream_t s) {
+  const int KS = 4 * ((K + 127) / 128);
+  const long long n = rows * (K / 16);
+  if (n == 0) return hipSuccess;
+  const unsigned grid = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
+  const uint8_t* qc = static_cast<const uint8_t*>(q);
+  const uint8_t* sc = static_cast<const uint8_t*>(scales);
+  if (dt == MOE_BF16)
+    hipLaunchKernelGGL(k_dequant_mxfp8<bf16_t>, dim3(grid), dim3(256), 0, s, qc, sc, n, K, KS, (bf16_t*)out);
+  else
+    hipLaunchKernelGGL(k_dequant_mxfp8<float>, dim3(grid), dim3(256), 0, s, qc, sc, n, K, KS, (float*)out);
+  return hipGetLastError();
+}
+
 }  // namespace moe

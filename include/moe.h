@@ -85,7 +85,8 @@ typedef enum moe_op {
   MOE_OP_LINEAR_FWD = 10,
   MOE_OP_LINEAR_BWD = 11,
   MOE_OP_LINEAR_CE_FWD = 12,
-  MOE_OP_LINEAR_CE_BWD = 13
+  MOE_OP_LINEAR_CE_BWD = 13,
+  MOE_OP_LAYER_BWD_CKPT8 = 14
 } moe_op;
 
 typedef enum moe_act {
@@ -504,6 +505,40 @@ moe_status moe_linear_bwd(moe_dtype dt, const void* dout, const void* x, const v
                           void* stream);
 
 /*
+ * The layer with its activation checkpoints in 8 bits.  hcache = [G | U], what the forward keeps of a
+ * layer for its backward, is held as MX-FP8 codes (the layout of moe_quantize_mxfp8), each half of a row by
+ * itself, so that no block mixes gate and up:
+ *   hq [M_cap, 2I]       row r: G's I codes, then U's
+ *   hs [M_cap, 2 KS(I)]  row r: G's scale codes (KS(I) = 4 ceil(I / 128), entries past I / 32 are 0), then U's
+ * (what moe_quantize_mxfp8 makes of the [2 M_cap, I] matrix of these halves): 33/32 bytes a value in place of 2.
+ *
+ * moe_grouped_gemm_fwd_ckpt8: moe_grouped_gemm_fwd for bf16 layers, with [G | U] written as codes from the fp32
+ * accumulators (one rounding); A and y come from the unrounded [G | U], bit for bit moe_grouped_gemm_fwd's.
+ * Rows >= M of hq, hs and y are not written.  Workspace: moe_workspace_bytes(MOE_OP_GEMM_FWD, MOE_BF16, ...).
+ *
+ * moe_layer_bwd_ckpt8: moe_layer_bwd for bf16 layers at the [G | U] that hq and hs stand for.  x is bf16 [N,H]
+ * (xs NULL), or e4m3 codes [N,H] with their scale codes xs [N, KS(H)], as moe_add_rmsnorm or moe_quantize_mxfp8 make
+ * them (16-byte aligned codes): dW_gate and dW_up are then taken at the values the codes stand for, in bf16 (exact from
+ * 2^-133 on).  Outputs, plans and errors as moe_layer_bwd.
+ * Workspace: moe_workspace_bytes(MOE_OP_LAYER_BWD_CKPT8, MOE_BF16, N, E, k, H, I, M_cap).
+ * Both: H a multiple of 8 (of 32 with xs), I a multiple of 32, hs 4-byte aligned.  The checkpoint is lossy: e4m3 has 4
+ * significant bits, so a value v of a block with largest magnitude m is off by at most 2^-4 |v| or m 2^-17.
+ * A NaN stays one in its place; an infinity becomes one, and its block's other values are rounded at scale 2^120.
+ *
+ * moe_dequantize_mxfp8: out [rows, K] (dtype dt) = the values that codes q [rows, K] and scale codes scales
+ * [rows, KS(K)] stand for, the inverse of moe_quantize_mxfp8.  K a positive multiple of 32; q and out 16-byte aligned.
+ */
+moe_status moe_grouped_gemm_fwd_ckpt8(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                                      int32_t H, int32_t I, const moe_plan* plan, uint8_t* hq, uint8_t* hs, void* y,
+                                      void* ws, size_t ws_bytes, void* stream);
+moe_status moe_layer_bwd_ckpt8(const void* dout, const void* x, const uint8_t* xs, const void* w_gate,
+                               const void* w_up, const void* w_down, int32_t H, int32_t I, const moe_plan* plan,
+                               const uint8_t* hq, const uint8_t* hs, void* dx, void* dw_gate, void* dw_up,
+                               void* dw_down, float* ds, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_dequantize_mxfp8(moe_dtype dt, const uint8_t* q, const uint8_t* scales, int64_t rows, int32_t K,
+                                void* out, void* stream);
+
+/*
  * Softmax cross entropy with a z-loss over a large vocabulary, straight from x and the output
  * projection w; the logits z = x w^T are formed piece by piece and never kept.  For token t with
  * target y = targets[t] in [0, V):
@@ -573,7 +608,10 @@ typedef enum moe_kernel_id {
   MOE_K_LINEAR_BWD = 25,      /* moe_linear_bwd: dz, dx, dw, dbias */
   MOE_K_LINEAR_CE = 26,       /* moe_linear_ce_fwd */
   MOE_K_LINEAR_CE_BWD = 27,   /* moe_linear_ce_bwd */
-  MOE_K_COUNT = 28
+  MOE_K_GATEUP_CKPT = 28,     /* moe_grouped_gemm_fwd_ckpt8: gate/up grouped GEMM that writes [G | U] as codes */
+  MOE_K_DH_CKPT = 29,         /* moe_layer_bwd_ckpt8: the dH kernel that reads them */
+  MOE_K_DEQUANT = 30,         /* moe_dequantize_mxfp8, and moe_layer_bwd_ckpt8's x */
+  MOE_K_COUNT = 31
 } moe_kernel_id;
 
 moe_status moe_set_kernel_events(int32_t kernel_id, void* start_event, void* stop_event);

@@ -110,3 +110,118 @@ def test_linear_ce_bindings():
         G.linear_ce_bwd(g.to(b), x, w, t, g)
     with pytest.raises(TypeError):
         G.linear_ce_bwd(g, x, w, t, g.to(b))
+
+
+def _plan(N=16, E=4, k=2, kind=G.PLAN_TOPK, mtile=0, **null):
+    cap = G.plan_rows_cap(kind, N, E, k, mtile)
+    f = dict(counts=FAKE, offsets=FAKE, row_token=FAKE, row_w=FAKE, row_pair=FAKE, tok_ptr=FAKE, tok_rows=FAKE)
+    f.update(null)
+    return G.CPlan(kind, N, E, k, cap, mtile, *f.values())
+
+
+def test_fwd_ckpt8_errors(L):
+    p = _plan()
+    need = L.moe_workspace_bytes(G.OP_GEMM_FWD, G.MOE_BF16, 16, 4, 2, 64, 96, p.M_cap)
+
+    def call(x=ptr(1), wg=ptr(2), wu=ptr(3), wd=ptr(4), H=64, I=96, plan=p, hq=ptr(5), hs=ptr(6), y=ptr(7), ws=ptr(8),
+             nb=need):
+        return L.moe_grouped_gemm_fwd_ckpt8(x, wg, wu, wd, H, I, None if plan is None else ctypes.byref(plan), hq, hs, y,
+                                            ws, nb, None)
+    assert call(I=0) == G.MOE_EINVAL
+    assert call(H=12) == G.MOE_EUNSUPPORTED
+    assert call(I=72) == G.MOE_EUNSUPPORTED             # blocks of 32
+    assert call(plan=None) == G.MOE_EINVAL
+    assert call(plan=_plan(counts=0)) == G.MOE_EINVAL
+    for n in ("x", "wg", "wu", "wd", "hq", "hs", "y", "ws"):
+        assert call(**{n: None}) == G.MOE_EINVAL, n
+    for n in ("x", "wg", "wu", "wd", "hq", "y", "ws"):
+        assert call(**{n: ODD}) == G.MOE_EUNSUPPORTED, n
+    assert call(hs=ctypes.c_void_p(FAKE + 2)) == G.MOE_EUNSUPPORTED
+    assert call(nb=need - 1) == G.MOE_EWORKSPACE
+    big = _plan(N=1 << 20)
+    assert call(plan=big, H=1024) == G.MOE_EUNSUPPORTED  # x of 2 GiB
+
+
+def test_bwd_ckpt8_errors(L):
+    p = _plan()
+    need = L.moe_workspace_bytes(G.OP_LAYER_BWD_CKPT8, G.MOE_BF16, 16, 4, 2, 64, 96, p.M_cap)
+    assert need > L.moe_workspace_bytes(G.OP_LAYER_BWD, G.MOE_BF16, 16, 4, 2, 64, 96, p.M_cap)
+    assert L.moe_workspace_bytes(G.OP_LAYER_BWD_CKPT8, G.MOE_BF16, 16, 4, 2, 64, 72, p.M_cap) == 0
+    assert L.moe_workspace_bytes(G.OP_LAYER_BWD_CKPT8, G.MOE_BF16, 16, 4, 2, 60, 96, p.M_cap) == 0
+
+    def call(dout=ptr(0), x=ptr(1), xs=None, wg=ptr(2), wu=ptr(3), wd=ptr(4), H=64, I=96, plan=p, hq=ptr(5), hs=ptr(6),
+             dx=ptr(7), dwg=ptr(8), dwu=ptr(9), dwd=ptr(10), ds=ptr(11), ws=ptr(12), nb=need):
+        return L.moe_layer_bwd_ckpt8(dout, x, xs, wg, wu, wd, H, I, None if plan is None else ctypes.byref(plan), hq, hs,
+                                     dx, dwg, dwu, dwd, ds, ws, nb, None)
+    assert call(I=72) == G.MOE_EUNSUPPORTED
+    assert call(H=72, xs=ptr(13)) == G.MOE_EUNSUPPORTED  # x as codes needs H % 32
+    assert call(plan=None) == G.MOE_EINVAL
+    for n in ("dout", "x", "wg", "wu", "wd", "hq", "hs", "dx", "dwg", "dwu", "dwd", "ds", "ws"):
+        assert call(**{n: None}) == G.MOE_EINVAL, n
+    for n in ("dout", "x", "wg", "wu", "wd", "hq", "dx", "dwg", "dwu", "dwd", "ws"):
+        assert call(**{n: ODD}) == G.MOE_EUNSUPPORTED, n
+    assert call(nb=need - 1) == G.MOE_EWORKSPACE
+
+
+def test_dequantize_errors(L):
+    def call(dt=G.MOE_BF16, q=ptr(1), s=ptr(2), rows=4, K=64, out=ptr(3)):
+        return L.moe_dequantize_mxfp8(dt, q, s, rows, K, out, None)
+    assert call(dt=5) == G.MOE_EUNSUPPORTED
+    assert call(rows=-1) == G.MOE_EINVAL
+    assert call(K=48) == G.MOE_EUNSUPPORTED
+    assert call(K=0) == G.MOE_EUNSUPPORTED
+    for n in ("q", "s", "out"):
+        assert call(**{n: None}) == G.MOE_EINVAL, n
+    assert call(q=ODD) == G.MOE_EUNSUPPORTED
+    assert call(out=ODD) == G.MOE_EUNSUPPORTED
+    assert call(rows=1 << 40) == G.MOE_EINVAL
+    assert call(rows=0, q=None, s=None, out=None) == G.MOE_OK
+
+
+def test_ckpt8_bindings():
+    b, u = torch.bfloat16, torch.uint8
+    plan = G.Plan(4, 3, 2, device="cpu")
+    x, wg, wd = torch.zeros(4, 64, dtype=b), torch.zeros(3, 32, 64, dtype=b), torch.zeros(3, 64, 32, dtype=b)
+    hq, hs = torch.zeros(8, 64, dtype=u), torch.zeros(8, 8, dtype=u)
+    xq, xs = torch.zeros(4, 64, dtype=u), torch.zeros(4, 4, dtype=u)
+
+    def fwd(x=x, wg=wg, wu=wg, wd=wd, plan=plan, **kw):
+        return G.grouped_gemm_fwd_ckpt8(x, wg, wu, wd, plan, **kw)
+
+    def bwd(dout=x, x=x, wg=wg, wu=wg, wd=wd, plan=plan, h=(hq, hs), **kw):
+        return G.layer_bwd_ckpt8(dout, x, wg, wu, wd, plan, h, **kw)
+    for f in (fwd, bwd):
+        with pytest.raises(ValueError, match="GPU"):
+            f()
+        with pytest.raises(TypeError):
+            f(x=x.float())
+        with pytest.raises(TypeError):
+            f(wd=wd.float())
+        with pytest.raises(ValueError):
+            f(x=x[:3])
+        with pytest.raises(ValueError):
+            f(wu=wg[:2])
+        with pytest.raises(ValueError):
+            f(wg=wg[0])
+        with pytest.raises(ValueError, match="experts"):
+            f(plan=G.Plan(4, 4, 2, device="cpu"))
+        with pytest.raises(ValueError, match="contiguous"):
+            f(x=torch.zeros(4, 128, dtype=b)[:, ::2])
+    with pytest.raises(ValueError, match="GPU"):
+        bwd(x=(xq, xs))
+    with pytest.raises(TypeError):
+        bwd(x=(x, xs))
+    with pytest.raises(ValueError):
+        bwd(x=(xq, xs[:, :2]))
+    with pytest.raises(ValueError):
+        bwd(h=(hq[:7], hs))
+    with pytest.raises(ValueError):
+        bwd(h=(hq, hs[:, :4].contiguous()))
+    with pytest.raises(TypeError):
+        bwd(h=(hq.to(b), hs))
+    with pytest.raises(ValueError, match="GPU"):
+        G.dequantize_mxfp8(xq, xs)
+    with pytest.raises(TypeError):
+        G.dequantize_mxfp8(x, xs)
+    with pytest.raises(ValueError):
+        G.dequantize_mxfp8(xq, xs[:, :3].contiguous())
