@@ -23,6 +23,7 @@ __all__ = [
     "balance_loss", "balance_loss_bwd", "OP_BALANCE_LOSS", "linear_fwd", "linear_bwd", "OP_LINEAR_FWD", "OP_LINEAR_BWD",
     "ACTIVATIONS", "linear_ce_fwd", "linear_ce_bwd", "OP_LINEAR_CE_FWD", "OP_LINEAR_CE_BWD",
     "dequantize_mxfp8", "grouped_gemm_fwd_ckpt8", "layer_bwd_ckpt8", "OP_LAYER_BWD_CKPT8",
+    "layer_few", "OP_LAYER_FEW", "FEW_MAX_TOKENS", "FEW_MAX_K",
 ]
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
@@ -37,6 +38,8 @@ OP_BALANCE_LOSS = 9
 OP_LINEAR_FWD, OP_LINEAR_BWD = 10, 11
 OP_LINEAR_CE_FWD, OP_LINEAR_CE_BWD = 12, 13
 OP_LAYER_BWD_CKPT8 = 14
+OP_LAYER_FEW = 15
+FEW_MAX_TOKENS, FEW_MAX_K = 64, 32  # limits of layer_few
 # activations of linear_fwd (moe_act in include/moe.h)
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -50,6 +53,7 @@ EXPORTED_SYMBOLS = (
     "moe_add_rmsnorm", "moe_add_rmsnorm_bwd", "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
     "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd",
     "moe_grouped_gemm_fwd_ckpt8", "moe_layer_bwd_ckpt8", "moe_dequantize_mxfp8",
+    "moe_layer_few", "moe_layer_few_mxfp8",
 )
 
 # kernel ids of the measurement hook (moe_kernel_id in include/moe.h)
@@ -58,7 +62,7 @@ KERNEL_IDS = {"gateup": 0, "down": 1, "dh": 2, "dx": 3, "dwd": 4, "dw1": 5, "com
               "router_dz": 13, "router_dx": 14, "router_dw": 15, "gateup_fp8": 16, "down_fp8": 17, "quant": 18,
               "dx_fp8": 19, "add_rmsnorm": 20, "add_rmsnorm_bwd": 21, "balance": 22,
               "balance_bwd": 23, "linear": 24, "linear_bwd": 25, "linear_ce": 26, "linear_ce_bwd": 27,
-              "gateup_ckpt": 28, "dh_ckpt": 29, "dequant": 30}
+              "gateup_ckpt": 28, "dh_ckpt": 29, "dequant": 30, "layer_few": 31}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -139,6 +143,8 @@ def load_library(path: str):
     L.moe_grouped_gemm_fwd_ckpt8.argtypes = [vp, vp, vp, vp, i32, i32, pp, vp, vp, vp, vp, sz, vp]
     L.moe_layer_bwd_ckpt8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, pp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.moe_dequantize_mxfp8.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int64, i32, vp, vp]
+    L.moe_layer_few.argtypes = [ctypes.c_int, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.moe_layer_few_mxfp8.argtypes = [vp] * 9 + [i32] * 5 + [vp, vp, vp, vp, sz, vp]
     for fn in ("moe_route_topk", "moe_permute", "moe_permute_noalloc", "moe_route_token_rounding",
                "moe_route_capacity",
                "moe_grouped_gemm_fwd",
@@ -147,7 +153,8 @@ def load_library(path: str):
                "moe_quantize_dx_weights_mxfp8", "moe_layer_bwd_mxfp8", "moe_add_rmsnorm", "moe_add_rmsnorm_bwd",
                "moe_balance_loss", "moe_balance_loss_bwd", "moe_router_bwd_acc",
                "moe_linear_fwd", "moe_linear_bwd", "moe_linear_ce_fwd", "moe_linear_ce_bwd",
-               "moe_grouped_gemm_fwd_ckpt8", "moe_layer_bwd_ckpt8", "moe_dequantize_mxfp8"):
+               "moe_grouped_gemm_fwd_ckpt8", "moe_layer_bwd_ckpt8", "moe_dequantize_mxfp8",
+               "moe_layer_few", "moe_layer_few_mxfp8"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -791,6 +798,54 @@ def linear_bwd(dout, x, w, z=None, act="none", want_dx=True, want_dw=True, want_
         _check(lib().moe_linear_bwd(dt, _addr(dout), _addr(x), _addr(w), _addr(z), code, N, K, O, _addr(dx), _addr(dw),
                                     _addr(dbias), _addr(ws), nb, _cur(dev)))
     return dict(dx=dx, dw=dw, dbias=dbias)
+
+
+@_on_stream
+def layer_few(x, w_r, w_gate, w_up, w_down, k: int, bias=None, out=None, topk_idx=None, topk_w=None, ws=None):
+    """The whole expert layer for at most FEW_MAX_TOKENS tokens: router product, top-k, gate/up with
+    SwiGLU, down and weighted sum.
+
+    x [N,H] bf16 or fp32; w_r fp32 [H,E], bias fp32 [E] or None (-inf leaves an expert out); w_gate, w_up [E,I,H]
+    and w_down [E,H,I] of x's type, or all three (codes, scale codes) from quantize_mxfp8 under bf16 x.
+    -> dict(out [N,H], topk_idx int32 [N,k], topk_w fp32 [N,k]).  stream: a torch stream to run on."""
+    torch = _torch
+    quant = isinstance(w_gate, (tuple, list))
+    mats = [("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)]
+    if any(isinstance(m, (tuple, list)) != quant for _, m in mats):
+        raise ValueError("w_gate, w_up and w_down must all be tensors or all (codes, scale codes)")
+    gate = w_gate[0] if quant else w_gate
+    if x.dim() != 2 or w_r.dim() != 2 or gate.dim() != 3:
+        raise ValueError("x must be [N, H], w_r [H, E], w_gate and w_up [E, I, H], w_down [E, H, I]")
+    N, H = x.shape
+    E, I = gate.shape[:2]
+    dt, ty = _dtype_code(x), x.dtype
+    if quant and dt != MOE_BF16:
+        raise TypeError(f"MX-FP8 weights need x in bfloat16 (got {ty})")
+    dev = x.get_device()
+    _want("x", x, (N, H), ty, dev)
+    _want("w_r", w_r, (H, E), torch.float32, dev)
+    if bias is not None:
+        _want("bias", bias, (E,), torch.float32, dev)
+    for name, m in mats:
+        shape = (E, H, I) if name == "w_down" else (E, I, H)
+        if quant:
+            _want(name + "'s codes", m[0], shape, torch.uint8, dev)
+            _want(name + "'s scale codes", m[1], shape[:2] + (mx_scale_cols(shape[2]),), torch.uint8, dev)
+        else:
+            _want(name, m, shape, ty, dev)
+    _on_gpu(x)
+    out = _out("out", out, (N, H), ty, x, dev)
+    topk_idx = _out("topk_idx", topk_idx, (N, k), torch.int32, x, dev)
+    topk_w = _out("topk_w", topk_w, (N, k), torch.float32, x, dev)
+    nb = _op_bytes(OP_LAYER_FEW, dt, N, E, k, H, I, 0)
+    ws = _op_ws(nb, x, ws, dev)
+    tail = (N, H, I, E, k, _addr(out), _addr(topk_idx), _addr(topk_w), _addr(ws), nb, _cur(dev))
+    if quant:
+        w = [_addr(t) for _, m in mats for t in m]
+        _check(lib().moe_layer_few_mxfp8(_addr(x), _addr(w_r), _addr(bias), *w, *tail))
+    else:
+        _check(lib().moe_layer_few(dt, _addr(x), _addr(w_r), _addr(bias), _addr(w_gate), _addr(w_up), _addr(w_down), *tail))
+    return dict(out=out, topk_idx=topk_idx, topk_w=topk_w)
 
 
 def _ckpt_layer(H, w_gate, w_up, w_down, plan, dev):

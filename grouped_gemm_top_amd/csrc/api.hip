@@ -129,6 +129,38 @@ moe_status check_linear(moe_dtype dt, int32_t N, int32_t K, int32_t O) {
   return MOE_OK;
 }
 
+// type and sizes of the layer for a few tokens; unit: what H and I are multiples of
+moe_status check_few(moe_dtype dt, int32_t N, int32_t H, int32_t I, int32_t E, int32_t k, int32_t unit) {
+  moe_status st;
+  if ((st = check_dtype(dt)) != MOE_OK) return st;
+  if ((st = check_dims(N, E, k)) != MOE_OK) return st;
+  REQUIRE(N <= MOE_FEW_MAX_TOKENS, MOE_EUNSUPPORTED, "N must be at most %d (got %d)", MOE_FEW_MAX_TOKENS, N);
+  REQUIRE(k <= MOE_FEW_MAX_K, MOE_EUNSUPPORTED, "k must be at most %d (got %d)", MOE_FEW_MAX_K, k);
+  REQUIRE(H >= unit && I >= unit, MOE_EINVAL, "H and I must be >= %d (got H=%d, I=%d)", unit, H, I);
+  REQUIRE(H % unit == 0 && I % unit == 0, MOE_EUNSUPPORTED, "H and I must be multiples of %d (got H=%d, I=%d)", unit, H,
+          I);
+  REQUIRE(H <= 1 << 20 && I <= 1 << 20, MOE_EUNSUPPORTED, "H and I must be at most 2^20 (got H=%d, I=%d)", H, I);
+  return MOE_OK;
+}
+
+// the arguments that both forms of the layer for a few tokens share
+moe_status check_few_args(moe_dtype dt, const void* x, const void* w_r, const void* bias, const void* wg,
+                          const void* wu, const void* wd, int32_t N, int32_t H, int32_t I, int32_t E, int32_t k,
+                          const void* out, const void* idx, const void* w, const void* ws, size_t ws_bytes) {
+  REQUIRE(w_r && wg && wu && wd, MOE_EINVAL, "NULL weight argument");
+  REQUIRE(N == 0 || (x && out && idx && w), MOE_EINVAL, "NULL x/out/topk_idx/topk_w");
+  REQUIRE(N == 0 || (out != x && idx != w && out != idx && out != w), MOE_EINVAL,
+          "out, topk_idx and topk_w must be no other argument");
+  REQUIRE(aligned16(x) && aligned16(wg) && aligned16(wu) && aligned16(wd) && aligned16(out) && aligned16(ws),
+          MOE_EUNSUPPORTED, "x, weights, out and workspace must be 16-byte aligned");
+  REQUIRE(aligned4(w_r) && aligned4(bias) && aligned4(idx) && aligned4(w), MOE_EUNSUPPORTED,
+          "w_r, bias, topk_idx and topk_w must be 4-byte aligned");
+  const size_t need = moe::layer_few_ws_bytes(dt, N, E, k, H, I);
+  REQUIRE(ws_bytes >= need, MOE_EWORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  REQUIRE(ws != nullptr, MOE_EINVAL, "NULL workspace");
+  return MOE_OK;
+}
+
 // type and sizes of the cross entropy: descriptors of 32-bit byte offsets over x and over a piece (256
 // columns at least) of dz and of w; launches of fewer than 2^32 threads
 moe_status check_ce(moe_dtype dt, int32_t N, int32_t H, int32_t V) {
@@ -247,6 +279,9 @@ size_t moe_workspace_bytes(moe_op op, moe_dtype dt, int32_t N, int32_t E, int32_
     case MOE_OP_LINEAR_CE_BWD:
       if (check_ce(dt, N, H, I) != MOE_OK) return 0;
       return moe::linear_ce_bwd_ws_bytes(dt, N, H, I);
+    case MOE_OP_LAYER_FEW:
+      if (check_few(dt, N, H, I, E, k, 8) != MOE_OK) return 0;
+      return moe::layer_few_ws_bytes(dt, N, E, k, H, I);
     case MOE_OP_ADD_RMSNORM_BWD: break;  // above
   }
   return 0;
@@ -806,6 +841,41 @@ moe_status moe_linear_ce_bwd(moe_dtype dt, const float* dloss, const void* x, co
       moe::launch_linear_ce_bwd(dt, dloss, x, w, targets, lse, N, H, V, z_coef, dx, dw, ws, (hipStream_t)stream);
   moe::kernel_event(MOE_K_LINEAR_CE_BWD, 1, (hipStream_t)stream);
   return hip_status(e, "moe_linear_ce_bwd");
+}
+
+moe_status moe_layer_few(moe_dtype dt, const void* x, const float* w_r, const float* bias, const void* w_gate,
+                         const void* w_up, const void* w_down, int32_t N, int32_t H, int32_t I, int32_t E, int32_t k,
+                         void* out, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_few(dt, N, H, I, E, k, 8)) != MOE_OK) return st;
+  if ((st = check_few_args(dt, x, w_r, bias, w_gate, w_up, w_down, N, H, I, E, k, out, topk_idx, topk_w, ws, ws_bytes)) !=
+      MOE_OK)
+    return st;
+  moe::kernel_event(MOE_K_LAYER_FEW, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_layer_few(dt, x, w_r, bias, w_gate, nullptr, w_up, nullptr, w_down, nullptr, N, H, I, E, k,
+                                       out, topk_idx, topk_w, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_LAYER_FEW, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_layer_few");
+}
+
+moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bias, const uint8_t* wg_q,
+                               const uint8_t* wg_s, const uint8_t* wu_q, const uint8_t* wu_s, const uint8_t* wd_q,
+                               const uint8_t* wd_s, int32_t N, int32_t H, int32_t I, int32_t E, int32_t k, void* out,
+                               int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  moe_status st;
+  if ((st = check_few(MOE_BF16, N, H, I, E, k, 32)) != MOE_OK) return st;
+  REQUIRE(wg_s && wu_s && wd_s, MOE_EINVAL, "NULL scale codes");
+  REQUIRE(aligned4(wg_s) && aligned4(wu_s) && aligned4(wd_s), MOE_EUNSUPPORTED, "scale codes must be 4-byte aligned");
+  if ((st = check_few_args(MOE_BF16, x, w_r, bias, wg_q, wu_q, wd_q, N, H, I, E, k, out, topk_idx, topk_w, ws,
+                           ws_bytes)) != MOE_OK)
+    return st;
+  moe::kernel_event(MOE_K_LAYER_FEW, 0, (hipStream_t)stream);
+  hipError_t e = moe::launch_layer_few(MOE_BF16, x, w_r, bias, wg_q, wg_s, wu_q, wu_s, wd_q, wd_s, N, H, I, E, k, out,
+                                       topk_idx, topk_w, ws, (hipStream_t)stream);
+  moe::kernel_event(MOE_K_LAYER_FEW, 1, (hipStream_t)stream);
+  return hip_status(e, "moe_layer_few_mxfp8");
 }
 
 }  // extern "C"

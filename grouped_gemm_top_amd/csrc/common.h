@@ -177,4 +177,9 @@ size_t layer_bwd_ckpt8_ws_bytes(int N, int M_cap, int H, int I);
 hipError_t launch_layer_bwd_ckpt8(const void* dout, const void* x, const void* xs, const void* wg, const void* wu,
                                   const void* wd, int H, int I, const moe_plan& p, const void* hq, const void* hs,
                                   void* dx, void* dwg, void* dwu, void* dwd, float* ds, void* ws, hipStream_t s);
+// the layer for a few tokens; gs, us, ds: scale codes of MX-FP8 weights (NULL: weights of type dt)
+size_t layer_few_ws_bytes(moe_dtype dt, int N, int E, int k, int H, int I);
+hipError_t launch_layer_few(moe_dtype dt, const void* x, const float* wr, const float* bias, const void* wg,
+                            const void* gs, const void* wu, const void* us, const void* wd, const void* ds, int N,
+                            int H, int I, int E, int k, void* out, int32_t* idx, float* w, void* ws, hipStream_t s);
 }  // namespace moe

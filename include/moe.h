@@ -86,7 +86,8 @@ typedef enum moe_op {
   MOE_OP_LINEAR_BWD = 11,
   MOE_OP_LINEAR_CE_FWD = 12,
   MOE_OP_LINEAR_CE_BWD = 13,
-  MOE_OP_LAYER_BWD_CKPT8 = 14
+  MOE_OP_LAYER_BWD_CKPT8 = 14,
+  MOE_OP_LAYER_FEW = 15
 } moe_op;
 
 typedef enum moe_act {
@@ -539,6 +540,33 @@ moe_status moe_dequantize_mxfp8(moe_dtype dt, const uint8_t* q, const uint8_t* s
                                 void* out, void* stream);
 
 /*
+ * The whole expert layer for a few tokens (decoding steps, verification of drafts): router product, top-k,
+ * gate/up with SwiGLU, down and weighted sum, without a plan.
+ *   z[t,e] = sum_h x[t,h] w_r[h,e] + bias[e]        (fp32; bias NULL: none, -inf leaves an expert out)
+ *   topk_idx[t,:], topk_w[t,:]: as moe_route_topk of z; a NaN z counts as -inf, an expert at -inf has weight 0
+ *   out[t] = sum_j topk_w[t,j] (silu(x[t] W_gate[e]^T) * (x[t] W_up[e]^T)) W_down[e]^T,  e = topk_idx[t,j]
+ * x, out [N,H]; w_r fp32 [H,E]; w_gate, w_up [E,I,H]; w_down [E,H,I] of dt; topk_idx int32, topk_w fp32 [N,k].
+ * The products accumulate in fp32; topk_w times the SwiGLU value is rounded to dt once, as the down product's operand.
+ * moe_layer_few_mxfp8 takes the weights as MX-FP8 codes and scale codes (w_gate and w_up quantized along H, w_down along
+ * I, as for moe_grouped_gemm_fwd_mxfp8) under bf16 x and out: the codes' values are the operands, exact in bf16; the
+ * activations are not quantized.
+ * 0 <= N <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= 1024, H and I multiples of 8 (codes: 32); x, weights,
+ * out and workspace 16-byte aligned, the rest 4-byte.  Only the matrices of the experts that some token names are
+ * read, once.  A token with NaN or infinities spoils its own outputs only.  Bitwise reproducible, and a token's
+ * topk_idx is what the call with that token alone gives wherever its logits differ by more than fp32's rounding.
+ * Workspace: moe_workspace_bytes(MOE_OP_LAYER_FEW, dt, N, E, k, H, I, 0) (the codes' form: MOE_BF16).
+ */
+#define MOE_FEW_MAX_TOKENS 64
+#define MOE_FEW_MAX_K 32
+moe_status moe_layer_few(moe_dtype dt, const void* x, const float* w_r, const float* bias, const void* w_gate,
+                         const void* w_up, const void* w_down, int32_t N, int32_t H, int32_t I, int32_t E, int32_t k,
+                         void* out, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bias, const uint8_t* wg_q,
+                               const uint8_t* wg_s, const uint8_t* wu_q, const uint8_t* wu_s, const uint8_t* wd_q,
+                               const uint8_t* wd_s, int32_t N, int32_t H, int32_t I, int32_t E, int32_t k, void* out,
+                               int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Softmax cross entropy with a z-loss over a large vocabulary, straight from x and the output
  * projection w; the logits z = x w^T are formed piece by piece and never kept.  For token t with
  * target y = targets[t] in [0, V):
@@ -611,7 +639,8 @@ typedef enum moe_kernel_id {
   MOE_K_GATEUP_CKPT = 28,     /* moe_grouped_gemm_fwd_ckpt8: gate/up grouped GEMM that writes [G | U] as codes */
   MOE_K_DH_CKPT = 29,         /* moe_layer_bwd_ckpt8: the dH kernel that reads them */
   MOE_K_DEQUANT = 30,         /* moe_dequantize_mxfp8, and moe_layer_bwd_ckpt8's x */
-  MOE_K_COUNT = 31
+  MOE_K_LAYER_FEW = 31,       /* moe_layer_few, moe_layer_few_mxfp8 */
+  MOE_K_COUNT = 32
 } moe_kernel_id;
 
 moe_status moe_set_kernel_events(int32_t kernel_id, void* start_event, void* stop_event);

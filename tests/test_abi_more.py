@@ -225,3 +225,77 @@ def test_ckpt8_bindings():
         G.dequantize_mxfp8(x, xs)
     with pytest.raises(ValueError):
         G.dequantize_mxfp8(xq, xs[:, :3].contiguous())
+
+
+def test_layer_few_errors(L):
+    need = L.moe_workspace_bytes(G.OP_LAYER_FEW, G.MOE_BF16, 16, 8, 2, 64, 96, 0)
+    assert need > 0 and L.moe_workspace_bytes(G.OP_LAYER_FEW, G.MOE_BF16, 0, 8, 2, 64, 96, 0) > 0
+    assert L.moe_workspace_bytes(G.OP_LAYER_FEW, G.MOE_BF16, 65, 8, 2, 64, 96, 0) == 0
+
+    def call(dt=G.MOE_BF16, x=ptr(1), wr=ptr(2), b=None, wg=ptr(3), wu=ptr(4), wd=ptr(5), N=16, H=64, I=96, E=8, k=2,
+             out=ptr(6), idx=ptr(7), w=ptr(8), ws=ptr(9), nb=need, sc=None):
+        if sc is None:
+            return L.moe_layer_few(dt, x, wr, b, wg, wu, wd, N, H, I, E, k, out, idx, w, ws, nb, None)
+        return L.moe_layer_few_mxfp8(x, wr, b, wg, sc, wu, sc, wd, sc, N, H, I, E, k, out, idx, w, ws, nb, None)
+    assert call(dt=4) == G.MOE_EUNSUPPORTED
+    for sc in (None, ptr(10)):
+        f = lambda **kw: call(sc=sc, **kw)  # noqa: E731,B023
+        assert f(N=-1) == G.MOE_EINVAL
+        assert f(N=65) == G.MOE_EUNSUPPORTED
+        assert f(E=0) == G.MOE_EINVAL
+        assert f(E=1025) == G.MOE_EINVAL
+        assert f(k=0) == G.MOE_EINVAL
+        assert f(k=9) == G.MOE_EINVAL
+        assert f(E=64, k=33) == G.MOE_EUNSUPPORTED
+        assert f(H=0) == G.MOE_EINVAL
+        assert f(I=100) == G.MOE_EUNSUPPORTED
+        assert f(H=1 << 21) == G.MOE_EUNSUPPORTED
+        for n in ("x", "wr", "wg", "wu", "wd", "out", "idx", "w", "ws"):
+            assert f(**{n: None}) == G.MOE_EINVAL, n
+        for n in ("x", "wg", "wu", "wd", "out", "ws"):
+            assert f(**{n: ODD}) == G.MOE_EUNSUPPORTED, n
+        for n in ("wr", "b", "idx", "w"):
+            assert f(**{n: ctypes.c_void_p(FAKE + 2)}) == G.MOE_EUNSUPPORTED, n
+        assert f(out=ptr(1)) == G.MOE_EINVAL        # out over x
+        assert f(idx=ptr(8)) == G.MOE_EINVAL        # topk_idx over topk_w
+        assert f(nb=need - 1) == G.MOE_EWORKSPACE
+        assert f(N=0, x=None, out=None, idx=None, w=None) == G.MOE_OK
+    assert call(sc=ptr(10), I=104, H=64) == G.MOE_EUNSUPPORTED    # codes: multiples of 32
+    assert call(sc=ctypes.c_void_p(FAKE + 2)) == G.MOE_EUNSUPPORTED
+    assert L.moe_layer_few_mxfp8(ptr(1), ptr(2), None, ptr(3), None, ptr(4), ptr(10), ptr(5), ptr(10), 16, 64, 96, 8, 2,
+                                 ptr(6), ptr(7), ptr(8), ptr(9), need, None) == G.MOE_EINVAL
+
+
+def test_layer_few_bindings():
+    b, u = torch.bfloat16, torch.uint8
+    x, wr = torch.zeros(4, 64, dtype=b), torch.zeros(64, 3)
+    wg, wd = torch.zeros(3, 32, 64, dtype=b), torch.zeros(3, 64, 32, dtype=b)
+    gq, dq = (torch.zeros(3, 32, 64, dtype=u), torch.zeros(3, 32, 4, dtype=u)), (torch.zeros(3, 64, 32, dtype=u),
+                                                                              torch.zeros(3, 64, 4, dtype=u))
+
+    def call(x=x, wr=wr, wg=wg, wu=wg, wd=wd, k=2, **kw):
+        return G.layer_few(x, wr, wg, wu, wd, k, **kw)
+    with pytest.raises(ValueError, match="GPU"):
+        call()
+    with pytest.raises(ValueError, match="GPU"):
+        call(wg=gq, wu=gq, wd=dq)
+    with pytest.raises(ValueError, match="all"):
+        call(wg=gq)
+    with pytest.raises(TypeError):
+        call(x=x.float(), wg=gq, wu=gq, wd=dq)
+    with pytest.raises(TypeError):
+        call(x=x.float())
+    with pytest.raises(TypeError):
+        call(wr=wr.to(b))
+    with pytest.raises(ValueError):
+        call(wr=wr[:, :2].contiguous())
+    with pytest.raises(ValueError):
+        call(bias=torch.zeros(4))
+    with pytest.raises(ValueError):
+        call(wd=wg)
+    with pytest.raises(ValueError):
+        call(wg=gq, wu=gq, wd=(dq[0], dq[1][:, :, :2].contiguous()))
+    with pytest.raises(ValueError):
+        call(x=x[0])
+    with pytest.raises(ValueError, match="contiguous"):
+        call(x=torch.zeros(4, 128, dtype=b)[:, ::2])
