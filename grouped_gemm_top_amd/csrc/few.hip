@@ -8,13 +8,19 @@
 // of the experts that any token names, E (1 - (1 - k/E)^N) of them, and everything else has to hide behind
 // that stream.  Launches:
 //  1. router product, sliced along H (fp32 on the vector units: 2 N H E operations are nothing here);
-//  2. gate/up: every workgroup joins the slices and chooses the experts itself (a few hundred logits: cheaper
-//     than a launch that hands the choice on), then takes tasks (expert, 16 columns of I).  Its eight wavefronts
+//  2. gate/up: every workgroup joins the slices and chooses the experts itself (beyond eight tokens a launch of
+//     its own does, a workgroup per token), then takes tasks (expert, 16 columns of I).  Its eight wavefronts
 //     split H, weights go straight from memory into registers as the matrix instruction's operand, and the
 //     sums meet in LDS; a' = w silu(g) u is rounded once, as the next product's operand;
-//  3. down: a workgroup owns 16 outputs of every token.  The other operand's columns are the tokens, zero for
-//     those that do not name the expert, so the sum over the experts is the matrix instruction's own
-//     accumulation: no scatter, no atomics, one fixed order.
+//  3. down: a workgroup owns 16 (or 8) outputs of every token, or a part of the experts for them; its
+//     wavefronts take the experts in turn and add each one's products to their tokens' sums in LDS.  No
+//     floating-point atomics, one fixed order.
+// One launch for 2 and 3, whose workgroups draw their tasks from a counter and where those of the down product wait
+// for gate/up's, took 57 us at N = 1 against 18: some hundred draws from one address, 40 ns each, are the time.
+//
+// Measured (E = 128, H = 2048, I = 512, k = 8): N = 1 20.7 us a call, launches 3.3 + 11.7 + 5.8.  51 MB take 10 us
+// at copy rate; the rest are three starts (2.7 each with nothing to do) and the choice (2).  N = 16, E = 256: 644 MB in
+// 116 us, 5.5 TB/s.  MX-FP8: N = 1 19.5, N = 24, E = 256, H = 4096, I = 256: 447 MB in 111.
 #include <type_traits>
 
 #include "gemm_lds.h"
@@ -26,6 +32,7 @@ using namespace gk;
 
 constexpr int MAXN = MOE_FEW_MAX_TOKENS, MAXK = MOE_FEW_MAX_K, MAXE = 1024;
 constexpr int NW = 8, NT = 64 * NW;  // wavefronts and threads of the two product kernels
+constexpr int MAXP = 4;  // parts of the down product
 
 struct Args {
   const void* x;
@@ -34,12 +41,15 @@ struct Args {
   const void *wg, *wu, *wd;
   const uint8_t *gs, *us, *ds;  // MX-FP8: scale codes
   int N, H, I, E, k;
-  int S, hs;      // slices of the router product and their length
-  float* part;    // [S, N, E]
-  void* act;      // a' [N k, I]: rows by expert, then token
-  int32_t* idx;   // [N, k]
-  float* w;       // [N, k]
-  void* out;      // [N, H]
+  int S, hs;         // slices of the router product and their length
+  int rb, P;         // outputs of a down workgroup (16 or 8) and parts of its sum
+  float* part;       // [S, N, E]
+  void* act;         // a' [N k, I]: rows by expert, then token (N = 1: by slot)
+  float* dpart;      // P > 1: [H / rb, P, N, 16]
+  unsigned* ticket;  // P > 1: [H / rb], zeroed by the router's launch
+  int32_t* idx;      // [N, k]
+  float* w;          // [N, k]
+  void* out;         // [N, H]
 };
 
 // ------------------------------------------------------------------ router product
@@ -52,28 +62,49 @@ __global__ __launch_bounds__(256) void k_few_router(Args a) {
   const int s = blockIdx.x, e = blockIdx.y * 64 + L, t0 = blockIdx.z * 16;
   const int lo = s * a.hs, len = max(0, min(a.hs, a.H - lo));
   const int nt = min(16, a.N - t0);
-  for (int q = threadIdx.x; q < 16 * 256; q += 256) {
-    const int t = q >> 8, h = q & 255;
-    s_x[t][h] = t < nt && h < len ? to_f32<T>(static_cast<const T*>(a.x)[(size_t)(t0 + t) * a.H + lo + h]) : 0.f;
+  if (a.ticket && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int q = s * 256 + threadIdx.x; q < (a.H + a.rb - 1) / a.rb; q += 256 * a.S) a.ticket[q] = 0;
+  // sixteen rows of w_r in flight, the first ones before x is staged
+  const float* wp = a.wr + (size_t)lo * a.E + min(e, a.E - 1);
+  float v[16];
+  auto fetch = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = h + j < len ? wp[(size_t)(h + j) * a.E] : 0.f;
+  };
+  fetch(16 * w);
+  // eight values of x a thread, two turns at most (a row's share ends with zeros: H and hs are multiples of 8)
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int q = threadIdx.x + 256 * u, t = q >> 5, h = (q & 31) * 8;
+    if (t < nt) {
+      float4 p[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      if (h < len) {
+        const T* src = static_cast<const T*>(a.x) + (size_t)(t0 + t) * a.H + lo + h;
+        load4(src, p[0].x, p[0].y, p[0].z, p[0].w);
+        load4(src + 4, p[1].x, p[1].y, p[1].z, p[1].w);
+      }
+      *reinterpret_cast<float4*>(&s_x[t][h]) = p[0];
+      *reinterpret_cast<float4*>(&s_x[t][h + 4]) = p[1];
+    }
   }
   __syncthreads();
   float acc[16];
 #pragma unroll
   for (int t = 0; t < 16; ++t) acc[t] = 0.f;
-  const float* wp = a.wr + (size_t)lo * a.E + min(e, a.E - 1);
-  for (int h = 4 * w; h < len; h += 16) {
-    float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = h + j < len ? wp[(size_t)(h + j) * a.E] : 0.f;
+  for (int h = 16 * w; h < len; h += 64) {
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
       if (t >= nt) break;
-      const float4 xv = *reinterpret_cast<const float4*>(&s_x[t][h]);
-      acc[t] = __builtin_fmaf(xv.x, v[0], acc[t]);
-      acc[t] = __builtin_fmaf(xv.y, v[1], acc[t]);
-      acc[t] = __builtin_fmaf(xv.z, v[2], acc[t]);
-      acc[t] = __builtin_fmaf(xv.w, v[3], acc[t]);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 xv = *reinterpret_cast<const float4*>(&s_x[t][h + j]);
+        acc[t] = __builtin_fmaf(xv.x, v[j], acc[t]);
+        acc[t] = __builtin_fmaf(xv.y, v[j + 1], acc[t]);
+        acc[t] = __builtin_fmaf(xv.z, v[j + 2], acc[t]);
+        acc[t] = __builtin_fmaf(xv.w, v[j + 3], acc[t]);
+      }
     }
+    if (h + 64 < len) fetch(h + 64);
   }
 #pragma unroll
   for (int t = 0; t < 16; ++t) s_p[w][t][L] = acc[t];
@@ -100,69 +131,162 @@ __device__ __forceinline__ float wave_max(float x) {
   return fmaxf(fmaxf(lane_f(x, 0), lane_f(x, 16)), fmaxf(lane_f(x, 32), lane_f(x, 48)));
 }
 
+// A token by one wavefront, from z[q] = the logit (without its bias) of expert L + 64 q: lane j < k gets slot j's
+// expert and weight.  A NaN logit counts as -inf; weights of experts at -inf are 0 (all of a token's, where it
+// has no other).
+template <int PL>  // experts per lane: E <= 64 PL
+__device__ __forceinline__ void choose_experts(const Args& a, float (&z)[PL], int L, int& my_e, float& my_w) {
+  uint32_t avail = 0;
+#pragma unroll
+  for (int q = 0; q < PL; ++q) {
+    if (L + 64 * q < a.E) avail |= 1u << q;
+    if (a.bias) z[q] += a.bias[min(L + 64 * q, a.E - 1)];
+    z[q] = z[q] == z[q] ? z[q] : -INFINITY;
+  }
+  float myz = -INFINITY, z0 = 0.f;
+  my_e = 0;
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < PL; ++q)
+      if ((avail >> q) & 1u) m = fmaxf(m, z[q]);
+    m = wave_max(m);
+    int e = 0;  // the lowest expert that has it (-0 and +0 tie)
+#pragma unroll
+    for (int q = PL - 1; q >= 0; --q) {
+      const unsigned long long b = __ballot(((avail >> q) & 1u) && z[q] == m);
+      if (b) e = 64 * q + __builtin_ctzll(b);
+    }
+    if ((e & 63) == L) avail &= ~(1u << (e >> 6));
+    if (L == j) myz = m, my_e = e;
+    if (j == 0) z0 = m;
+  }
+  const float zm = z0 == -INFINITY ? 0.f : z0;
+  const float ex = L < a.k ? expf(myz - zm) : 0.f;
+  float sum = ex;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+  my_w = sum == 0.f ? 0.f : ex / sum;
+}
+// z[q] += the slices s0, s0 + step, ... of token t
+template <int PL>
+__device__ __forceinline__ void join_slices(const Args& a, int t, int s0, int step, int L, float (&z)[PL]) {
+  constexpr int B = PL <= 2 ? 16 : PL <= 4 ? 8 : 4;  // in flight
+#pragma unroll 1
+  for (int i0 = s0; i0 < a.S; i0 += step * B) {
+    float v[PL][B];
+#pragma unroll
+    for (int q = 0; q < PL; ++q)
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        v[q][i] = a.part[((size_t)min(i0 + step * i, a.S - 1) * a.N + t) * a.E + min(L + 64 * q, a.E - 1)];
+#pragma unroll
+    for (int q = 0; q < PL; ++q)
+#pragma unroll
+      for (int i = 0; i < B; ++i) z[q] += i0 + step * i < a.S ? v[q][i] : 0.f;
+  }
+}
+
+// The choice as a launch of its own (more than CHOOSE_IN tokens): a workgroup per token, whose four wavefronts share
+// the slices.
+template <int PL>
+__global__ __launch_bounds__(256) void k_few_choose(Args a) {
+  __shared__ float s_z[4][64 * PL];
+  const int t = blockIdx.x, w = threadIdx.x >> 6, L = threadIdx.x & 63;
+  float z[PL], wt;
+#pragma unroll
+  for (int q = 0; q < PL; ++q) z[q] = 0.f;
+  join_slices<PL>(a, t, w, 4, L, z);
+#pragma unroll
+  for (int q = 0; q < PL; ++q) s_z[w][L + 64 * q] = z[q];
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int q = 0; q < PL; ++q) z[q] = (z[q] + s_z[1][L + 64 * q]) + (s_z[2][L + 64 * q] + s_z[3][L + 64 * q]);
+  int e;
+  choose_experts<PL>(a, z, L, e, wt);
+  if (L < a.k) {
+    a.idx[t * a.k + L] = e;
+    a.w[t * a.k + L] = wt;
+  }
+}
+
+// A single token: the eight wavefronts share the slices, then every expert's rank is counted against the others
+// (z descending, expert ascending), which takes no rounds one after the other.
+struct One {  // in LDS
+  __attribute__((aligned(16))) float z[NW][MAXE];
+  int rank[MAXE];
+  int e[MAXK];
+};
+template <int PL>
+__device__ __forceinline__ void choose_one(const Args& a, One& s, int w, int L) {
+  constexpr int EP = 64 * PL;
+  const int tid = threadIdx.x;
+  float z[PL];
+#pragma unroll
+  for (int q = 0; q < PL; ++q) z[q] = 0.f;
+  join_slices<PL>(a, 0, w, NW, L, z);
+#pragma unroll
+  for (int q = 0; q < PL; ++q) s.z[w][L + 64 * q] = z[q];
+  for (int e = tid; e < EP; e += NT) s.rank[e] = 0;
+  __syncthreads();
+  for (int e = tid; e < EP; e += NT) {
+    float v = s.z[0][e];
+#pragma unroll
+    for (int q = 1; q < NW; ++q) v += s.z[q][e];
+    if (a.bias && e < a.E) v += a.bias[e];
+    s.z[0][e] = v == v && e < a.E ? v : -INFINITY;
+  }
+  __syncthreads();
+  constexpr int PARTS = EP >= NT ? 1 : NT / EP, PER = EP / PARTS;
+  for (int q = tid; q < EP * PARTS; q += NT) {
+    const int e = q % EP, f0 = q / EP * PER;
+    const float ze = s.z[0][e];
+    int c = 0;
+    // (| and &: no branches.  What stands behind the last expert is -inf and behind everything.)
+#pragma unroll 4
+    for (int f = f0; f < f0 + PER; f += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(&s.z[0][f]);
+      c += (int)((v.x > ze) | ((v.x == ze) & (f < e)));
+      c += (int)((v.y > ze) | ((v.y == ze) & (f + 1 < e)));
+      c += (int)((v.z > ze) | ((v.z == ze) & (f + 2 < e)));
+      c += (int)((v.w > ze) | ((v.w == ze) & (f + 3 < e)));
+    }
+    if (PARTS == 1) s.rank[e] = c;
+    else atomicAdd(&s.rank[e], c);
+  }
+  __syncthreads();
+  for (int e = tid; e < a.E; e += NT)
+    if (s.rank[e] < a.k) s.e[s.rank[e]] = e;
+  __syncthreads();
+}
+// slot L's weight (lanes < k), from what choose_one left
+__device__ __forceinline__ float weight_one(const Args& a, const One& s, int L) {
+  const float z0 = s.z[0][s.e[0]], zm = z0 == -INFINITY ? 0.f : z0;
+  const float ex = L < a.k ? expf(s.z[0][s.e[L < a.k ? L : 0]] - zm) : 0.f;
+  float sum = ex;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+  return sum == 0.f ? 0.f : ex / sum;
+}
+
 struct Lists {  // in LDS
   unsigned long long mask[MAXE];  // the tokens that name an expert
-  int exp[MAXE], row[MAXE];       // active experts, ascending, and the first row of a' of each
-  int idx[MAXN * MAXK];
-  float w[MAXN * MAXK];
+  uint16_t exp[MAXE];             // active experts, ascending
+  uint16_t row[MAXE];             // an expert's first row of a'
+  uint16_t idx[MAXN * MAXK];      // [N, k]
+  uint8_t tok[MAXN * MAXK];       // a row's token
   int scan[NW];
   int n;                          // active experts
 };
 
-// Experts and weights of every token, a wavefront per token.  A NaN logit counts as -inf; weights of
-// experts at -inf are 0 (all of a token's, where it has no other).
-template <int PL>  // experts per lane: E <= 64 PL
-__device__ __forceinline__ void choose_experts(const Args& a, Lists& s, int w, int L) {
-  for (int t = w; t < a.N; t += NW) {
-    float z[PL];
-    uint32_t avail = 0;
-#pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      const int e = L + 64 * q, ec = min(e, a.E - 1);
-      const float* p = a.part + (size_t)t * a.E + ec;
-      float v = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < a.S; ++i) v += p[(size_t)i * a.N * a.E];
-      if (a.bias) v += a.bias[ec];
-      z[q] = v == v ? v : -INFINITY;
-      if (e < a.E) avail |= 1u << q;
-    }
-    float myz = -INFINITY, z0 = 0.f;
-    int mye = 0;
-    for (int j = 0; j < a.k; ++j) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int q = 0; q < PL; ++q)
-        if ((avail >> q) & 1u) m = fmaxf(m, z[q]);
-      m = wave_max(m);
-      int e = 0;  // the lowest expert that has it (-0 and +0 tie)
-#pragma unroll
-      for (int q = PL - 1; q >= 0; --q) {
-        const unsigned long long b = __ballot(((avail >> q) & 1u) && z[q] == m);
-        if (b) e = 64 * q + __builtin_ctzll(b);
-      }
-      if ((e & 63) == L) avail &= ~(1u << (e >> 6));
-      if (L == j) myz = m, mye = e;
-      if (j == 0) z0 = m;
-    }
-    const float zm = z0 == -INFINITY ? 0.f : z0;
-    const float ex = L < a.k ? expf(myz - zm) : 0.f;
-    float sum = ex;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-    if (L < a.k) {
-      s.idx[t * a.k + L] = mye;
-      s.w[t * a.k + L] = sum == 0.f ? 0.f : ex / sum;
-    }
-  }
-}
-
-// From s.idx: each expert's tokens, the active experts and the rows of a'.  Ends with a barrier.
+// From s.idx (behind a barrier): the experts' tokens and rows.  Ends with a barrier.
 __device__ __forceinline__ void make_lists(const Args& a, Lists& s, int w, int L) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, np = a.N * a.k;
   for (int e = tid; e < MAXE; e += NT) s.mask[e] = 0;
   __syncthreads();
-  for (int p = tid; p < a.N * a.k; p += NT) atomicOr(&s.mask[s.idx[p]], 1ull << (p / a.k));
+  for (int p = tid; p < np; p += NT) atomicOr(&s.mask[s.idx[p]], 1ull << (p / a.k));
   __syncthreads();
   const unsigned long long m0 = s.mask[2 * tid], m1 = s.mask[2 * tid + 1];
   // (active experts, rows) before this thread's two, packed
@@ -178,17 +302,16 @@ __device__ __forceinline__ void make_lists(const Args& a, Lists& s, int w, int L
   int before = v - c0 - c1;
 #pragma unroll
   for (int q = 0; q < NW; ++q) before += q < w ? s.scan[q] : 0;
-  if (m0) s.exp[before >> 16] = 2 * tid, s.row[before >> 16] = before & 0xFFFF;
+  if (m0) s.exp[before >> 16] = (uint16_t)(2 * tid), s.row[2 * tid] = (uint16_t)before;
   before += c0;
-  if (m1) s.exp[before >> 16] = 2 * tid + 1, s.row[before >> 16] = before & 0xFFFF;
+  if (m1) s.exp[before >> 16] = (uint16_t)(2 * tid + 1), s.row[2 * tid + 1] = (uint16_t)before;
   if (tid == NT - 1) s.n = (before + c1) >> 16;
   __syncthreads();
-}
-
-// the r-th set bit of m (r < popcount)
-__device__ __forceinline__ int nth_bit(unsigned long long m, int r) {
-  for (; r > 0; --r) m &= m - 1;
-  return __builtin_ctzll(m);
+  for (int p = tid; p < np; p += NT) {
+    const int t = p / a.k, e = s.idx[p];
+    s.tok[s.row[e] + __popcll(s.mask[e] & ((1ull << t) - 1))] = (uint8_t)t;
+  }
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------ operands
@@ -244,25 +367,23 @@ template <typename T, bool F8> struct Vec {
     }
   }
 };
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+// two e4m3 codes (the low or the high half of w) times the power of two x, in bf16
+template <bool HI>
+__device__ __forceinline__ uint32_t mx2(uint32_t w, float x) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, x, HI));
+}
 template <typename T, bool F8>
 __device__ __forceinline__ f32x4 line_mma(const Line<T, F8>& w, const Vec<T, F8>& x, f32x4 acc, int g) {
   if constexpr (F8) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // block 2 h + (g >> 1) of the line's four; a power of two
-      const int c = (int)((w.s >> (16 * h + 8 * (g >> 1))) & 255u);
+      // block 2 h + (g >> 1) of the line's four
+      const float c = __uint_as_float(((w.s >> (16 * h + 8 * (g >> 1))) & 255u) << 23);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t f[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t u = w.v[h][2 * q + j];
-          const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)u, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)u, true);
-          f[2 * j] = pk2(__builtin_amdgcn_ldexpf(lo.x, c - 127), __builtin_amdgcn_ldexpf(lo.y, c - 127));
-          f[2 * j + 1] = pk2(__builtin_amdgcn_ldexpf(hi.x, c - 127), __builtin_amdgcn_ldexpf(hi.y, c - 127));
-        }
-        acc = mma(__builtin_bit_cast(bf16x8, u32x4{f[0], f[1], f[2], f[3]}), __builtin_bit_cast(bf16x8, x.v[2 * h + q]), acc);
+        const uint32_t u0 = w.v[h][2 * q], u1 = w.v[h][2 * q + 1];
+        const u32x4 f = {mx2<false>(u0, c), mx2<true>(u0, c), mx2<false>(u1, c), mx2<true>(u1, c)};
+        acc = mma(__builtin_bit_cast(bf16x8, f), __builtin_bit_cast(bf16x8, x.v[2 * h + q]), acc);
       }
     }
   } else if constexpr (sizeof(T) == 2) {
@@ -281,39 +402,81 @@ __device__ __forceinline__ f32x4 line_mma(const Line<T, F8>& w, const Vec<T, F8>
 __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ------------------------------------------------------------------ gate / up
-// TB: blocks of 16 tokens (N <= 16 TB)
-template <typename T, bool F8, int PL, int TB>
-__global__ __launch_bounds__(NT, 2) void k_few_gateup(Args a) {
+// TB: blocks of 16 tokens (N <= 16 TB; 0: N = 1).  PL: experts per lane of the choice made here; 0: it was made
+// before.
+template <typename T, bool F8, int PL, int TB_>
+__global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
   using Ln = Line<T, F8>;
-  constexpr int U = F8 ? 2 : 4;  // k-steps in flight
-  __shared__ Lists s;
+  constexpr bool ONE = TB_ == 0;
+  constexpr int TB = ONE ? 1 : TB_;
+  // k-steps in flight: as many as 128 registers hold, for two workgroups a compute unit are worth more than
+  // longer bursts (N = 24 on MX-FP8 weights: 59 us with one step, 74 with four in twice the registers; N = 61 in
+  // fp32: 79 and 98)
+  constexpr int U = F8 ? (TB > 1 ? 1 : 2) : TB > 2 ? 1 : 4;
+  __shared__ typename std::conditional<ONE, One, Lists>::type s;
   __shared__ f32x4 s_sum[NW][2][64];
+  __shared__ float s_w[MAXN * MAXK];
   const int L = threadIdx.x & 63, w = ufl(threadIdx.x >> 6);
   const int r = L & 15, g = L >> 4;
-  choose_experts<PL>(a, s, w, L);
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int p = threadIdx.x; p < a.N * a.k; p += NT) {
-      a.idx[p] = s.idx[p];
-      a.w[p] = s.w[p];
+  int n = a.k;
+  if constexpr (ONE) {
+    choose_one<PL>(a, s, w, L);
+  } else {
+    if constexpr (PL > 0) {
+      for (int t = w; t < a.N; t += NW) {
+        int e;
+        float wt, z[PL];
+#pragma unroll
+        for (int q = 0; q < PL; ++q) z[q] = 0.f;
+        join_slices<PL>(a, t, 0, 1, L, z);
+        choose_experts<PL>(a, z, L, e, wt);
+        if (L < a.k) {
+          const int p = t * a.k + L;
+          s.idx[p] = (uint16_t)e;
+          s_w[p] = wt;
+          if (blockIdx.x == 0) {
+            a.idx[p] = e;
+            a.w[p] = wt;
+          }
+        }
+      }
+    } else {
+      for (int p = threadIdx.x; p < a.N * a.k; p += NT) {
+        s.idx[p] = (uint16_t)a.idx[p];
+        s_w[p] = a.w[p];
+      }
     }
-  make_lists(a, s, w, L);
-  const int IB = (a.I + 15) / 16, tasks = ufl(s.n) * IB;
+    __syncthreads();
+    make_lists(a, s, w, L);
+    n = ufl(s.n);
+  }
+  const int IB = (a.I + 15) / 16, tasks = n * IB;
   const int KS = 4 * ((a.H + 127) / 128);
   constexpr size_t ES = F8 ? 1 : sizeof(T);
   for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int ai = task / IB, i0 = (task - ai * IB) * 16, e = ufl(s.exp[ai]);
-    const unsigned long long m = s.mask[e];
-    const int cnt = __popcll(m), nb = ufl((cnt + 15) / 16);
+    const int ai = task / IB, i0 = (task - ai * IB) * 16;
+    int e, row0, cnt, nb;
+    if constexpr (ONE) {
+      e = ufl(s.e[ai]);
+      row0 = ai;
+      cnt = nb = 1;
+    } else {
+      e = ufl(s.exp[ai]);
+      row0 = ufl(s.row[e]);
+      cnt = ufl(__popcll(s.mask[e]));
+      nb = (cnt + 15) / 16;
+    }
     const size_t row = (size_t)e * a.I + min(i0 + r, a.I - 1);
     const char* pg = static_cast<const char*>(a.wg) + row * a.H * ES;
     const char* pu = static_cast<const char*>(a.wu) + row * a.H * ES;
     const uint8_t* sg = F8 ? a.gs + row * KS : nullptr;
     const uint8_t* su = F8 ? a.us + row * KS : nullptr;
-    const T* px[TB];
-#pragma unroll
-    for (int b = 0; b < TB; ++b)
-      px[b] = static_cast<const T*>(a.x) + (size_t)nth_bit(m, min(16 * b + r, cnt - 1)) * a.H;
+    auto x_row = [&](int b) __attribute__((always_inline)) {
+      const T* p = static_cast<const T*>(a.x);
+      if constexpr (!ONE) p += (size_t)s.tok[row0 + min(16 * b + r, cnt - 1)] * a.H;
+      return p;
+    };
+    const T* px = x_row(0);
     f32x4 ag[TB], au[TB];
 #pragma unroll
     for (int b = 0; b < TB; ++b) ag[b] = au[b] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -325,7 +488,19 @@ __global__ __launch_bounds__(NT, 2) void k_few_gateup(Args a) {
         const int k = k0 + u * NW * Ln::K;
         lg[u].load(pg, sg, k, a.H, g);
         lu[u].load(pu, su, k, a.H, g);
-        xv[u].load(px[0], k, a.H, g);
+        xv[u].load(px, k, a.H, g);
+      }
+      if constexpr (ONE) {  // the weights, while the first lines are on their way
+        if (w == 0 && k0 == 0 && task == (int)blockIdx.x) {
+          const float wt = weight_one(a, s, L);
+          if (L < a.k) {
+            s_w[L] = wt;
+            if (blockIdx.x == 0) {
+              a.idx[L] = s.e[L];
+              a.w[L] = wt;
+            }
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -335,10 +510,11 @@ __global__ __launch_bounds__(NT, 2) void k_few_gateup(Args a) {
 #pragma unroll
       for (int b = 1; b < TB; ++b) {
         if (b >= nb) break;
+        const T* pb = x_row(b);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           Vec<T, F8> xb;
-          xb.load(px[b], k0 + u * NW * Ln::K, a.H, g);
+          xb.load(pb, k0 + u * NW * Ln::K, a.H, g);
           ag[b] = line_mma(lg[u], xb, ag[b], g);
           au[b] = line_mma(lu[u], xb, au[b], g);
         }
@@ -360,11 +536,15 @@ __global__ __launch_bounds__(NT, 2) void k_few_gateup(Args a) {
         }
         const int slot = 16 * b + r, i = i0 + 4 * g;
         if (slot < cnt && i < a.I) {
-          const int t = nth_bit(m, slot);
           float wt = 0.f;
-          for (int j = 0; j < a.k; ++j)
-            if (s.idx[t * a.k + j] == e) wt = s.w[t * a.k + j];
-          T* o = static_cast<T*>(a.act) + (size_t)(s.row[ai] + slot) * a.I + i;
+          if constexpr (ONE) {
+            wt = s_w[ai];
+          } else {
+            const int t = s.tok[row0 + slot];
+            for (int j = 0; j < a.k; ++j)
+              if (s.idx[t * a.k + j] == e) wt = s_w[t * a.k + j];
+          }
+          T* o = static_cast<T*>(a.act) + (size_t)(row0 + slot) * a.I + i;
           store4(o, wt * silu(G[0]) * Uv[0], wt * silu(G[1]) * Uv[1], wt * silu(G[2]) * Uv[2], wt * silu(G[3]) * Uv[3]);
         }
       }
@@ -374,79 +554,143 @@ __global__ __launch_bounds__(NT, 2) void k_few_gateup(Args a) {
 }
 
 // ------------------------------------------------------------------ down
-template <typename T, bool F8, int TB>
-__global__ __launch_bounds__(NT, 2) void k_few_down(Args a) {
+// Part p of the outputs h0 .. h0 + rb - 1 of all tokens.  A unit is an expert's share of k-steps (all of them,
+// unless there are fewer experts than wavefronts); a wavefront takes every eighth unit of its part and adds each
+// unit's products to its own [token][output] sums in LDS; the wavefronts' and the parts' sums meet in order.
+template <typename T, bool F8, int TB_>
+__global__ __launch_bounds__(NT, 4) void k_few_down(Args a) {
   using Ln = Line<T, F8>;
-  constexpr int U = F8 ? 2 : 4;
-  __shared__ Lists s;
-  __shared__ f32x4 s_sum[NW][TB][64];
+  constexpr bool ONE = TB_ == 0;
+  constexpr int TB = ONE ? 1 : TB_;
+  constexpr int U = F8 || TB > 2 ? 2 : 4;  // k-steps in flight
+  __shared__ typename std::conditional<ONE, int, Lists>::type s;
+  __shared__ __attribute__((aligned(16))) float s_acc[NW][16 * TB][16];
+  __shared__ int s_last;
   const int L = threadIdx.x & 63, w = ufl(threadIdx.x >> 6);
   const int r = L & 15, g = L >> 4;
-  for (int p = threadIdx.x; p < a.N * a.k; p += NT) s.idx[p] = a.idx[p];
-  __syncthreads();
-  make_lists(a, s, w, L);
-  const int h0 = blockIdx.x * 16;
-  const int KS = 4 * ((a.I + 127) / 128), steps = (a.I + Ln::K - 1) / Ln::K, units = ufl(s.n) * steps;
+  for (int q = L; q < 16 * TB * 4; q += 64) *reinterpret_cast<f32x4*>(&s_acc[w][0][4 * q]) = f32x4{0.f, 0.f, 0.f, 0.f};
+  int n = a.k;
+  if constexpr (!ONE) {
+    for (int p = threadIdx.x; p < a.N * a.k; p += NT) s.idx[p] = (uint16_t)a.idx[p];
+    __syncthreads();
+    make_lists(a, s, w, L);
+    n = ufl(s.n);
+  }
+  const int hb = blockIdx.x / a.P, p = blockIdx.x - hb * a.P, h0 = hb * a.rb;
+  const int KS = 4 * ((a.I + 127) / 128), steps = (a.I + Ln::K - 1) / Ln::K;
+  const int split = max(1, min(steps, (NW * a.P + n - 1) / n)), units = n * split;
+  const int u_hi = (int)((long long)units * (p + 1) / a.P);
   constexpr size_t ES = F8 ? 1 : sizeof(T);
-  const int hr = min(h0 + r, a.H - 1);
-  f32x4 acc[TB];
+  const bool mine = r < a.rb && h0 + r < a.H;  // (rb = 8: half the lanes load, and half the sums are not used)
+  for (int un = (int)((long long)units * p / a.P) + w; un < u_hi; un += NW) {
+    const int ai = un / split, sp = un - ai * split;
+    int e, row0, cnt, nb;
+    if constexpr (ONE) {
+      e = ufl(a.idx[ai]);
+      row0 = ai;
+      cnt = nb = 1;
+    } else {
+      e = ufl(s.exp[ai]);
+      row0 = ufl(s.row[e]);
+      cnt = ufl(__popcll(s.mask[e]));
+      nb = (cnt + 15) / 16;
+    }
+    const int k_lo = steps * sp / split * Ln::K, k_hi = min(a.I, steps * (sp + 1) / split * Ln::K);
+    const size_t row = (size_t)e * a.H + h0 + (mine ? r : 0);
+    const char* pw = static_cast<const char*>(a.wd) + row * a.I * ES;
+    const uint8_t* sw = F8 ? a.ds + row * KS : nullptr;
+    const T* pa = static_cast<const T*>(a.act) + (size_t)(row0 + min(r, cnt - 1)) * a.I;
+    f32x4 d[TB];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int u0 = w; u0 < units; u0 += U * NW) {
-    Ln l[U];
-    Vec<T, F8> v[U][TB];
-    bool has[U][TB];
+    for (int b = 0; b < TB; ++b) d[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = k_lo; k0 < k_hi; k0 += U * Ln::K) {
+      Ln l[U];
+      Vec<T, F8> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int un = u0 + u * NW, ai = min(un / steps, s.n - 1);
-      const int k0 = un < units ? (un - ai * steps) * Ln::K : a.I;
-      const int e = ufl(s.exp[ai]);
-      const unsigned long long m = s.mask[e];
-      const size_t row = (size_t)e * a.H + hr;
-      l[u].load(static_cast<const char*>(a.wd) + row * a.I * ES, F8 ? a.ds + row * KS : nullptr, k0, a.I, g);
+      for (int u = 0; u < U; ++u) {
+        l[u].load(pw, sw, k0 + u * Ln::K, mine ? k_hi : 0, g);
+        v[u].load(pa, k0 + u * Ln::K, k_hi, g);
+      }
 #pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        const int t = 16 * b + r;
-        has[u][b] = (m >> t) & 1ull;
-        const T* p = static_cast<const T*>(a.act) + (size_t)(s.row[ai] + __popcll(m & ((1ull << t) - 1))) * a.I;
-        v[u][b].load(has[u][b] ? p : nullptr, k0, a.I, g);
+      for (int u = 0; u < U; ++u) d[0] = line_mma(l[u], v[u], d[0], g);
+#pragma unroll
+      for (int b = 1; b < TB; ++b) {
+        if (b >= nb) break;
+        const T* pb = static_cast<const T*>(a.act) + (size_t)(row0 + min(16 * b + r, cnt - 1)) * a.I;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Vec<T, F8> vb;
+          vb.load(pb, k0 + u * Ln::K, k_hi, g);
+          d[b] = line_mma(l[u], vb, d[b], g);
+        }
       }
     }
-    // (a step's products are added only where the token names the expert: an infinity or NaN among another
-    // expert's weights, times its zeros, would spoil every token)
+    // d[b][v] = output h0 + 4 g + v of the expert's token slot 16 b + r
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        const f32x4 d = line_mma(l[u], v[u][b], f32x4{0.f, 0.f, 0.f, 0.f}, g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[b][j] += has[u][b] ? d[j] : 0.f;
+    for (int b = 0; b < TB; ++b) {
+      if (16 * b + r < cnt) {
+        int t = 0;
+        if constexpr (!ONE) t = s.tok[row0 + 16 * b + r];
+        f32x4* q = reinterpret_cast<f32x4*>(&s_acc[w][t][4 * g]);
+        *q = *q + d[b];
       }
+    }
   }
-#pragma unroll
-  for (int b = 0; b < TB; ++b) s_sum[w][b][L] = acc[b];
   __syncthreads();
-  for (int b = w; b < TB; b += NW) {
-    f32x4 o = s_sum[0][b][L];
+  for (int q = threadIdx.x; q < a.N * 16; q += NT) {
+    const int t = q >> 4, o = q & 15;
+    float v = s_acc[0][t][o];
 #pragma unroll
-    for (int q = 1; q < NW; ++q) o += s_sum[q][b][L];
-    const int t = 16 * b + r, h = h0 + 4 * g;
-    if (t < a.N && h < a.H) store4(static_cast<T*>(a.out) + (size_t)t * a.H + h, o[0], o[1], o[2], o[3]);
+    for (int i = 1; i < NW; ++i) v += s_acc[i][t][o];
+    if (a.P == 1) {
+      if (o < a.rb && h0 + o < a.H) static_cast<T*>(a.out)[(size_t)t * a.H + h0 + o] = from_f32<T>(v);
+    } else {
+      __hip_atomic_store(&a.dpart[((size_t)blockIdx.x * a.N + t) * 16 + o], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (a.P == 1) return;
+  // The part that arrives last adds the parts in order.  Each share was stored with device scope and has
+  // arrived (the wait) before the workgroup's ticket is drawn, and is read with device scope.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    s_last = __hip_atomic_fetch_add(a.ticket + hb, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)a.P - 1;
+  __syncthreads();
+  if (!s_last) return;
+  for (int q = threadIdx.x; q < a.N * 16; q += NT) {
+    const int t = q >> 4, o = q & 15;
+    float v = 0.f, b[MAXP];
+#pragma unroll
+    for (int i = 0; i < MAXP; ++i)
+      b[i] = __hip_atomic_load(&a.dpart[(((size_t)hb * a.P + min(i, a.P - 1)) * a.N + t) * 16 + o], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int i = 0; i < MAXP; ++i) v += i < a.P ? b[i] : 0.f;
+    if (o < a.rb && h0 + o < a.H) static_cast<T*>(a.out)[(size_t)t * a.H + h0 + o] = from_f32<T>(v);
   }
 }
 
 // ------------------------------------------------------------------ host side
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
+constexpr int CHOOSE_IN = 8;  // tokens up to which the choice is made by every gate/up workgroup
 
-// slices of the router product: about 128 workgroups, 32 to 256 of H each
+// slices of the router product: 32 to 256 of H each, and no more than a lane joins with one round of loads
 void slices(int N, int H, int E, int& S, int& hs) {
-  const int others = ((E + 63) / 64) * (N > 16 ? (N + 15) / 16 : 1);
-  S = 128 / others;
-  if (S > 32) S = 32;
-  if (S > H / 32) S = H / 32;
+  const int most = N > CHOOSE_IN ? 64 : E <= 128 ? 32 : 16;
+  S = H / 32;
+  if (S > most) S = most;
   if (S < 1) S = 1;
   if (S < (H + 255) / 256) S = (H + 255) / 256;
   hs = ((H + S - 1) / S + 15) / 16 * 16;
+}
+
+// The down product's workgroups: 8 outputs each for few tokens, where the launch is a matter of latency and one
+// more join costs 3 us; else 16 and two workgroups a compute unit.
+void parts(int N, int H, int& rb, int& P) {
+  rb = N <= 2 && H < 4096 ? 8 : 16;
+  const int hb = (H + rb - 1) / rb, want = N <= 2 ? 128 : 512;
+  P = hb >= want ? 1 : (want + hb - 1) / hb;
+  if (P > MAXP) P = MAXP;
 }
 
 template <typename T, bool F8, int PL, int TB>
@@ -454,12 +698,21 @@ hipError_t run(const Args& a, hipStream_t s) {
   const dim3 gr(a.S, (a.E + 63) / 64, (a.N + 15) / 16);
   hipLaunchKernelGGL(k_few_router<T>, gr, dim3(256), 0, s, a);
   const long long act = a.E < a.N * a.k ? a.E : a.N * a.k, tasks = act * ((a.I + 15) / 16);
-  hipLaunchKernelGGL((k_few_gateup<T, F8, PL, TB>), dim3((unsigned)(tasks < 512 ? tasks : 512)), dim3(NT), 0, s, a);
-  hipLaunchKernelGGL((k_few_down<T, F8, TB>), dim3((a.H + 15) / 16), dim3(NT), 0, s, a);
+  const dim3 gg((unsigned)(tasks < 512 ? tasks : 512));
+  if (TB == 0) {
+    hipLaunchKernelGGL((k_few_gateup<T, F8, PL, 0>), gg, dim3(NT), 0, s, a);
+  } else if (TB == 1 && a.N <= CHOOSE_IN) {
+    hipLaunchKernelGGL((k_few_gateup<T, F8, PL, 1>), gg, dim3(NT), 0, s, a);
+  } else {
+    hipLaunchKernelGGL(k_few_choose<PL>, dim3(a.N), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_few_gateup<T, F8, 0, (TB > 0 ? TB : 1)>), gg, dim3(NT), 0, s, a);
+  }
+  hipLaunchKernelGGL((k_few_down<T, F8, TB>), dim3((a.H + a.rb - 1) / a.rb * a.P), dim3(NT), 0, s, a);
   return hipGetLastError();
 }
 template <typename T, bool F8, int PL>
 hipError_t run_tb(const Args& a, hipStream_t s) {
+  if (a.N == 1) return run<T, F8, PL, 0>(a, s);
   if (a.N <= 16) return run<T, F8, PL, 1>(a, s);
   if (a.N <= 32) return run<T, F8, PL, 2>(a, s);
   return run<T, F8, PL, 4>(a, s);
@@ -471,26 +724,41 @@ hipError_t run_pl(const Args& a, hipStream_t s) {
   return run_tb<T, F8, 16>(a, s);
 }
 
+struct Ws {
+  int S, hs, rb, P;
+  size_t part, act, dpart, ticket;
+  Ws(moe_dtype dt, int N, int E, int k, int H, int I) {
+    slices(N, H, E, S, hs);
+    parts(N, H, rb, P);
+    const int hb = (H + rb - 1) / rb;
+    part = up((size_t)S * N * E * 4);
+    act = up((size_t)N * k * I * (dt == MOE_BF16 ? 2 : 4));
+    dpart = P > 1 ? up((size_t)hb * P * N * 64) : 0;
+    ticket = P > 1 ? up((size_t)hb * 4) : 0;
+  }
+  size_t total() const { return 256 + part + act + dpart + ticket; }
+};
+
 }  // namespace fw
 
-size_t layer_few_ws_bytes(moe_dtype dt, int N, int E, int k, int H, int I) {
-  int S, hs;
-  fw::slices(N, H, E, S, hs);
-  return 256 + fw::up((size_t)S * N * E * 4) + fw::up((size_t)N * k * I * (dt == MOE_BF16 ? 2 : 4));
-}
+size_t layer_few_ws_bytes(moe_dtype dt, int N, int E, int k, int H, int I) { return fw::Ws(dt, N, E, k, H, I).total(); }
 
 hipError_t launch_layer_few(moe_dtype dt, const void* x, const float* wr, const float* bias, const void* wg,
                             const void* gs, const void* wu, const void* us, const void* wd, const void* ds, int N,
                             int H, int I, int E, int k, void* out, int32_t* idx, float* w, void* ws, hipStream_t s) {
   using namespace fw;
   if (N == 0) return hipSuccess;
+  const Ws b(dt, N, E, k, H, I);
   Args a{};
   a.x = x; a.wr = wr; a.bias = bias; a.wg = wg; a.wu = wu; a.wd = wd;
   a.gs = (const uint8_t*)gs; a.us = (const uint8_t*)us; a.ds = (const uint8_t*)ds;
   a.N = N; a.H = H; a.I = I; a.E = E; a.k = k; a.out = out; a.idx = idx; a.w = w;
-  slices(N, H, E, a.S, a.hs);
-  a.part = (float*)ws;
-  a.act = (char*)ws + up((size_t)a.S * N * E * 4);
+  a.S = b.S; a.hs = b.hs; a.rb = b.rb; a.P = b.P;
+  char* p = static_cast<char*>(ws);
+  a.part = (float*)p;
+  a.act = p + b.part;
+  a.dpart = (float*)(p + b.part + b.act);
+  a.ticket = b.P > 1 ? (unsigned*)(p + b.part + b.act + b.dpart) : nullptr;
   if (gs) return run_pl<bf16_t, true>(a, s);
   return dt == MOE_BF16 ? run_pl<bf16_t, false>(a, s) : run_pl<float, false>(a, s);
 }

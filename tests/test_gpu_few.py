@@ -225,6 +225,29 @@ def test_a_spoilt_token_and_a_spoilt_expert(kind):
     assert bool(torch.isnan(p["out"][names]).all())
 
 
+@pytest.mark.parametrize("code", [0, 1, 2, 9, 253])
+def test_smallest_and_largest_scales(code):
+    """W_down at the ends of the scale codes' range: its values are exact in bf16 down to 2^-133, out's in bf16 and fp32 too
+    (subnormals: half of 2^-133 is allowed for every rounding)."""
+    c = _case(9, 64, 64, 4, 2, "mxfp8", seed=29)
+    q, s = c["wd"]
+    q = (q & 0x87) | 0x08 if code == 253 else q  # (magnitudes below 2^-5: out stays finite)
+    c["wd"] = (q, torch.full_like(s, code))
+    c["wd"][1][:, :, 2:] = 0
+    o, _ = _run(c)
+    idx, w = o["topk_idx"].long(), o["topk_w"].double()
+    ref, size = torch.zeros(9, 64, dtype=torch.float64, device="cuda"), torch.zeros(9, 64, dtype=torch.float64, device="cuda")
+    x, wg, wu, wd = c["x"].double(), _val(c["wg"]), _val(c["wu"]), q.view(torch.float8_e4m3fn).double() * 2.0 ** (code - 127)
+    for t in range(9):
+        for j in range(2):
+            e = idx[t, j]
+            a = w[t, j] * torch.nn.functional.silu(wg[e] @ x[t]) * (wu[e] @ x[t])
+            ref[t] += wd[e] @ a
+            size[t] += wd[e].abs() @ a.abs()
+    # a' is off by 2^-8 and what its own factors are (below 2^-12 here), out by 2^-8 and the subnormals' steps of 64 * 2 terms
+    assert bool(((o["out"].double() - ref).abs() <= 2 ** -8 * ref.abs() + 1.07 * 2 ** -8 * size + 130 * 2.0 ** -134).all())
+
+
 def test_empty():
     import grouped_gemm_top_amd as G
     c = _case(1, 64, 32, 4, 2, "bf16")
