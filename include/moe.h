@@ -582,8 +582,8 @@ moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bia
  *   dx = dz w [N,H] (zero for tokens that take no part),  dw = dz^T x [V,H]      (NULL skips each)
  * z is formed again.  dz is rounded to MOE_BF16 for its two products, once (2^-8 of each value at most); MOE_F32
  * keeps fp32 accuracy throughout, by three bf16 parts an operand, with moe_linear_fwd's limits (infinities and
- * magnitudes from 3.38e38 on make their sums NaN).  Its working copy of dz is a piece of the vocabulary: at most
- * 128 MB (MOE_F32: 192 MB), or 256 columns where N is above 262144 (131072).
+ * magnitudes from 3.38e38 on make their sums NaN).  Its working copy of dz is one or two pieces of the vocabulary, each
+ * of at most 128 MB (MOE_F32: 192 MB), or 256 columns where N is above 262144 (131072).
  * A counted token with NaN or infinite logits spoils its own loss, lse and dx, and all of dw.
  * H a multiple of 8, V >= 1 (any); tensors and workspace 16-byte aligned, targets, loss, lse and dloss 4-byte;
  * N max(H, 256) elements below 2 GiB (MOE_F32: 2 GiB / 6 elements), 256 H likewise, N V at most 2^36; z_coef finite.
