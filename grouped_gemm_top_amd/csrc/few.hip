@@ -12,7 +12,7 @@
 //     its own does, a workgroup per token), then takes tasks (expert, 16 columns of I).  Its eight wavefronts
 //     split H, weights go straight from memory into registers as the matrix instruction's operand, and the
 //     sums meet in LDS; a' = w silu(g) u is rounded once, as the next product's operand;
-//  3. down: a workgroup owns 16 (or 8) outputs of every token, or a part of the experts for them; its
+//  3. down: a workgroup owns 8 to 16 outputs of every token, or a part of the experts for them; its
 //     wavefronts take the experts in turn and add each one's products to their tokens' sums in LDS.  No
 //     floating-point atomics, one fixed order.
 // One launch for 2 and 3, whose workgroups draw their tasks from a counter and where those of the down product wait
@@ -42,7 +42,7 @@ struct Args {
   const uint8_t *gs, *us, *ds;  // MX-FP8: scale codes
   int N, H, I, E, k;
   int S, hs;         // slices of the router product and their length
-  int rb, P;         // outputs of a down workgroup (16 or 8) and parts of its sum
+  int rb, P;         // outputs of a down workgroup (8 to 16) and parts of its sum
   float* part;       // [S, N, E]
   void* act;         // a' [N k, I]: rows by expert, then token (N = 1: by slot)
   float* dpart;      // P > 1: [H / rb, P, N, 16]
@@ -581,7 +581,7 @@ __global__ __launch_bounds__(NT, 4) void k_few_down(Args a) {
   const int split = max(1, min(steps, (NW * a.P + n - 1) / n)), units = n * split;
   const int u_hi = (int)((long long)units * (p + 1) / a.P);
   constexpr size_t ES = F8 ? 1 : sizeof(T);
-  const bool mine = r < a.rb && h0 + r < a.H;  // (rb = 8: half the lanes load, and half the sums are not used)
+  const bool mine = r < a.rb && h0 + r < a.H;  // (rb < 16: the other lanes load nothing, and their sums are not used)
   for (int un = (int)((long long)units * p / a.P) + w; un < u_hi; un += NW) {
     const int ai = un / split, sp = un - ai * split;
     int e, row0, cnt, nb;
@@ -684,13 +684,27 @@ void slices(int N, int H, int E, int& S, int& hs) {
   hs = ((H + S - 1) / S + 15) / 16 * 16;
 }
 
-// The down product's workgroups: 8 outputs each for few tokens, where the launch is a matter of latency and one
-// more join costs 3 us; else 16 and two workgroups a compute unit.
+// The down product's workgroups.  Few tokens, where the launch is a matter of latency and a join of parts costs 3
+// us: 8 outputs each, parts only where that leaves half the chip idle.  Else the most outputs (8 to 16) and parts (up to
+// MAXP) for which the fullest compute unit has least to do, two workgroups a unit where that is equal, and then the
+// most outputs, as a lane without one loads nothing (H = 1432, N = 61: 480 workgroups of 12 outputs in four parts 59
+// us, 480 of 9 in three 69, 360 of 16 67; H = 2048, N = 16, E = 256: 16 outputs in four parts 35, 8 in two 46).
 void parts(int N, int H, int& rb, int& P) {
-  rb = N <= 2 && H < 4096 ? 8 : 16;
-  const int hb = (H + rb - 1) / rb, want = N <= 2 ? 128 : 512;
-  P = hb >= want ? 1 : (want + hb - 1) / hb;
-  if (P > MAXP) P = MAXP;
+  if (N <= 2) {
+    rb = H < 4096 ? 8 : 16;
+    const int hb = (H + rb - 1) / rb;
+    P = hb >= 128 ? 1 : (128 + hb - 1) / hb;
+    if (P > MAXP) P = MAXP;
+    return;
+  }
+  double best = 1e30;
+  long long most = 0;  // workgroups of the best, 0 where they are more than two a unit
+  for (int p = MAXP; p >= 1; --p)
+    for (int r = 16; r >= 8; --r) {
+      const long long wg = (long long)((H + r - 1) / r) * p, fit = wg <= 512 ? wg : 0;
+      const double load = (double)((wg + 255) / 256) * r / p;
+      if (load < best || (load == best && fit > most)) best = load, most = fit, rb = r, P = p;
+    }
 }
 
 template <typename T, bool F8, int PL, int TB>
