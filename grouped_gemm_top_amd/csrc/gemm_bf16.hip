@@ -543,6 +543,26 @@ __device__ __forceinline__ uint4 stage_read(const char* st, int p, int L) {
 __device__ __forceinline__ void st16(rsrc_t r, uint32_t off, const uint4& v) {
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, 0);
 }
+// dSwiGLU of four values: d = dA', w the row's weight; dG, dU and A' as bf16, and their part of dS = <dA', A>
+__device__ __forceinline__ void dswiglu4(const float (&G)[4], const float (&U)[4], const f32x4& d, float w, float& ds,
+                                         u32x2& dg, u32x2& du, u32x2& ap) {
+  float rg[4], ru[4], ra[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float g = G[v], u = U[v];
+    const float sg = sigm(g);
+    const float silu = g * sg;
+    const float act = silu * u;
+    ds += d[v] * act;
+    const float da = w * d[v];
+    rg[v] = da * u * sg * (1.0f + g * (1.0f - sg));
+    ru[v] = da * silu;
+    ra[v] = w * act;
+  }
+  dg = u32x2{pk2(rg[0], rg[1]), pk2(rg[2], rg[3])};
+  du = u32x2{pk2(ru[0], ru[1]), pk2(ru[2], ru[3])};
+  ap = u32x2{pk2(ra[0], ra[1]), pk2(ra[2], ra[3])};
+}
 // [G | U] kept in 8 bits (the checkpoint form of hcache): codes [M_cap, 2I] and scale codes [M_cap, 2 KS(I)], each
 // half of a row laid out and quantized by itself as moe_quantize_mxfp8 does a row of I values.
 //
@@ -716,44 +736,109 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&a
     // goes to dspart[r nP + q] (nP = 2 ceil(I / 256)), summed in order by the next kernel.
     // Rows >= mlen and columns >= I lie past the descriptors' ranges: their loads read zeros
     // and their stores are dropped.
-    constexpr int HB = CK ? 1 : 2;  // bytes of a [G | U] value
-    const int KS = 4 * ((I + 127) / 128);
-    const rsrc_t rhc = gg::mkr_off(a.hcache, rb * 2 * I * HB, (long long)c.mlen * 2 * I * HB);
-    const rsrc_t rhs = gg::mkr_off(CK ? a.hs : a.hcache, CK ? rb * 2 * KS : 0, CK ? (long long)c.mlen * 2 * KS : 0);
     const rsrc_t rdh = gg::mkr_off(a.out0, rb * 2 * I * 2, (long long)c.mlen * 2 * I * 2);
     const rsrc_t rap = gg::mkr_off(a.out1, rb * I * 2, (long long)c.mlen * I * 2);
     const rsrc_t rw = gg::mkr_off(a.row_w, rb * 4, (long long)c.mlen * 4);
     const int nP = 2 * ((I + 255) / 256);
     const rsrc_t rds = gg::mkr_off(a.dspart, rb * nP * 4, (long long)c.mlen * nP * 4);
     const int c0 = c.nt * BN + wn * 128;
-    char* sgu = st;         // G, then dG, then A'
-    char* suu = st + 4096;  // U, then dU
     const int q = L & 15, g4 = L >> 4;
-    const int col = c0 + 8 * q;  // the 8 columns this lane moves in row-contiguous form
-    // (loading block i + 1's G and U during block i would keep 33 more registers live and
-    // pushes them into scratch, which made the epilogue twice as slow)
-    // As codes, G and U come in as rows of 128 bytes (8 lanes a row, placed as ckpt_store does), and a lane
-    // takes its 32 of each and its row's scale words into registers before dG and dU overwrite them.
-    constexpr int NV = CK ? 2 : 4;
-    uint4 gv[NV], uv[NV];
-    uint32_t gs = 0, us = 0;
-    float w = 0.f;
-    auto gu_load = [&](int i) __attribute__((always_inline)) {
-      if constexpr (CK) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint32_t m = (uint32_t)(16 * (4 * i + wm) + 8 * p + (L >> 3));
-          const int cc = c0 + 16 * (L & 7);
-          const uint32_t off = m * (uint32_t)(2 * I) + (uint32_t)cc;
-          gv[p] = gg::bld16(rhc, cc < I ? off : OOB);
-          uv[p] = gg::bld16(rhc, cc < I ? off + (uint32_t)I : OOB);
-        }
+    if constexpr (CK) {
+      // As codes, a block's G and U go straight into LDS (rows of 128 bytes, placed as ckpt_store does; 2 KB
+      // each) and the results leave 64 columns at a time through the other 4 KB.  The next block's are fetched as soon
+      // as the second half's codes are in registers: in front of that half's arithmetic and stores, so that the
+      // wait for them leaves its seven stores in flight.  (N = 4096, E = 128, H = 2048, I = 512, k = 8: 103 us, the
+      // bf16 form 107; H = I = 2880, N = 8192, k = 4: 967, 1053.  Through registers as in the bf16 form 123 and
+      // 1232: a block's loads waited for all stores before them, and 42 registers spilled.)
+      const int KS = 4 * ((I + 127) / 128);
+      const i32x4 rhc = sgpr4(dmadesc(static_cast<const char*>(a.hcache) + rb * 2 * I, (long long)c.mlen * 2 * I));
+      const rsrc_t rhs = gg::mkr_off(a.hs, rb * 2 * KS, (long long)c.mlen * 2 * KS);
+      char* sd = st + 4096;
+      const uint32_t sm = lds_addr(st);
+      const int r8 = L >> 3, q8 = L & 7;
+      uint32_t gs = 0, us = 0;
+      float w = 0.f;
+      auto fetch = [&](int i) __attribute__((always_inline)) {
         const uint32_t so = (uint32_t)(16 * (4 * i + wm) + q) * (uint32_t)(2 * KS) + (uint32_t)(c0 / 32);
         gs = (uint32_t)gg::bld4(rhs, c0 < I ? so : OOB);
         us = (uint32_t)gg::bld4(rhs, c0 < I ? so + (uint32_t)KS : OOB);
         w = __int_as_float(gg::bld4(rw, (uint32_t)(16 * (4 * i + wm) + q) * 4u));
-        return;
+        const int cc = c0 + 16 * (q8 ^ r8);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t off = (uint32_t)(16 * (4 * i + wm) + 8 * p + r8) * (uint32_t)(2 * I) + (uint32_t)cc;
+          dma16(rhc, sm + 1024u * p, cc < I ? off : OOB, 0u);
+          dma16(rhc, sm + 2048u + 1024u * p, cc < I ? off + (uint32_t)I : OOB, 0u);
+        }
+      };
+      fetch(0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (i == 0) vm_wait<0>();
+        else vm_wait<7>();
+        const float wi = w;
+        const uint32_t gsi = gs, usi = us;
+        float ds = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t gq[4], uq[4];
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const int o = q * 128 + (((4 * h + jj) ^ (q & 7)) << 4) + 4 * g4;
+            gq[jj] = *reinterpret_cast<const uint32_t*>(st + o);
+            uq[jj] = *reinterpret_cast<const uint32_t*>(st + 2048 + o);
+          }
+          if (h == 1 && i + 1 < MI) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            fetch(i + 1);
+          }
+          u32x2 apk[4];
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const int sh = 8 * (2 * h + (jj >> 1)), o = q * 128 + (((2 * jj + (g4 >> 1)) ^ (q & 7)) << 4) + 8 * (g4 & 1);
+            float G4[4], U4[4];
+            ckpt_val4(gq[jj], (int)((gsi >> sh) & 255u) - 127, G4);
+            ckpt_val4(uq[jj], (int)((usi >> sh) & 255u) - 127, U4);
+            u32x2 dg, du;
+            dswiglu4(G4, U4, acc[i][4 * h + jj], wi, ds, dg, du, apk[jj]);
+            *reinterpret_cast<u32x2*>(sd + o) = dg;
+            *reinterpret_cast<u32x2*>(sd + 2048 + o) = du;
+          }
+          const int col = c0 + 64 * h + 8 * q8;
+          auto row = [&](const char* s, int p) __attribute__((always_inline)) {
+            return *reinterpret_cast<const uint4*>(s + (8 * p + r8) * 128 + ((q8 ^ r8) << 4));
+          };
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t off = ((uint32_t)(16 * (4 * i + wm) + 8 * p + r8) * (uint32_t)(2 * I) + (uint32_t)col) * 2u;
+            st16(rdh, col < I ? off : OOB, row(sd, p));
+            st16(rdh, col < I ? off + (uint32_t)I * 2u : OOB, row(sd + 2048, p));
+          }
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+            *reinterpret_cast<u32x2*>(sd + q * 128 + (((2 * jj + (g4 >> 1)) ^ (q & 7)) << 4) + 8 * (g4 & 1)) = apk[jj];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t off = ((uint32_t)(16 * (4 * i + wm) + 8 * p + r8) * (uint32_t)I + (uint32_t)col) * 2u;
+            st16(rap, col < I ? off : OOB, row(sd, p));
+          }
+        }
+        ds += __shfl_xor(ds, 16);
+        ds += __shfl_xor(ds, 32);
+        const uint32_t doff = ((uint32_t)(16 * (4 * i + wm) + q) * (uint32_t)nP + (uint32_t)(2 * c.nt + wn)) * 4u;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(ds), rds, g4 == 0 ? doff : OOB, 0, 0);
       }
+      return;
+    }
+    const rsrc_t rhc = gg::mkr_off(a.hcache, rb * 2 * I * 2, (long long)c.mlen * 2 * I * 2);
+    char* sgu = st;         // G, then dG, then A'
+    char* suu = st + 4096;  // U, then dU
+    const int col = c0 + 8 * q;  // the 8 columns this lane moves in row-contiguous form
+    // (loading block i + 1's G and U during block i would keep 33 more registers live and
+    // pushes them into scratch, which made the epilogue twice as slow)
+    uint4 gv[4], uv[4];
+    float w = 0.f;
+    auto gu_load = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const uint32_t m = (uint32_t)(16 * (4 * i + wm) + 4 * p + g4);
@@ -767,64 +852,30 @@ __device__ __forceinline__ void epilogue(const Args& a, const Tile& c, f32x4 (&a
     for (int i = 0; i < MI; ++i) {
       gu_load(i);
       const float wi = w;
-      uint32_t gq[CK ? 8 : 1], uq[CK ? 8 : 1];
-      if constexpr (CK) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int r = 8 * p + (L >> 3), o = r * 128 + (((L & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(sgu + o) = gv[p];
-          *reinterpret_cast<uint4*>(suu + o) = uv[p];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int o = q * 128 + ((j ^ (q & 7)) << 4) + 4 * g4;
-          gq[j] = *reinterpret_cast<const uint32_t*>(sgu + o);
-          uq[j] = *reinterpret_cast<const uint32_t*>(suu + o);
-        }
-      } else {
-#pragma unroll
-        for (int p = 0; p < NV; ++p) {
-          const int r = 4 * p + g4;
-          *reinterpret_cast<uint4*>(sgu + r * 256 + ((q ^ r) << 4)) = gv[p];
-          *reinterpret_cast<uint4*>(suu + r * 256 + ((q ^ r) << 4)) = uv[p];
-        }
+      for (int p = 0; p < 4; ++p) {
+        const int r = 4 * p + g4;
+        *reinterpret_cast<uint4*>(sgu + r * 256 + ((q ^ r) << 4)) = gv[p];
+        *reinterpret_cast<uint4*>(suu + r * 256 + ((q ^ r) << 4)) = uv[p];
       }
       float ds = 0.f;
       u32x2 apk[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int o = q * 256 + (((2 * j + (g4 >> 1)) ^ q) << 4) + (g4 & 1) * 8;
+        const u32x2 G2 = *reinterpret_cast<const u32x2*>(sgu + o);
+        const u32x2 U2 = *reinterpret_cast<const u32x2*>(suu + o);
         float G4[4], U4[4];
-        if constexpr (CK) {
-          ckpt_val4(gq[j], (int)((gs >> (8 * (j >> 1))) & 255u) - 127, G4);
-          ckpt_val4(uq[j], (int)((us >> (8 * (j >> 1))) & 255u) - 127, U4);
-        } else {
-          const u32x2 G2 = *reinterpret_cast<const u32x2*>(sgu + o);
-          const u32x2 U2 = *reinterpret_cast<const u32x2*>(suu + o);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint32_t gw = v < 2 ? G2.x : G2.y, uw = v < 2 ? U2.x : U2.y;
-            G4[v] = __uint_as_float((v & 1) ? (gw & 0xFFFF0000u) : (gw << 16));
-            U4[v] = __uint_as_float((v & 1) ? (uw & 0xFFFF0000u) : (uw << 16));
-          }
-        }
-        float rg[4], ru[4], ra[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float gg_ = G4[v], u = U4[v];
-          const float sg = sigm(gg_);
-          const float silu = gg_ * sg;
-          const float act = silu * u;
-          const float d = acc[i][j][v];
-          ds += d * act;
-          const float da = wi * d;
-          rg[v] = da * u * sg * (1.0f + gg_ * (1.0f - sg));
-          ru[v] = da * silu;
-          ra[v] = wi * act;
+          const uint32_t gw = v < 2 ? G2.x : G2.y, uw = v < 2 ? U2.x : U2.y;
+          G4[v] = __uint_as_float((v & 1) ? (gw & 0xFFFF0000u) : (gw << 16));
+          U4[v] = __uint_as_float((v & 1) ? (uw & 0xFFFF0000u) : (uw << 16));
         }
-        *reinterpret_cast<u32x2*>(sgu + o) = u32x2{pk2(rg[0], rg[1]), pk2(rg[2], rg[3])};
-        *reinterpret_cast<u32x2*>(suu + o) = u32x2{pk2(ru[0], ru[1]), pk2(ru[2], ru[3])};
-        apk[j] = u32x2{pk2(ra[0], ra[1]), pk2(ra[2], ra[3])};
+        u32x2 dg, du;
+        dswiglu4(G4, U4, acc[i][j], wi, ds, dg, du, apk[j]);
+        *reinterpret_cast<u32x2*>(sgu + o) = dg;
+        *reinterpret_cast<u32x2*>(suu + o) = du;
       }
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
