@@ -56,80 +56,85 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   load4(p + 4, v[4], v[5], v[6], v[7]);
 }
 
-// A workgroup takes 32 tokens.  It counts the counted ones before them over all targets (a list of N / 32
-// counts would be another launch; at N = 8192 a workgroup reads 32 KB), then lists its own with their targets
+// A workgroup takes `groups` times 32 tokens.  It counts the counted ones before them over all targets (a list of
+// counts would be another launch; at N = 8192 a workgroup reads 32 KB, and beyond N = 65536 the workgroups are 2048, so
+// that all of them together read 4 KB a token at most), then, 32 at a time, lists its own with their targets
 // (BWD: with what dz needs) and copies their rows of x one behind the other (fp32: as three planes of N rows).  The
 // others' loss and lse (BWD: rows of dx, where wanted) are 0.
 template <typename T, bool BWD>
 __global__ __launch_bounds__(1024) void k_ce_select(const int* __restrict__ target, const T* __restrict__ x, int N, int H,
-                                                   int V, int* __restrict__ list, int* __restrict__ cnt,
+                                                   int V, int groups, int* __restrict__ list, int* __restrict__ cnt,
                                                    int* __restrict__ tgt, bf16_t* __restrict__ xc, float* __restrict__ loss,
                                                    float* __restrict__ lse_out, const float* __restrict__ lse,
                                                    const float* __restrict__ dloss, float zc, float4* __restrict__ info,
                                                    T* __restrict__ dx) {
   __shared__ int s_n[16], s_pos[32];
-  const int L = threadIdx.x & 63, w = threadIdx.x >> 6, t0 = blockIdx.x * 32;
+  const int L = threadIdx.x & 63, w = threadIdx.x >> 6, t_lo = blockIdx.x * groups * 32;
   int c = 0;
-  for (int t = threadIdx.x; t < t0; t += 4 * 1024) {
+  for (int t = threadIdx.x; t < t_lo; t += 4 * 1024) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c += t + 1024 * j < t0 && in_vocab(target[min(t + 1024 * j, t0 - 1)], V);
+    for (int j = 0; j < 4; ++j) c += t + 1024 * j < t_lo && in_vocab(target[min(t + 1024 * j, t_lo - 1)], V);
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) c += __shfl_xor(c, o);
   if (L == 0) s_n[w] = c;
   __syncthreads();
-  if (w == 0) {
-    int base = 0;
+  int base = 0;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) base += s_n[q];
-    const int t = t0 + L;
-    const bool mine = L < 32 && t < N;
-    const int y = mine ? target[t] : -1;
-    const unsigned long long live = __ballot(in_vocab(y, V));
-    const int p = base + __popcll(live & ((1ull << L) - 1));
-    if (L < 32) s_pos[L] = in_vocab(y, V) ? p : -1;
-    if (in_vocab(y, V)) {
-      list[p] = t;
-      tgt[p] = y;
-      if constexpr (BWD) {
-        const float l = lse[t], g = dloss ? dloss[t] : 1.0f;
-        info[p] = make_float4(l, g * (1.0f + 2.0f * zc * l), g, 0.f);
-      }
-    } else if (!BWD && mine) {
-      loss[t] = 0.f;
-      lse_out[t] = 0.f;
-    }
-    if (L == 0 && t0 + 32 >= N) *cnt = base + __popcll(live);
-  }
-  __syncthreads();
-  for (int r = w; r < 32 && t0 + r < N; r += 16) {
-    const int p = s_pos[r];
-    const T* src = x + (size_t)(t0 + r) * H;
-    if (p >= 0) {
-      bf16_t* dst = xc + (size_t)p * H;
-      for (int h0 = 8 * L; h0 < H; h0 += 4 * 512) {  // four loads in flight
-        if constexpr (sizeof(T) == 2) {
-          uint4 v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + min(h0 + 512 * q, H - 8));
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (h0 + 512 * q < H) *reinterpret_cast<uint4*>(dst + h0 + 512 * q) = v[q];
-        } else {
-          float v[4][8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) load8(src + min(h0 + 512 * q, H - 8), v[q]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (h0 + 512 * q < H) store_parts(dst + h0 + 512 * q, (size_t)N * H, v[q]);
+  for (int q = 0; q < 16; ++q) base += s_n[q];
+  for (int t0 = t_lo; t0 < N && t0 < t_lo + 32 * groups; t0 += 32) {
+    if (w == 0) {
+      const int t = t0 + L;
+      const bool mine = L < 32 && t < N;
+      const int y = mine ? target[t] : -1;
+      const unsigned long long live = __ballot(in_vocab(y, V));
+      const int p = base + __popcll(live & ((1ull << L) - 1));
+      if (L < 32) s_pos[L] = in_vocab(y, V) ? p : -1;
+      if (in_vocab(y, V)) {
+        list[p] = t;
+        tgt[p] = y;
+        if constexpr (BWD) {
+          const float l = lse[t], g = dloss ? dloss[t] : 1.0f;
+          info[p] = make_float4(l, g * (1.0f + 2.0f * zc * l), g, 0.f);
         }
+      } else if (!BWD && mine) {
+        loss[t] = 0.f;
+        lse_out[t] = 0.f;
       }
-    } else if (BWD && dx) {
-      for (int h = 8 * L; h < H; h += 512)
-#pragma unroll
-        for (int q = 0; q < (int)sizeof(T) / 2; ++q)
-          *reinterpret_cast<uint4*>(dx + (size_t)(t0 + r) * H + h + q * 16 / sizeof(T)) = make_uint4(0u, 0u, 0u, 0u);
+      base += __popcll(live);
+      if (L == 0 && t0 + 32 >= N) *cnt = base;
     }
+    __syncthreads();
+    for (int r = w; r < 32 && t0 + r < N; r += 16) {
+      const int p = s_pos[r];
+      const T* src = x + (size_t)(t0 + r) * H;
+      if (p >= 0) {
+        bf16_t* dst = xc + (size_t)p * H;
+        for (int h0 = 8 * L; h0 < H; h0 += 4 * 512) {  // four loads in flight
+          if constexpr (sizeof(T) == 2) {
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + min(h0 + 512 * q, H - 8));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (h0 + 512 * q < H) *reinterpret_cast<uint4*>(dst + h0 + 512 * q) = v[q];
+          } else {
+            float v[4][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load8(src + min(h0 + 512 * q, H - 8), v[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (h0 + 512 * q < H) store_parts(dst + h0 + 512 * q, (size_t)N * H, v[q]);
+          }
+        }
+      } else if (BWD && dx) {
+        for (int h = 8 * L; h < H; h += 512)
+#pragma unroll
+          for (int q = 0; q < (int)sizeof(T) / 2; ++q)
+            *reinterpret_cast<uint4*>(dx + (size_t)(t0 + r) * H + h + q * 16 / sizeof(T)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    __syncthreads();  // s_pos has been read
   }
 }
 
@@ -689,6 +694,10 @@ constexpr long long kDesc = 0x7FFFFFFF;
 
 int tile_n(int big) { return big == 2 ? 256 : big == 1 ? 128 : 64; }
 
+// groups of 32 tokens that a workgroup of k_ce_select takes
+int select_groups(int N) { return (N + 65535) / 65536; }
+unsigned select_grid(int N) { return (unsigned)((N + 32 * select_groups(N) - 1) / (32 * select_groups(N))); }
+
 // the tile of x W^T: no K slices (the epilogue needs whole sums)
 int z_tile(int N, int H, int V, int terms) {
   const int b = choose(K_FWD, N, V, H, terms, 1).big;
@@ -810,7 +819,8 @@ hipError_t fwd(const T* x, const T* w, const int* target, int N, int H, int V, f
   a.part = (float2*)take(b.part);
   bf16_t* xp = (bf16_t*)take(b.xp);
   bf16_t* wp = (bf16_t*)take(b.wp);
-  hipLaunchKernelGGL((k_ce_select<T, false>), dim3((N + 31) / 32), dim3(1024), 0, s, target, x, N, H, V, list, cnt, tgt,
+  hipLaunchKernelGGL((k_ce_select<T, false>), dim3(select_grid(N)), dim3(1024), 0, s, target, x, N, H, V,
+                     select_groups(N), list, cnt, tgt,
                      xp, loss, lse, (const float*)nullptr, (const float*)nullptr, zc, (float4*)nullptr, (T*)nullptr);
   a.cnt = cnt;
   a.tgt = tgt;
@@ -856,7 +866,8 @@ hipError_t bwd(const float* dloss, const T* x, const T* w, const int* target, co
     dz[i] = i && !b.two ? dz[0] : (bf16_t*)take(b.dz);
     wp[i] = i && !b.two ? wp[0] : (bf16_t*)take(b.wp);
   }
-  hipLaunchKernelGGL((k_ce_select<T, true>), dim3((N + 31) / 32), dim3(1024), 0, s, target, x, N, H, V, list, cnt, tgt,
+  hipLaunchKernelGGL((k_ce_select<T, true>), dim3(select_grid(N)), dim3(1024), 0, s, target, x, N, H, V,
+                     select_groups(N), list, cnt, tgt,
                      xc, (float*)nullptr, (float*)nullptr, lse, dloss, zc, info, dx);
   a.info = info;
   a.cnt = cnt;

@@ -152,6 +152,16 @@ def test_pieces_of_the_vocabulary(ty):
     _check(o, ref, bound)
 
 
+@TYPES
+def test_many_tokens(ty):
+    """More tokens than one group a workgroup lists: 140003 of them, a third without a target."""
+    N, H, V = 140003, 16, 40
+    c = _case(N, H, V, ty, 0.33, 1e-3, seed=12)
+    ref, bound = _exact(c)
+    o, _ = _run(c)
+    _check(o, ref, bound)
+
+
 def test_past_32_bits():
     """W of more than 2^31 elements and 2 GiB: forward pieces, offsets of W and dW past 32 bits.  The first
     and last rows alone are checked in full."""
