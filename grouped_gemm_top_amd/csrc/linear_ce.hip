@@ -164,7 +164,7 @@ enum { LSE = 0, DZ = 1 };
 // tiles have the same K.
 template <int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, bool F32>
 struct Pipe {
-  using C = Core<BM, BN, WM, WN, NST, AKC, BKC, F32>;
+  using C = Core<BM, BN, WM, WN, NST, AKC, BKC, F32, true>;
   typedef Op<BM, C::NW, AKC> OpA;
   typedef Op<BN, C::NW, BKC> OpB;
   static constexpr int MB = C::MB, NB = C::NB, NIA = OpA::NI, NI = NIA + OpB::NI;
@@ -194,9 +194,9 @@ struct Pipe {
     const bool live = lit >= 0;
     const int k0 = live ? lk : 0, klim = live ? K : 0;
     uint32_t pa = 0u, pb = 0u;
-    if constexpr (F32) {  // digits of the terms' parts, A: 0 0 1 1 0 2, B: 0 1 0 1 2 0
-      pa = live ? ((0x201100u >> (4 * lt)) & 3u) * A.plane : 0u;
-      pb = live ? ((0x021010u >> (4 * lt)) & 3u) * B.plane : 0u;
+    if constexpr (F32) {
+      pa = live ? ((C::DA >> (4 * lt)) & 3u) * A.plane : 0u;
+      pb = live ? ((C::DB >> (4 * lt)) & 3u) * B.plane : 0u;
     }
     if (q < NIA) oa.issue(q, m, A.ld, k0, klim, pa, w);
     else ob.issue(q - NIA, m + C::OPA, B.ld, k0, klim, pb, w);
@@ -461,7 +461,7 @@ __device__ __forceinline__ void z_tiles(const Args& a, int b, int G, char* s_rin
 }
 template <int BM, int BN, int WM, int WN, int NST, int EPI, bool F32>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_ce_z(Args a) {
-  using C = Core<BM, BN, WM, WN, NST, true, true, F32>;
+  using C = Core<BM, BN, WM, WN, NST, true, true, F32, true>;
   __shared__ __attribute__((aligned(1024))) char s_ring[NST * C::STG];
   __shared__ __attribute__((aligned(256))) char s_stage[C::NW * 2048];
   z_tiles<BM, BN, WM, WN, NST, EPI, F32>(a, blockIdx.x, gridDim.x, s_ring, s_stage);
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(1024) void k_ce_loss(const float2* __restrict__ par
 // dx = dz W of a piece: straight, or (S > 1) fp32 slices of its K range
 template <int BM, int BN, int WM, int WN, int NST, bool PART, bool F32>
 __device__ __forceinline__ void dx_tile(const Args& a, int b, char* s_ring) {
-  using C = Core<BM, BN, WM, WN, NST, true, false, F32>;
+  using C = Core<BM, BN, WM, WN, NST, true, false, F32, true>;
   typedef typename std::conditional<F32, float, bf16_t>::type T;
   constexpr int MB = C::MB, NB = C::NB;
   const int L = threadIdx.x & 63, w = ufl(threadIdx.x >> 6);
@@ -560,7 +560,7 @@ __device__ __forceinline__ void dx_tile(const Args& a, int b, char* s_ring) {
 
 template <int BM, int BN, int WM, int WN, int NST, bool PART, bool F32>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_ce_dx(Args a) {
-  __shared__ __attribute__((aligned(1024))) char s_ring[NST * Core<BM, BN, WM, WN, NST, true, false, F32>::STG];
+  __shared__ __attribute__((aligned(1024))) char s_ring[NST * Core<BM, BN, WM, WN, NST, true, false, F32, true>::STG];
   dx_tile<BM, BN, WM, WN, NST, PART, F32>(a, blockIdx.x, s_ring);
 }
 
@@ -650,7 +650,7 @@ __device__ __forceinline__ void dw_tiles(const Args& a, int b, int G, char* s_ri
 }
 template <int BM, int BN, int WM, int WN, int NST, bool PART, bool F32>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_ce_dw(Args a) {
-  using C = Core<BM, BN, WM, WN, NST, false, false, F32>;
+  using C = Core<BM, BN, WM, WN, NST, false, false, F32, true>;
   __shared__ __attribute__((aligned(1024))) char s_ring[NST * C::STG];
   __shared__ __attribute__((aligned(256))) char s_stage[C::NW * 4096];
   dw_tiles<BM, BN, WM, WN, NST, PART, F32>(a, blockIdx.x, gridDim.x, s_ring, s_stage);
@@ -661,7 +661,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_ce_dw(Args a) {
 // many short ones fill what they leave.
 template <bool F32>
 __global__ __launch_bounds__(512, 2) void k_ce_piece(Args p, Args z, int b_dx, int b_dw) {
-  __shared__ __attribute__((aligned(1024))) char s_ring[2 * Core<256, 256, 2, 4, 2, true, true, F32>::STG];
+  __shared__ __attribute__((aligned(1024))) char s_ring[2 * Core<256, 256, 2, 4, 2, true, true, F32, true>::STG];
   __shared__ __attribute__((aligned(256))) char s_stage[8 * 4096];
   const int b = blockIdx.x;
   if (b < b_dx) dx_tile<256, 256, 2, 4, 2, false, F32>(p, b, s_ring);
