@@ -698,9 +698,13 @@ int tile_n(int big) { return big == 2 ? 256 : big == 1 ? 128 : 64; }
 int select_groups(int N) { return (N + 65535) / 65536; }
 unsigned select_grid(int N) { return (unsigned)((N + 32 * select_groups(N) - 1) / (32 * select_groups(N))); }
 
-// the tile of x W^T: no K slices (the epilogue needs whole sums)
+// The tile of x W^T: choose's, without K slices (the epilogue needs whole sums); for up to 64 tokens 3 = 64 x 128
+// with three stages in place of 128 x 128 with two, as W's way from memory is the time then and twice as much of it is
+// on its way (N = 1, H = 2048, losses alone: V = 130001 118 us, 134 with two; V = 50021 55, 59; V <= 32000 equal).
+constexpr int kZm[4] = {64, 128, 256, 64}, kZn[4] = {64, 128, 256, 128};
 int z_tile(int N, int H, int V, int terms) {
   const int b = choose(K_FWD, N, V, H, terms, 1).big;
+  if (b == 1 && N <= 64) return 3;
   return b < 2 && (long long)((N + 63) / 64) * ((V + 63) / 64) > 1 << 20 ? 2 : b;
 }
 
@@ -729,7 +733,7 @@ struct FwdWs {
   FwdWs(bool f, int N, int H, int V) {
     vc = fwd_piece(f, H, V);
     tile = z_tile(N, H, vc, f ? 6 : 1);
-    const int bn = tile_n(tile);
+    const int bn = kZn[tile];
     tiles = (V + bn - 1) / bn;  // (a piece is a multiple of 256 unless it is the last)
     list = tgt = zt = up((size_t)N * 4);
     cnt = 256;
@@ -779,11 +783,12 @@ long long n_tiles(int M, int N, int bm, int bn) { return (long long)((M + bm - 1
 
 template <int EPI, bool F>
 void launch_z(const Args& a, int tile, hipStream_t s) {
-  const int b = tile_n(tile), room = tile == 2 ? 256 : 512;  // workgroups that fit at once
-  const unsigned all = grid8(n_tiles(a.N, a.V, b, b));
+  const int room = tile == 2 ? 256 : 512;  // workgroups that fit at once
+  const unsigned all = grid8(n_tiles(a.N, a.V, kZm[tile], kZn[tile]));
   const dim3 g(all < (unsigned)room ? all : (unsigned)room);
   if (tile == 2) hipLaunchKernelGGL((k_ce_z<256, 256, 2, 4, 2, EPI, F>), g, dim3(512), 0, s, a);
   else if (tile == 1) hipLaunchKernelGGL((k_ce_z<128, 128, 2, 2, 2, EPI, F>), g, dim3(256), 0, s, a);
+  else if (tile == 3) hipLaunchKernelGGL((k_ce_z<64, 128, 2, 2, 3, EPI, F>), g, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_ce_z<64, 64, 4, 1, 3, EPI, F>), g, dim3(256), 0, s, a);
 }
 template <bool PART, bool F>
@@ -830,7 +835,7 @@ hipError_t fwd(const T* x, const T* w, const int* target, int N, int H, int V, f
   for (int v0 = 0; v0 < V; v0 += b.vc) {
     a.v0 = v0;
     a.V = V - v0 < b.vc ? V - v0 : b.vc;
-    a.nt0 = v0 / tile_n(b.tile);
+    a.nt0 = v0 / kZn[b.tile];
     a.w = w + (size_t)v0 * H;
     if (F) {
       const size_t n = (size_t)a.V * H;

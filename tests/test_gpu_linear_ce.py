@@ -153,6 +153,15 @@ def test_pieces_of_the_vocabulary(ty):
 
 
 @TYPES
+@pytest.mark.parametrize("N,H,V,ign", [(1, 96, 60011, 0.0), (33, 328, 50021, 0.2), (64, 200, 33001, 0.0)])
+def test_few_tokens_large_vocabulary(N, H, V, ign, ty):
+    c = _case(N, H, V, ty, ign, 1e-3)
+    ref, bound = _exact(c)
+    o, _ = _run(c)
+    _check(o, ref, bound)
+
+
+@TYPES
 def test_many_tokens(ty):
     """More tokens than one group a workgroup lists: 140003 of them, a third without a target."""
     N, H, V = 140003, 16, 40
