@@ -576,7 +576,7 @@ __global__ __launch_bounds__(256) void k_ce_dx_sum(Args a) {
       v[0] = *reinterpret_cast<const f32x4*>(a.acc + 8 * i);
       v[1] = *reinterpret_cast<const f32x4*>(a.acc + 8 * i + 4);
     }
-#pragma unroll 4
+#pragma unroll 16
     for (int s = 0; s < a.S; ++s) {
       const float* p = a.slices + (size_t)s * slice + 8 * i;
       v[0] += *reinterpret_cast<const f32x4*>(p);
@@ -674,7 +674,7 @@ __global__ __launch_bounds__(256) void k_ce_dw_sum(Args a) {
   const size_t slice = (size_t)a.V * a.H, nv = slice / 8;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nv; i += (size_t)gridDim.x * 256) {
     f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 4
+#pragma unroll 16
     for (int s = 0; s < a.S; ++s) {
       const float* p = a.slices + (size_t)s * slice + 8 * i;
       v[0] += *reinterpret_cast<const f32x4*>(p);
@@ -744,9 +744,18 @@ struct FwdWs {
   size_t total() const { return 256 + list + tgt + cnt + zt + part + xp + wp; }
 };
 
+// Tile and K slices of dx and dW: the sum runs over a whole vocabulary or a whole batch while the output may be a
+// tile or two, so more than 16 slices as long as they go once into the chip (loss and gradients: N = 1, H = 96, V = 60011
+// fp32 121 us, 220 with 16; N = 100, H = 512, V = 100000 140, 151; N = 100000, H = 64, V = 100 178, 213; beyond that
+// the partial sums cost more: N = 300, H = 1024, V = 50021 188 with 32, 179).
+Shape sliced(Kind kind, int M, int N, int K, int terms) {
+  const long long tiles = (long long)((M + 127) / 128) * ((N + 127) / 128);
+  return choose(kind, M, N, K, terms, tiles <= 4 ? 64 : tiles <= 8 ? 32 : 16);
+}
+
 // whether all products of a piece run on the large tile without K slices
 bool mixes(int N, int H, int v, int terms) {
-  const Shape dx = choose(K_DX, N, H, v, terms), dw = choose(K_DW, v, H, N, terms);
+  const Shape dx = sliced(K_DX, N, H, v, terms), dw = sliced(K_DW, v, H, N, terms);
   return dx.big == 2 && dx.S == 1 && dw.big == 2 && dw.S == 1 && z_tile(N, H, v, terms) == 2;
 }
 
@@ -769,7 +778,7 @@ struct BwdWs {
     const int sizes[2] = {vc, V % vc};
     for (int p : sizes) {
       if (p == 0) continue;
-      const Shape dx = choose(K_DX, N, H, p, terms), dw = choose(K_DW, p, H, N, terms);
+      const Shape dx = sliced(K_DX, N, H, p, terms), dw = sliced(K_DW, p, H, N, terms);
       const size_t a = dx.S > 1 ? up((size_t)dx.S * N * H * 4) : 0, b = dw.S > 1 ? up((size_t)dw.S * p * H * 4) : 0;
       if (a > slices) slices = a;
       if (b > slices) slices = b;
@@ -912,7 +921,7 @@ hipError_t bwd(const float* dloss, const T* x, const T* w, const int* target, co
       hipLaunchKernelGGL((k_ce_piece<F>), dim3(g_dx + g_dw + g_z), dim3(512), 0, s, c, nx, (int)g_dx, (int)g_dw);
     } else {
       if (dx) {
-        const Shape h = choose(K_DX, N, H, c.V, terms);
+        const Shape h = sliced(K_DX, N, H, c.V, terms);
         c.S = h.S;
         if (h.S > 1) {
           launch_dx_tiles<true, F>(c, h.big, s);
@@ -922,7 +931,7 @@ hipError_t bwd(const float* dloss, const T* x, const T* w, const int* target, co
         }
       }
       if (dw) {
-        const Shape h = choose(K_DW, c.V, H, N, terms);
+        const Shape h = sliced(K_DW, c.V, H, N, terms);
         c.S = h.S;
         if (h.S > 1) {
           launch_dw_tiles<true, F>(c, h.big, s);
