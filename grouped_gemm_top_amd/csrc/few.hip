@@ -685,11 +685,14 @@ void slices(int N, int H, int E, int& S, int& hs) {
 }
 
 // The down product's workgroups.  Few tokens, where the launch is a matter of latency and a join of parts costs 3
-// us: 8 outputs each, parts only where that leaves half the chip idle.  Else the most outputs (8 to 16) and parts (up to
-// MAXP) for which the fullest compute unit has least to do, two workgroups a unit where that is equal, and then the
-// most outputs, as a lane without one loads nothing (H = 1432, N = 61: 480 workgroups of 12 outputs in four parts 59
-// us, 480 of 9 in three 69, 360 of 16 67; H = 2048, N = 16, E = 256: 16 outputs in four parts 35, 8 in two 46).
-void parts(int N, int H, int& rb, int& P) {
+// us: 8 outputs each, parts only where that leaves half the chip idle.  Else the outputs (8 to 16) and parts (up to
+// MAXP) with the least time of the fullest compute unit: its share of the matrices at 20 KB a us, and 4 us for each
+// turn of two workgroups (its lists, its join); where equal, the most workgroups, and then the most outputs, as a lane
+// without one loads nothing (H = 1432, N = 61: 480 workgroups of 12 outputs in four parts 59 us, 480 of 9 in three 69,
+// 360 of 16 67; H = 2048, N = 16, E = 256: 16 outputs in four parts 35, 8 in two 46; little to read, H = 3160, N = 26,
+// E = 9, I = 104: the call 29 us with 488 workgroups, 37 with 1264).
+// row: the bytes that an output takes from all experts' matrices
+void parts(int N, int H, double row, int& rb, int& P) {
   if (N <= 2) {
     rb = H < 4096 ? 8 : 16;
     const int hb = (H + rb - 1) / rb;
@@ -698,12 +701,12 @@ void parts(int N, int H, int& rb, int& P) {
     return;
   }
   double best = 1e30;
-  long long most = 0;  // workgroups of the best, 0 where they are more than two a unit
+  long long most = 0;
   for (int p = MAXP; p >= 1; --p)
     for (int r = 16; r >= 8; --r) {
-      const long long wg = (long long)((H + r - 1) / r) * p, fit = wg <= 512 ? wg : 0;
-      const double load = (double)((wg + 255) / 256) * r / p;
-      if (load < best || (load == best && fit > most)) best = load, most = fit, rb = r, P = p;
+      const long long wg = (long long)((H + r - 1) / r) * p;
+      const double t = (double)((wg + 255) / 256) * r / p * row / 20e3 + 4.0 * (double)((wg + 511) / 512);
+      if (t < best || (t == best && wg > most)) best = t, most = wg, rb = r, P = p;
     }
 }
 
@@ -743,7 +746,8 @@ struct Ws {
   size_t part, act, dpart, ticket;
   Ws(moe_dtype dt, int N, int E, int k, int H, int I) {
     slices(N, H, E, S, hs);
-    parts(N, H, rb, P);
+    // (MX-FP8 weights count as bf16's, so that one workspace serves both)
+    parts(N, H, (double)(E < N * k ? E : N * k) * I * (dt == MOE_BF16 ? 2 : 4), rb, P);
     const int hb = (H + rb - 1) / rb;
     part = up((size_t)S * N * E * 4);
     act = up((size_t)N * k * I * (dt == MOE_BF16 ? 2 : 4));
