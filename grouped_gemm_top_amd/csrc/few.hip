@@ -8,8 +8,8 @@
 // of the experts that any token names, E (1 - (1 - k/E)^N) of them, and everything else has to hide behind
 // that stream.  Launches:
 //  1. router product, sliced along H (fp32 on the vector units: 2 N H E operations are nothing here);
-//  2. gate/up: every workgroup joins the slices and chooses the experts itself (beyond eight tokens a launch of
-//     its own does, a workgroup per token), then takes tasks (expert, 16 columns of I).  Its eight wavefronts
+//  2. gate/up: for a single token every workgroup joins the slices and chooses the experts itself (for more a launch
+//     of its own does, a workgroup per token), then takes tasks (expert, 16 columns of I).  Its eight wavefronts
 //     split H, weights go straight from memory into registers as the matrix instruction's operand, and the
 //     sums meet in LDS; a' = w silu(g) u is rounded once, as the next product's operand;
 //  3. down: a workgroup owns 8 to 16 outputs of every token, or a part of the experts for them; its
@@ -20,7 +20,10 @@
 //
 // Measured (E = 128, H = 2048, I = 512, k = 8): N = 1 20.7 us a call, launches 3.3 + 11.7 + 5.8.  51 MB take 10 us
 // at copy rate; the rest are three starts (2.7 each with nothing to do) and the choice (2).  N = 16, E = 256: 644 MB in
-// 116 us, 5.5 TB/s.  MX-FP8: N = 1 19.5, N = 24, E = 256, H = 4096, I = 256: 447 MB in 111.
+// 115 us, 5.5 TB/s.  fp32, N = 61, E = 64, H = 1432, I = 520, k = 4: 562 MB in 152.  MX-FP8: N = 1 19, N = 24, E = 256,
+// H = 4096, I = 256: 447 MB in 112.  Beyond a token or two what is above the stream is the router and the choice (12 us)
+// and gate/up's last round of tasks (2112 over 512 workgroups: four rounds and an eighth); cutting that round's tasks along
+// H, with their parts joined by a ticket, cost 2 to 10 % on most shapes.
 #include <type_traits>
 
 #include "gemm_lds.h"
@@ -188,8 +191,9 @@ __device__ __forceinline__ void join_slices(const Args& a, int t, int s0, int st
   }
 }
 
-// The choice as a launch of its own (more than CHOOSE_IN tokens): a workgroup per token, whose four wavefronts share
-// the slices.
+// The choice as a launch of its own (more than one token): a workgroup per token, whose four wavefronts share the
+// slices.  (Made in every gate/up workgroup instead: N = 8, H = 4096, I = 256, E = 256, k = 2 43 us, 38 with the
+// launch; N = 4, H = 2048, I = 512, E = 128, k = 8 51.4, 51.8; N = 2 35.5, 35.9.)
 template <int PL>
 __global__ __launch_bounds__(256) void k_few_choose(Args a) {
   __shared__ float s_z[4][64 * PL];
@@ -402,8 +406,8 @@ __device__ __forceinline__ f32x4 line_mma(const Line<T, F8>& w, const Vec<T, F8>
 __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ------------------------------------------------------------------ gate / up
-// TB: blocks of 16 tokens (N <= 16 TB; 0: N = 1).  PL: experts per lane of the choice made here; 0: it was made
-// before.
+// TB: blocks of 16 tokens (N <= 16 TB; 0: N = 1).  PL: experts per lane of the choice, which is made here for a single
+// token (0: it was made before).
 template <typename T, bool F8, int PL, int TB_>
 __global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
   using Ln = Line<T, F8>;
@@ -422,29 +426,9 @@ __global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
   if constexpr (ONE) {
     choose_one<PL>(a, s, w, L);
   } else {
-    if constexpr (PL > 0) {
-      for (int t = w; t < a.N; t += NW) {
-        int e;
-        float wt, z[PL];
-#pragma unroll
-        for (int q = 0; q < PL; ++q) z[q] = 0.f;
-        join_slices<PL>(a, t, 0, 1, L, z);
-        choose_experts<PL>(a, z, L, e, wt);
-        if (L < a.k) {
-          const int p = t * a.k + L;
-          s.idx[p] = (uint16_t)e;
-          s_w[p] = wt;
-          if (blockIdx.x == 0) {
-            a.idx[p] = e;
-            a.w[p] = wt;
-          }
-        }
-      }
-    } else {
-      for (int p = threadIdx.x; p < a.N * a.k; p += NT) {
-        s.idx[p] = (uint16_t)a.idx[p];
-        s_w[p] = a.w[p];
-      }
+    for (int p = threadIdx.x; p < a.N * a.k; p += NT) {
+      s.idx[p] = (uint16_t)a.idx[p];
+      s_w[p] = a.w[p];
     }
     __syncthreads();
     make_lists(a, s, w, L);
@@ -672,11 +656,10 @@ __global__ __launch_bounds__(NT, 4) void k_few_down(Args a) {
 
 // ------------------------------------------------------------------ host side
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
-constexpr int CHOOSE_IN = 8;  // tokens up to which the choice is made by every gate/up workgroup
 
 // slices of the router product: 32 to 256 of H each, and no more than a lane joins with one round of loads
 void slices(int N, int H, int E, int& S, int& hs) {
-  const int most = N > CHOOSE_IN ? 64 : E <= 128 ? 32 : 16;
+  const int most = N > 1 ? 64 : E <= 128 ? 32 : 16;
   S = H / 32;
   if (S > most) S = most;
   if (S < 1) S = 1;
@@ -716,13 +699,11 @@ hipError_t run(const Args& a, hipStream_t s) {
   hipLaunchKernelGGL(k_few_router<T>, gr, dim3(256), 0, s, a);
   const long long act = a.E < a.N * a.k ? a.E : a.N * a.k, tasks = act * ((a.I + 15) / 16);
   const dim3 gg((unsigned)(tasks < 512 ? tasks : 512));
-  if (TB == 0) {
+  if constexpr (TB == 0) {
     hipLaunchKernelGGL((k_few_gateup<T, F8, PL, 0>), gg, dim3(NT), 0, s, a);
-  } else if (TB == 1 && a.N <= CHOOSE_IN) {
-    hipLaunchKernelGGL((k_few_gateup<T, F8, PL, 1>), gg, dim3(NT), 0, s, a);
   } else {
     hipLaunchKernelGGL(k_few_choose<PL>, dim3(a.N), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_few_gateup<T, F8, 0, (TB > 0 ? TB : 1)>), gg, dim3(NT), 0, s, a);
+    hipLaunchKernelGGL((k_few_gateup<T, F8, 0, TB>), gg, dim3(NT), 0, s, a);
   }
   hipLaunchKernelGGL((k_few_down<T, F8, TB>), dim3((a.H + a.rb - 1) / a.rb * a.P), dim3(NT), 0, s, a);
   return hipGetLastError();
