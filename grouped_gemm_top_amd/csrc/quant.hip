@@ -131,25 +131,38 @@ hipError_t launch_quant_mxfp8(moe_dtype dt, const void* src, long long rows, int
   return hipGetLastError();
 }
 
-// The values that codes and scale codes stand for, in T: a thread per 16 codes (half a block).  code 2^(c - 127)
-// has 4 significant bits, so bf16 and fp32 hold it exactly from their smallest subnormal (2^-133, 2^-149) on.
+// The values that codes and scale codes stand for, in T: a thread per 8 codes, so that a wavefront's loads and stores
+// are whole lines (16 a thread: N = 8192, K = 2880 to bf16, 71 MB, 21 us; this 14, 5.1 TB/s).  code 2^(c - 127) has 4 significant
+// bits, so bf16 and fp32 hold it exactly from their smallest subnormal (2^-133, 2^-149) on.
 template <typename T>
 __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc,
-                                                       long long n16, int K, int KS, T* __restrict__ out) {
+                                                       long long n8, int K, int KS, T* __restrict__ out) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  const int cpr = K / 16;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n16; i += (long long)gridDim.x * 256) {
+  const int cpr = K / 8;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n8; i += (long long)gridDim.x * 256) {
     const long long r = i / cpr;
     const int c = (int)(i - r * cpr);
-    const uint4 u = reinterpret_cast<const uint4*>(q)[i];
-    const int e = (int)sc[r * KS + (c >> 1)] - 127;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint2 u = reinterpret_cast<const uint2*>(q)[i];
+    const int e = (int)sc[r * KS + (c >> 2)] - 127;
+    const uint32_t w[2] = {u.x, u.y};
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
       const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
-      store4(out + 16 * i + 4 * j, __builtin_amdgcn_ldexpf(lo.x, e), __builtin_amdgcn_ldexpf(lo.y, e),
-             __builtin_amdgcn_ldexpf(hi.x, e), __builtin_amdgcn_ldexpf(hi.y, e));
+      v[4 * j] = __builtin_amdgcn_ldexpf(lo.x, e);
+      v[4 * j + 1] = __builtin_amdgcn_ldexpf(lo.y, e);
+      v[4 * j + 2] = __builtin_amdgcn_ldexpf(hi.x, e);
+      v[4 * j + 3] = __builtin_amdgcn_ldexpf(hi.y, e);
+    }
+    if constexpr (sizeof(T) == 2) {
+      uint32_t p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = (uint32_t)f32_to_bf16(v[2 * j]) | (uint32_t)f32_to_bf16(v[2 * j + 1]) << 16;
+      reinterpret_cast<uint4*>(out)[i] = make_uint4(p[0], p[1], p[2], p[3]);
+    } else {
+      reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   }
 }
@@ -157,7 +170,7 @@ __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict
 hipError_t launch_dequant_mxfp8(moe_dtype dt, const void* q, const void* scales, long long rows, int K, void* out,
                                 hipStream_t s) {
   const int KS = 4 * ((K + 127) / 128);
-  const long long n = rows * (K / 16);
+  const long long n = rows * (K / 8);
   if (n == 0) return hipSuccess;
   const unsigned grid = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
   const uint8_t* qc = static_cast<const uint8_t*>(q);
