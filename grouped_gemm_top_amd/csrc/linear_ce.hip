@@ -65,11 +65,14 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   load4(p + 4, v[4], v[5], v[6], v[7]);
 }
 
-// A workgroup takes `groups` times 32 tokens.  It counts the counted ones before them over all targets (a list of
-// counts would be another launch; at N = 8192 a workgroup reads 32 KB, and beyond N = 65536 the workgroups are 2048, so
-// that all of them together read 4 KB a token at most), then, 32 at a time, lists its own with their targets
+constexpr int GR = 16;  // tokens of a group: one a wavefront
+
+// A workgroup takes `groups` groups of tokens.  It counts the counted ones before them over all targets (a list of
+// counts would be another launch; at N = 8192 a workgroup reads 32 KB, and beyond N = 32768 the workgroups are 2048, so
+// that all of them together read 4 KB a token at most), then, a group at a time, lists its own with their targets
 // (BWD: with what dz needs) and copies their rows of x one behind the other (fp32: as three planes of N rows).  The
-// others' loss and lse (BWD: rows of dx, where wanted) are 0.
+// others' loss and lse (BWD: rows of dx, where wanted) are 0.  H = 2048: N = 4096 10.9 us (12.8 with groups of 32,
+// 11.0 of 8), N = 8192 14.6 (14.9, 17.4).
 template <typename T, bool BWD>
 __global__ __launch_bounds__(1024) void k_ce_select(const int* __restrict__ target, const T* __restrict__ x, int N, int H,
                                                    int V, int groups, int* __restrict__ list, int* __restrict__ cnt,
@@ -77,8 +80,8 @@ __global__ __launch_bounds__(1024) void k_ce_select(const int* __restrict__ targ
                                                    float* __restrict__ lse_out, const float* __restrict__ lse,
                                                    const float* __restrict__ dloss, float zc, float4* __restrict__ info,
                                                    T* __restrict__ dx) {
-  __shared__ int s_n[16], s_pos[32];
-  const int L = threadIdx.x & 63, w = threadIdx.x >> 6, t_lo = blockIdx.x * groups * 32;
+  __shared__ int s_n[16], s_pos[GR];
+  const int L = threadIdx.x & 63, w = threadIdx.x >> 6, t_lo = blockIdx.x * groups * GR;
   int c = 0;
   for (int t = threadIdx.x; t < t_lo; t += 4 * 1024) {
 #pragma unroll
@@ -91,14 +94,14 @@ __global__ __launch_bounds__(1024) void k_ce_select(const int* __restrict__ targ
   int base = 0;
 #pragma unroll
   for (int q = 0; q < 16; ++q) base += s_n[q];
-  for (int t0 = t_lo; t0 < N && t0 < t_lo + 32 * groups; t0 += 32) {
+  for (int t0 = t_lo; t0 < N && t0 < t_lo + GR * groups; t0 += GR) {
     if (w == 0) {
       const int t = t0 + L;
-      const bool mine = L < 32 && t < N;
+      const bool mine = L < GR && t < N;
       const int y = mine ? target[t] : -1;
       const unsigned long long live = __ballot(in_vocab(y, V));
       const int p = base + __popcll(live & ((1ull << L) - 1));
-      if (L < 32) s_pos[L] = in_vocab(y, V) ? p : -1;
+      if (L < GR) s_pos[L] = in_vocab(y, V) ? p : -1;
       if (in_vocab(y, V)) {
         list[p] = t;
         tgt[p] = y;
@@ -111,10 +114,10 @@ __global__ __launch_bounds__(1024) void k_ce_select(const int* __restrict__ targ
         lse_out[t] = 0.f;
       }
       base += __popcll(live);
-      if (L == 0 && t0 + 32 >= N) *cnt = base;
+      if (L == 0 && t0 + GR >= N) *cnt = base;
     }
     __syncthreads();
-    for (int r = w; r < 32 && t0 + r < N; r += 16) {
+    for (int r = w; r < GR && t0 + r < N; r += 16) {
       const int p = s_pos[r];
       const T* src = x + (size_t)(t0 + r) * H;
       if (p >= 0) {
@@ -703,9 +706,9 @@ constexpr long long kDesc = 0x7FFFFFFF;
 
 int tile_n(int big) { return big == 2 ? 256 : big == 1 ? 128 : 64; }
 
-// groups of 32 tokens that a workgroup of k_ce_select takes
-int select_groups(int N) { return (N + 65535) / 65536; }
-unsigned select_grid(int N) { return (unsigned)((N + 32 * select_groups(N) - 1) / (32 * select_groups(N))); }
+// groups that a workgroup of k_ce_select takes
+int select_groups(int N) { return (N + 2048 * GR - 1) / (2048 * GR); }
+unsigned select_grid(int N) { return (unsigned)((N + GR * select_groups(N) - 1) / (GR * select_groups(N))); }
 
 // The tile of x W^T: choose's, without K slices (the epilogue needs whole sums); for up to 64 tokens 3 = 64 x 128
 // with three stages in place of 128 x 128 with two, as W's way from memory is the time then and twice as much of it is
