@@ -161,6 +161,54 @@ def test_few_tokens_large_vocabulary(N, H, V, ign, ty):
     _check(o, ref, bound)
 
 
+@pytest.mark.parametrize("ty,N,H,V", [(BF, 8192, 2048, 9001), (F32, 8192, 4096, 8100)], ids=["bf16", "f32"])
+def test_pieces_that_share_launches(ty, N, H, V):
+    """Pieces large enough that dx and dW of one run beside dz of the next; on two streams at once and from a graph.
+    In the 2-norm: bf16 rounds dz and the result, sqrt 2 2^-8 / sqrt 3 = 0.0032; fp32 rounds 6 K / 32 running sums, which
+    for K = 8100 at random is 39 2^-24 = 2.3e-6 of the sum, and dz carries that of z, K = 4096, 1.7e-6."""
+    import grouped_gemm_top_amd as G
+    gen = torch.Generator(device="cuda").manual_seed(91)
+    x = torch.randn(N, H, generator=gen, device="cuda").to(ty)
+    w = (H ** -0.5 * torch.randn(V, H, generator=gen, device="cuda")).to(ty)
+    t = torch.randint(-V // 9, V, (N,), generator=gen, device="cuda").int()
+    g = torch.rand(N, generator=gen, device="cuda")
+
+    def step(stream=None):
+        f = G.linear_ce_fwd(x, w, t, z_coef=1e-3, stream=stream)
+        return dict(f, **G.linear_ce_bwd(g, x, w, t, f["lse"], z_coef=1e-3, stream=stream))
+    o = step()
+    live = t >= 0
+    xl, wd, tl = x[live].double(), w.double(), t[live].long()[:, None]
+    z = xl @ wd.t()
+    lse = torch.logsumexp(z, dim=1)
+    rel = lambda p, q: float((p.double() - q).norm() / q.norm())  # noqa: E731
+    assert rel(o["loss"][live], lse - z.gather(1, tl)[:, 0] + 1e-3 * lse ** 2) <= 1e-6
+    gl = g[live].double()
+    dz = torch.exp(z - lse[:, None]) * (gl * (1 + 2e-3 * lse))[:, None]
+    dz.scatter_add_(1, tl, -gl[:, None])
+    tol = 4e-3 if ty is BF else 1e-5
+    assert rel(o["dx"][live], dz @ wd) <= tol and bool((o["dx"][~live] == 0).all())
+    assert rel(o["dw"], dz.t().contiguous() @ xl) <= tol
+    st = [torch.cuda.Stream() for _ in range(2)]
+    for s in st:
+        s.wait_stream(torch.cuda.current_stream())
+    p, q = step(st[0]), step(st[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[n], p[n]) and torch.equal(o[n], q[n]) for n in o)
+    with torch.cuda.stream(st[0]):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st[0]):
+            r = step()
+    for i in range(2):
+        x.copy_(torch.randn(N, H, generator=gen, device="cuda"))
+        t.copy_(torch.randint(-V * (2 - i), V, (N,), generator=gen, device="cuda"))
+        e = step()
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(e[n], r[n]) for n in e), i
+
+
 @TYPES
 def test_many_tokens(ty):
     """More tokens than one group a workgroup lists: 140003 of them, a third without a target."""
