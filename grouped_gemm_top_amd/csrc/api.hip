@@ -172,8 +172,8 @@ moe_status check_ce(moe_dtype dt, int32_t N, int32_t H, int32_t V) {
   const int64_t es = dt == MOE_F32 ? 6 : 2, h = H > 256 ? H : 256;
   REQUIRE(N * h * es <= kDescBytes && 256 * (int64_t)H * es <= kDescBytes, MOE_EUNSUPPORTED,
           "x [N=%d, max(H=%d, 256)] must be < 2 GiB (bf16; fp32: a third of it in elements)", N, H);
-  REQUIRE((int64_t)N * V <= (int64_t)1 << 36 && (int64_t)V * H <= (int64_t)1 << 36, MOE_EUNSUPPORTED,
-          "N V and V H must be at most 2^36 (got N=%d, V=%d, H=%d)", N, V, H);
+  REQUIRE(V <= 1 << 30 && (int64_t)N * V <= (int64_t)1 << 36 && (int64_t)V * H <= (int64_t)1 << 36, MOE_EUNSUPPORTED,
+          "V must be at most 2^30, N V and V H at most 2^36 (got N=%d, V=%d, H=%d)", N, V, H);
   return MOE_OK;
 }
 

@@ -586,7 +586,8 @@ moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bia
  * of at most 128 MB (MOE_F32: 192 MB), or 256 columns where N is above 262144 (131072).
  * A counted token with NaN or infinite logits spoils its own loss, lse and dx, and all of dw.
  * H a multiple of 8, V >= 1 (any); tensors and workspace 16-byte aligned, targets, loss, lse and dloss 4-byte;
- * N max(H, 256) elements below 2 GiB (MOE_F32: 2 GiB / 6 elements), 256 H likewise, N V at most 2^36; z_coef finite.
+ * N max(H, 256) elements below 2 GiB (MOE_F32: 2 GiB / 6 elements), 256 H likewise, N V and V H at most 2^36, V at most 2^30; z_coef
+ * finite.
  * Everything is written fresh, in a fixed order (bitwise reproducible); N == 0 sets dw to zero.  Workspaces:
  * moe_workspace_bytes(MOE_OP_LINEAR_CE_FWD / _BWD, dt, N, 1, 1, H, V, 0).
  */

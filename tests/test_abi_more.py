@@ -299,3 +299,15 @@ def test_layer_few_bindings():
         call(x=x[0])
     with pytest.raises(ValueError, match="contiguous"):
         call(x=torch.zeros(4, 128, dtype=b)[:, ::2])
+
+
+def test_linear_ce_largest_vocabulary(L):
+    """Columns are counted in 32 bits: V up to 2^30, whatever memory there is."""
+    for op in (G.OP_LINEAR_CE_FWD, G.OP_LINEAR_CE_BWD):
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, 1, 1, 1, 8, 1 << 30, 0) > 0
+        assert L.moe_workspace_bytes(op, G.MOE_BF16, 1, 1, 1, 8, (1 << 30) + 1, 0) == 0
+    big = 1 << 62
+    assert L.moe_linear_ce_fwd(G.MOE_BF16, ptr(1), ptr(2), ptr(3), 1, 8, (1 << 31) - 1, 0.0, ptr(4), ptr(5), ptr(6), big,
+                               None) == G.MOE_EUNSUPPORTED
+    assert L.moe_linear_ce_bwd(G.MOE_BF16, None, ptr(1), ptr(2), ptr(3), ptr(4), 1, 8, (1 << 31) - 1, 0.0, ptr(5), ptr(7),
+                               ptr(6), big, None) == G.MOE_EUNSUPPORTED
