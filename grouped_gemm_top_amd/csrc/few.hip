@@ -45,6 +45,7 @@ struct Args {
   const uint8_t *gs, *us, *ds;  // MX-FP8: scale codes
   int N, H, I, E, k;
   int S, hs;         // slices of the router product and their length
+  int ws;            // wavefronts that share a gate/up task
   int rb, P;         // outputs of a down workgroup (8 to 16) and parts of its sum
   float* part;       // [S, N, E]
   void* act;         // a' [N k, I]: rows by expert, then token (N = 1: by slot)
@@ -406,17 +407,19 @@ __device__ __forceinline__ f32x4 line_mma(const Line<T, F8>& w, const Vec<T, F8>
 __device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ------------------------------------------------------------------ gate / up
+// k-steps in flight: as many as 128 registers hold, for two workgroups a compute unit are worth more than longer bursts
+// (N = 24 on MX-FP8 weights: 59 us with one step, 74 with four in twice the registers; N = 61 in fp32: 79 and 98)
+constexpr int lines_ahead(bool f8, int TB) { return f8 ? (TB > 1 ? 1 : 2) : TB > 2 ? 1 : 4; }
+
 // TB: blocks of 16 tokens (N <= 16 TB; 0: N = 1).  PL: experts per lane of the choice, which is made here for a single
-// token (0: it was made before).
-template <typename T, bool F8, int PL, int TB_>
+// token (0: it was made before).  GRP: a.ws wavefronts share a task and a workgroup takes NW / a.ws of them at a time (see
+// shares()); else all of them one.
+template <typename T, bool F8, int PL, int TB_, bool GRP>
 __global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
   using Ln = Line<T, F8>;
   constexpr bool ONE = TB_ == 0;
   constexpr int TB = ONE ? 1 : TB_;
-  // k-steps in flight: as many as 128 registers hold, for two workgroups a compute unit are worth more than
-  // longer bursts (N = 24 on MX-FP8 weights: 59 us with one step, 74 with four in twice the registers; N = 61 in
-  // fp32: 79 and 98)
-  constexpr int U = F8 ? (TB > 1 ? 1 : 2) : TB > 2 ? 1 : 4;
+  constexpr int U = lines_ahead(F8, TB);
   __shared__ typename std::conditional<ONE, One, Lists>::type s;
   __shared__ f32x4 s_sum[NW][2][64];
   __shared__ float s_w[MAXN * MAXK];
@@ -437,7 +440,10 @@ __global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
   const int IB = (a.I + 15) / 16, tasks = n * IB;
   const int KS = 4 * ((a.H + 127) / 128);
   constexpr size_t ES = F8 ? 1 : sizeof(T);
-  for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+  const int WS = GRP ? a.ws : NW, per = GRP ? NW / WS : 1, sub = GRP ? w / WS : 0, wi = GRP ? w - sub * WS : w;
+  for (int first = blockIdx.x * per; first < tasks; first += (int)gridDim.x * per) {
+    const bool on = !GRP || first + sub < tasks;  // (a wavefront without a task takes the last one and stores nothing)
+    const int task = GRP ? min(first + sub, tasks - 1) : first;
     const int ai = task / IB, i0 = (task - ai * IB) * 16;
     int e, row0, cnt, nb;
     if constexpr (ONE) {
@@ -464,12 +470,12 @@ __global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
     f32x4 ag[TB], au[TB];
 #pragma unroll
     for (int b = 0; b < TB; ++b) ag[b] = au[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = w * Ln::K; k0 < a.H; k0 += U * NW * Ln::K) {
+    for (int k0 = wi * Ln::K; k0 < a.H; k0 += U * WS * Ln::K) {
       Ln lg[U], lu[U];
       Vec<T, F8> xv[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * NW * Ln::K;
+        const int k = k0 + u * WS * Ln::K;
         lg[u].load(pg, sg, k, a.H, g);
         lu[u].load(pu, su, k, a.H, g);
         xv[u].load(px, k, a.H, g);
@@ -498,25 +504,26 @@ __global__ __launch_bounds__(NT, PL == 16 ? 2 : 4) void k_few_gateup(Args a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           Vec<T, F8> xb;
-          xb.load(pb, k0 + u * NW * Ln::K, a.H, g);
+          xb.load(pb, k0 + u * WS * Ln::K, a.H, g);
           ag[b] = line_mma(lg[u], xb, ag[b], g);
           au[b] = line_mma(lu[u], xb, au[b], g);
         }
       }
     }
-    // the wavefronts' sums in wavefront order; lane l of wavefront 0: columns i0 + 4 (l >> 4) + v, token slot l & 15
+    // the wavefronts' sums in wavefront order; lane l of a task's first: columns i0 + 4 (l >> 4) + v, token slot l & 15
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
-      if (b >= nb) break;
+      if (GRP ? 16 * b >= a.N : b >= nb) break;  // (the same for all wavefronts)
       s_sum[w][0][L] = ag[b];
       s_sum[w][1][L] = au[b];
       __syncthreads();
-      if (w == 0) {
-        f32x4 G = s_sum[0][0][L], Uv = s_sum[0][1][L];
+      if (wi == 0 && on) {
+        f32x4 G = s_sum[w][0][L], Uv = s_sum[w][1][L];
 #pragma unroll
         for (int q = 1; q < NW; ++q) {
-          G += s_sum[q][0][L];
-          Uv += s_sum[q][1][L];
+          if (GRP && q >= WS) break;
+          G += s_sum[w + q][0][L];
+          Uv += s_sum[w + q][1][L];
         }
         const int slot = 16 * b + r, i = i0 + 4 * g;
         if (slot < cnt && i < a.I) {
@@ -667,6 +674,16 @@ void slices(int N, int H, int E, int& S, int& hs) {
   hs = ((H + S - 1) / S + 15) / 16 * 16;
 }
 
+// Wavefronts that share a gate/up task: eight, unless H has no U lines for each and there are tasks for all workgroups
+// all the same (MX-FP8, H = 160, N = 43, E = 190, I = 1120, k = 7: the call 73 us, 99 with eight; H = 224, N = 37, E = 133,
+// I = 1536: 80, 105).  tasks: at most, U: lines in flight, K: values of a line
+int shares(int H, long long tasks, int U, int K) {
+  const int lines = (H + K - 1) / K;
+  int n = NW;
+  while (n > 1 && U * n / 2 >= lines && tasks * n >= 512 * NW * 2) n /= 2;
+  return n;
+}
+
 // The down product's workgroups.  Few tokens, where the launch is a matter of latency and a join of parts costs 3
 // us: 8 outputs each, parts only where that leaves half the chip idle.  Else the outputs (8 to 16) and parts (up to
 // MAXP) with the least time of the fullest compute unit: its share of the matrices at 20 KB a us, and 4 us for each
@@ -694,16 +711,18 @@ void parts(int N, int H, double row, int& rb, int& P) {
 }
 
 template <typename T, bool F8, int PL, int TB>
-hipError_t run(const Args& a, hipStream_t s) {
+hipError_t run(Args a, hipStream_t s) {
   const dim3 gr(a.S, (a.E + 63) / 64, (a.N + 15) / 16);
   hipLaunchKernelGGL(k_few_router<T>, gr, dim3(256), 0, s, a);
   const long long act = a.E < a.N * a.k ? a.E : a.N * a.k, tasks = act * ((a.I + 15) / 16);
   const dim3 gg((unsigned)(tasks < 512 ? tasks : 512));
   if constexpr (TB == 0) {
-    hipLaunchKernelGGL((k_few_gateup<T, F8, PL, 0>), gg, dim3(NT), 0, s, a);
+    hipLaunchKernelGGL((k_few_gateup<T, F8, PL, 0, false>), gg, dim3(NT), 0, s, a);
   } else {
     hipLaunchKernelGGL(k_few_choose<PL>, dim3(a.N), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_few_gateup<T, F8, 0, TB>), gg, dim3(NT), 0, s, a);
+    a.ws = shares(a.H, tasks, lines_ahead(F8, TB), Line<T, F8>::K);
+    if (a.ws < NW) hipLaunchKernelGGL((k_few_gateup<T, F8, 0, TB, true>), gg, dim3(NT), 0, s, a);
+    else hipLaunchKernelGGL((k_few_gateup<T, F8, 0, TB, false>), gg, dim3(NT), 0, s, a);
   }
   hipLaunchKernelGGL((k_few_down<T, F8, TB>), dim3((a.H + a.rb - 1) / a.rb * a.P), dim3(NT), 0, s, a);
   return hipGetLastError();

@@ -137,6 +137,16 @@ def test_multiples_of_eight(N, H, I, E, k, ty):
 
 
 @KINDS
+@pytest.mark.parametrize("N,H,I,E,k", [(2, 96, 2080, 32, 8), (10, 128, 1024, 128, 8), (24, 160, 544, 80, 6),
+                                       (61, 224, 544, 64, 5), (40, 32, 800, 100, 2)])
+def test_narrow_rows_and_many_tasks(N, H, I, E, k, kind):
+    """Where a few of a workgroup's wavefronts share a task, and it has several at a time."""
+    c = _case(N, H, I, E, k, kind, seed=6)
+    o, _ = _run(c)
+    _check(c, o)
+
+
+@KINDS
 @pytest.mark.parametrize("N", [1, 16, 48, 64])
 def test_all_tokens_name_the_same_experts(N, kind):
     c = _case(N, 128, 96, 6, 2, kind, seed=5, same=True)
