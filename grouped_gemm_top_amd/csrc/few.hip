@@ -9,9 +9,10 @@
 // that stream.  Launches:
 //  1. router product, sliced along H (fp32 on the vector units: 2 N H E operations are nothing here);
 //  2. gate/up: for a single token every workgroup joins the slices and chooses the experts itself (for more a launch
-//     of its own does, a workgroup per token), then takes tasks (expert, 16 columns of I).  Its eight wavefronts
-//     (fewer, with several tasks at a time, where H is short) split H, weights go straight from memory into registers as the matrix instruction's operand, and the
-//     sums meet in LDS; a' = w silu(g) u is rounded once, as the next product's operand;
+//     of its own does, a workgroup per token), then takes tasks (expert, 16 columns of I).  Its eight wavefronts split
+//     H (fewer, with several tasks at a time, where H is short), weights go straight from memory into registers as
+//     the matrix instruction's operand, and the sums meet in LDS; a' = w silu(g) u is rounded once, as the next
+//     product's operand;
 //  3. down: a workgroup owns 8 to 16 outputs of every token, or a part of the experts for them; its
 //     wavefronts take the experts in turn and add each one's products to their tokens' sums in LDS.  No
 //     floating-point atomics, one fixed order.
