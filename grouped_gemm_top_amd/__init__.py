@@ -811,7 +811,7 @@ def layer_few(x, w_r, w_gate, w_up, w_down, k: int, bias=None, out=None, topk_id
     torch = _torch
     quant = isinstance(w_gate, (tuple, list))
     mats = [("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)]
-    if any(isinstance(m, (tuple, list)) != quant for _, m in mats):
+    if any(isinstance(m, (tuple, list)) != quant or (quant and len(m) != 2) for _, m in mats):
         raise ValueError("w_gate, w_up and w_down must all be tensors or all (codes, scale codes)")
     gate = w_gate[0] if quant else w_gate
     if x.dim() != 2 or w_r.dim() != 2 or gate.dim() != 3:

@@ -311,3 +311,19 @@ def test_linear_ce_largest_vocabulary(L):
                                None) == G.MOE_EUNSUPPORTED
     assert L.moe_linear_ce_bwd(G.MOE_BF16, None, ptr(1), ptr(2), ptr(3), ptr(4), 1, 8, (1 << 31) - 1, 0.0, ptr(5), ptr(7),
                                ptr(6), big, None) == G.MOE_EUNSUPPORTED
+
+
+def test_layer_few_codes_come_in_pairs():
+    """MX-FP8 weights are (codes, scale codes): anything longer or shorter is refused, not passed on argument by argument."""
+    b, u = torch.bfloat16, torch.uint8
+    x, wr = torch.zeros(4, 64, dtype=b), torch.zeros(64, 3)
+    gq, dq = [torch.zeros(3, 32, 64, dtype=u), torch.zeros(3, 32, 4, dtype=u)], [torch.zeros(3, 64, 32, dtype=u),
+                                                                              torch.zeros(3, 64, 4, dtype=u)]
+    for n in range(3):
+        for m in ([], [0], [0, 1, 1]):
+            w = [gq, gq, dq]
+            w[n] = tuple(w[n][i] for i in m)
+            with pytest.raises(ValueError, match=r"\(codes, scale codes\)"):
+                G.layer_few(x, wr, *w, 2)
+    with pytest.raises(ValueError, match="GPU"):  # a list is a pair too
+        G.layer_few(x, wr, gq, gq, dq, 2)
