@@ -191,14 +191,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
   int mt, nt;
   tile_at(t - s * nT, a.nM, a.nN, mt, nt);
   const int m0 = mt * BM, n0 = nt * BN;
-  const int steps = (a.K + BK - 1) / BK;  // of one term
-  const int k_lo = (int)((long long)C::TERMS * steps * s / a.S);
-  const int nk = (int)((long long)C::TERMS * steps * (s + 1) / a.S) - k_lo;
+  const KSlice sl = k_slice(C::TERMS, (a.K + BK - 1) / BK, s, a.S);
   const uint32_t pa = (uint32_t)a.M * (uint32_t)a.K * 2u, pb = (uint32_t)a.N * (uint32_t)a.K * 2u;
   const Opnd A{a.A, a.M, AKC ? a.K : a.M, (long long)C::PLANES * a.M * a.K * 2, pa, nullptr};
   const Opnd B{a.B, a.N, BKC ? a.K : a.N, (long long)C::PLANES * a.N * a.K * 2, pb, nullptr};
   f32x4 acc[MB][NB];
-  C::run(s_ring, A, B, m0, n0, a.K, steps, k_lo, nk, w, L, acc);
+  C::run(s_ring, A, B, m0, n0, a.K, sl, w, L, acc);
 
   // acc[i][j][v] = C[wm.. + 16 i + (L & 15)][wn.. + 16 j + 4 (L >> 4) + v]; through LDS a lane gets
   // columns 8 (L & 7) .. + 7 of row 8 p + (L >> 3), so eight lanes cover a row's 128-byte line.  The

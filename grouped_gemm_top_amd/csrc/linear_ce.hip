@@ -533,14 +533,11 @@ __device__ __forceinline__ void dx_tile(const Args& a, int b, char* s_ring) {
   int mt, nt, s;
   if (!my_tile(b, (n + BM - 1) / BM, (a.H + BN - 1) / BN, PART ? a.S : 1, mt, nt, s)) return;
   const int m0 = mt * BM, n0 = nt * BN;
-  const int steps = (a.V + BK - 1) / BK;
-  const int S = PART ? a.S : 1;
-  const int k_lo = (int)((long long)C::TERMS * steps * s / S);
-  const int nk = (int)((long long)C::TERMS * steps * (s + 1) / S) - k_lo;
+  const KSlice sl = k_slice(C::TERMS, (a.V + BK - 1) / BK, s, PART ? a.S : 1);
   const Opnd A{a.dz, n, a.ldz, (long long)C::PLANES * a.N * a.ldz * 2, (uint32_t)a.N * (uint32_t)a.ldz * 2u, nullptr};
   const Opnd B{a.w, a.H, a.H, (long long)C::PLANES * a.V * a.H * 2, (uint32_t)a.V * (uint32_t)a.H * 2u, nullptr};
   f32x4 acc[MB][NB];
-  C::run(s_ring, A, B, m0, n0, a.V, steps, k_lo, nk, w, L, acc);
+  C::run(s_ring, A, B, m0, n0, a.V, sl, w, L, acc);
   char* sg = s_ring + w * 4096;
 #pragma unroll
   for (int h = 0; h < NB / 4; ++h) {
@@ -629,9 +626,7 @@ __device__ __forceinline__ void dw_tiles(const Args& a, int b, int G, char* s_ri
   f32x4 acc[MB][NB];
   P pipe;
   if constexpr (PART) {
-    const int steps = (n + BK - 1) / BK, k_lo = (int)((long long)C::TERMS * steps * s / S);
-    const int nk = (int)((long long)C::TERMS * steps * (s + 1) / S) - k_lo;
-    C::run(s_ring, A, B, m0, n0, n, steps, k_lo, nk, w, L, acc);
+    C::run(s_ring, A, B, m0, n0, n, k_slice(C::TERMS, (n + BK - 1) / BK, s, S), w, L, acc);
   } else {
     pipe.start(s_ring, A, B, n, w, L, at);
   }

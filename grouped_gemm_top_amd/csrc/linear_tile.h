@@ -123,6 +123,15 @@ struct Frag {
   }
 };
 
+// Slice s of S of a contraction of `terms` times `steps` k-steps: how many it has, and the term and the step within it
+// of its first one.  (steps is 0 where a count made on the device leaves nothing to sum over.)
+struct KSlice { int n, term, step; };
+__host__ __device__ constexpr KSlice k_slice(int terms, int steps, int s, int S) {
+  const int lo = (int)((long long)terms * steps * s / S), hi = (int)((long long)terms * steps * (s + 1) / S);
+  const int term = terms > 1 && steps > 0 ? lo / steps : 0;
+  return KSlice{hi - lo, term, lo - term * steps};
+}
+
 // C[m0 ..][n0 ..] of a BM x BN tile by WM x WN wavefronts, each (BM / WM) x (BN / WN) in 16 x 16 blocks.
 // F32: six terms of three parts an operand; SF: the smallest terms first, which are then rounded to a small sum
 // (cross entropy at H = 1880: losses off by 7e-7 in place of 2.1e-6).
@@ -138,10 +147,11 @@ struct Core {
   static_assert(NST * STG >= NW * 4096, "the epilogue's staging");
   static_assert(MB > 1 || NB == 4, "shapes below");
 
-  // k-steps k_lo .. k_lo + nk - 1 of TERMS `steps` (of BK each) into acc; the ring is free afterwards.
+  // A slice's k-steps (of BK each) into acc; the ring is free afterwards.
   // acc[i][j][v] = C[wm (BM / WM) + 16 i + (L & 15)][wn (BN / WN) + 16 j + 4 (L >> 4) + v]
   static __device__ __forceinline__ void run(char* s_ring, const Opnd& A, const Opnd& B, int m0, int n0, int K,
-                                             int steps, int k_lo, int nk, int w, int L, f32x4 (&acc)[MB][NB]) {
+                                             const KSlice& sl, int w, int L, f32x4 (&acc)[MB][NB]) {
+    const int nk = sl.n;
     const int wm = w % WM, wn = w / WM;
     Op<BM, NW, AKC> oa;
     Op<BN, NW, BKC> ob;
@@ -154,7 +164,7 @@ struct Core {
     const uint32_t ring = lds_addr(s_ring);
     constexpr int NIA = Op<BM, NW, AKC>::NI, NI = NIA + Op<BN, NW, BKC>::NI;
     // the next step to load: its number, k and term (all wavefront-uniform)
-    int lc = 0, lt = F32 ? k_lo / steps : 0, lk = (k_lo - lt * steps) * BK;
+    int lc = 0, lt = sl.term, lk = sl.step * BK;
     // its load instruction q into stage st (a step past the last one is all masked)
     auto issue = [&](int q, int st) __attribute__((always_inline)) {
       const uint32_t m = ring + (uint32_t)st * STG;
