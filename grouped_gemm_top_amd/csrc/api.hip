@@ -27,6 +27,9 @@ moe_status hip_status(hipError_t e, const char* where) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+// whether the output p (if there is one) is none of the arguments o
+template <typename... P>
+bool apart(const void* p, P... o) { return !p || ((p != (const void*)o) && ...); }
 
 #define REQUIRE(cond, st, ...) \
   do {                         \
@@ -149,8 +152,9 @@ moe_status check_few_args(moe_dtype dt, const void* x, const void* w_r, const vo
                           const void* out, const void* idx, const void* w, const void* ws, size_t ws_bytes) {
   REQUIRE(w_r && wg && wu && wd, MOE_EINVAL, "NULL weight argument");
   REQUIRE(N == 0 || (x && out && idx && w), MOE_EINVAL, "NULL x/out/topk_idx/topk_w");
-  REQUIRE(N == 0 || (out != x && idx != w && out != idx && out != w), MOE_EINVAL,
-          "out, topk_idx and topk_w must be no other argument");
+  REQUIRE(N == 0 || (apart(out, x, w_r, bias, wg, wu, wd, idx, w, ws) && apart(idx, x, w_r, bias, wg, wu, wd, w, ws) &&
+                     apart(w, x, w_r, bias, wg, wu, wd, ws)),
+          MOE_EINVAL, "out, topk_idx and topk_w must be no other argument");
   REQUIRE(aligned16(x) && aligned16(wg) && aligned16(wu) && aligned16(wd) && aligned16(out) && aligned16(ws),
           MOE_EUNSUPPORTED, "x, weights, out and workspace must be 16-byte aligned");
   REQUIRE(aligned4(w_r) && aligned4(bias) && aligned4(idx) && aligned4(w), MOE_EUNSUPPORTED,
@@ -804,7 +808,7 @@ moe_status moe_linear_ce_fwd(moe_dtype dt, const void* x, const void* w, const i
   REQUIRE(z_coef - z_coef == 0.f, MOE_EINVAL, "z_coef must be finite");
   REQUIRE(w, MOE_EINVAL, "NULL w");
   REQUIRE(N == 0 || (x && targets && loss && lse), MOE_EINVAL, "NULL x/targets/loss/lse");
-  REQUIRE(N == 0 || (loss != lse && loss != x && lse != x && (void*)loss != targets && (void*)lse != targets), MOE_EINVAL,
+  REQUIRE(N == 0 || (apart(loss, x, w, targets, lse, ws) && apart(lse, x, w, targets, ws)), MOE_EINVAL,
           "loss and lse must be no other argument");
   REQUIRE(aligned16(x) && aligned16(w) && aligned16(ws), MOE_EUNSUPPORTED, "x, w and workspace must be 16-byte aligned");
   REQUIRE(aligned4(targets) && aligned4(loss) && aligned4(lse), MOE_EUNSUPPORTED,
@@ -827,8 +831,8 @@ moe_status moe_linear_ce_bwd(moe_dtype dt, const float* dloss, const void* x, co
   REQUIRE(z_coef - z_coef == 0.f, MOE_EINVAL, "z_coef must be finite");
   REQUIRE(dx || dw, MOE_EINVAL, "no gradient requested");
   REQUIRE(N == 0 || (x && w && targets && lse), MOE_EINVAL, "NULL x/w/targets/lse");
-  REQUIRE(N == 0 || ((!dx || (dx != x && dx != w && dx != dw)) && (!dw || (dw != x && dw != w))), MOE_EINVAL,
-          "dx and dw must be no other argument");
+  REQUIRE(apart(dw, w, ws) && (N == 0 || (apart(dx, x, w, targets, lse, dloss, dw, ws) && apart(dw, x, targets, lse, dloss))),
+          MOE_EINVAL, "dx and dw must be no other argument");
   REQUIRE(aligned16(x) && aligned16(w) && aligned16(dx) && aligned16(dw) && aligned16(ws), MOE_EUNSUPPORTED,
           "x, w, dx, dw and workspace must be 16-byte aligned");
   REQUIRE(aligned4(targets) && aligned4(lse) && aligned4(dloss), MOE_EUNSUPPORTED,
@@ -871,6 +875,8 @@ moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bia
   if ((st = check_few_args(MOE_BF16, x, w_r, bias, wg_q, wu_q, wd_q, N, H, I, E, k, out, topk_idx, topk_w, ws,
                            ws_bytes)) != MOE_OK)
     return st;
+  REQUIRE(N == 0 || (apart(out, wg_s, wu_s, wd_s) && apart(topk_idx, wg_s, wu_s, wd_s) && apart(topk_w, wg_s, wu_s, wd_s)),
+          MOE_EINVAL, "out, topk_idx and topk_w must be no other argument");
   moe::kernel_event(MOE_K_LAYER_FEW, 0, (hipStream_t)stream);
   hipError_t e = moe::launch_layer_few(MOE_BF16, x, w_r, bias, wg_q, wg_s, wu_q, wu_s, wd_q, wd_s, N, H, I, E, k, out,
                                        topk_idx, topk_w, ws, (hipStream_t)stream);

@@ -551,7 +551,7 @@ moe_status moe_dequantize_mxfp8(moe_dtype dt, const uint8_t* q, const uint8_t* s
  * I, as for moe_grouped_gemm_fwd_mxfp8) under bf16 x and out: the codes' values are the operands, exact in bf16; the
  * activations are not quantized.
  * 0 <= N <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= 1024, H and I multiples of 8 (codes: 32); x, weights,
- * out and workspace 16-byte aligned, the rest 4-byte.  Only the matrices of the experts that some token names are
+ * out and workspace 16-byte aligned, the rest 4-byte; out, topk_idx and topk_w are no other argument.  Only the matrices of the experts that some token names are
  * read, once.  A token with NaN or infinities spoils its own outputs only.  Bitwise reproducible, and a token's
  * topk_idx is what the call with that token alone gives wherever its logits differ by more than fp32's rounding.
  * Workspace: moe_workspace_bytes(MOE_OP_LAYER_FEW, dt, N, E, k, H, I, 0) (the codes' form: MOE_BF16).
@@ -585,7 +585,8 @@ moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bia
  * magnitudes from 3.38e38 on make their sums NaN).  Its working copy of dz is one or two pieces of the vocabulary, each
  * of at most 128 MB (MOE_F32: 192 MB), or 256 columns where N is above 262144 (131072).
  * A counted token with NaN or infinite logits spoils its own loss, lse and dx, and all of dw.
- * H a multiple of 8, V >= 1 (any); tensors and workspace 16-byte aligned, targets, loss, lse and dloss 4-byte;
+ * H a multiple of 8, V >= 1 (any); tensors and workspace 16-byte aligned, targets, loss, lse and dloss 4-byte; each
+ * output is no other argument of its call;
  * N max(H, 256) elements below 2 GiB (MOE_F32: 2 GiB / 6 elements), 256 H likewise, N V and V H at most 2^36, V at most 2^30; z_coef
  * finite.
  * Everything is written fresh, in a fixed order (bitwise reproducible); N == 0 sets dw to zero.  Workspaces:

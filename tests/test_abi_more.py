@@ -327,3 +327,38 @@ def test_layer_few_codes_come_in_pairs():
                 G.layer_few(x, wr, *w, 2)
     with pytest.raises(ValueError, match="GPU"):  # a list is a pair too
         G.layer_few(x, wr, gq, gq, dq, 2)
+
+
+def test_outputs_are_no_other_argument(L):
+    """Every output of the calls that say so, over every other argument (an output written early would be read as input)."""
+    q = G.workspace_bytes
+
+    def few(a, sc):
+        nb = q(G.OP_LAYER_FEW, G.MOE_BF16, 16, 8, 2, 64, 96)
+        size = (16, 64, 96, 8, 2)
+        if sc:
+            return L.moe_layer_few_mxfp8(a["x"], a["wr"], a["b"], a["wg"], a["gs"], a["wu"], a["us"], a["wd"], a["ds"], *size,
+                                         a["out"], a["idx"], a["w"], a["ws"], nb, None)
+        return L.moe_layer_few(G.MOE_BF16, a["x"], a["wr"], a["b"], a["wg"], a["wu"], a["wd"], *size, a["out"], a["idx"],
+                               a["w"], a["ws"], nb, None)
+
+    def fwd(a):
+        nb = q(G.OP_LINEAR_CE_FWD, G.MOE_F32, 40, 1, 1, 64, 101)
+        return L.moe_linear_ce_fwd(G.MOE_F32, a["x"], a["w"], a["t"], 40, 64, 101, 0.0, a["loss"], a["lse"], a["ws"], nb, None)
+
+    def bwd(a):
+        nb = q(G.OP_LINEAR_CE_BWD, G.MOE_F32, 40, 1, 1, 64, 101)
+        return L.moe_linear_ce_bwd(G.MOE_F32, a["g"], a["x"], a["w"], a["t"], a["lse"], 40, 64, 101, 0.0, a["dx"], a["dw"],
+                                   a["ws"], nb, None)
+    for call, ins, outs in ((lambda a: few(a, False), ("x", "wr", "b", "wg", "wu", "wd", "ws"), ("out", "idx", "w")),
+                            (lambda a: few(a, True), ("x", "wr", "b", "wg", "gs", "wu", "us", "wd", "ds", "ws"), ("out", "idx", "w")),
+                            (fwd, ("x", "w", "t", "ws"), ("loss", "lse")), (bwd, ("g", "x", "w", "t", "lse", "ws"), ("dx", "dw"))):
+        every = {n: ptr(i + 1) for i, n in enumerate(ins + outs)}
+        for o in outs:
+            for n in every:
+                if n != o:
+                    assert call(dict(every, **{o: every[n]})) == G.MOE_EINVAL, (o, n)
+    # no token: dw is still written
+    nb = q(G.OP_LINEAR_CE_BWD, G.MOE_F32, 0, 1, 1, 64, 101)
+    assert L.moe_linear_ce_bwd(G.MOE_F32, None, None, ptr(1), None, None, 0, 64, 101, 0.0, None, ptr(1), ptr(2), nb,
+                               None) == G.MOE_EINVAL
