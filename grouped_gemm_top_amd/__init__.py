@@ -551,16 +551,16 @@ def _first_use():
     return torch
 
 
-def _on_stream(fn):
-    """Run a binding on its first tensor's device and, if `stream` (a torch stream, or any object
+def _on_stream(fn, at=0):
+    """Run a binding on the device of its argument number `at` (a tensor) and, if `stream` (a torch stream, or any object
     whose cuda_stream is the handle of one of that device) is given, with that stream as the current
     one: what the call allocates then belongs to the stream that uses it."""
-    name = fn.__code__.co_varnames[0]
+    name = fn.__code__.co_varnames[at]
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         torch = _torch or _first_use()
-        first = args[0] if args else kw.get(name)
+        first = args[at] if len(args) > at else kw.get(name)
         if first is None:
             raise TypeError(f"{fn.__name__}() needs {name}")
         # (a host tensor is refused by the binding)
@@ -973,14 +973,15 @@ def linear_ce_fwd(x, w, targets, z_coef: float = 0.0, loss=None, lse=None, ws=No
     return dict(loss=loss, lse=lse)
 
 
-@_on_stream
+@functools.partial(_on_stream, at=1)
 def linear_ce_bwd(dloss, x, w, targets, lse, z_coef: float = 0.0, want_dx=True, want_dw=True, dx=None, dw=None, ws=None):
     """Backward of linear_ce_fwd at the same x, w, targets and z_coef, from its lse and dloss fp32 [N], the
-    gradients of the losses -> dict(dx [N,H] (zero for tokens that take no part), dw [V,H]); what is not
+    gradients of the losses (None: ones) -> dict(dx [N,H] (zero for tokens that take no part), dw [V,H]); what is not
     wanted is None."""
     torch = _torch
     N, H, V, dt, dev = _ce_args(x, w, targets)
-    _want("dloss", dloss, (N,), torch.float32, dev)
+    if dloss is not None:
+        _want("dloss", dloss, (N,), torch.float32, dev)
     _want("lse", lse, (N,), torch.float32, dev)
     _on_gpu(x)
     if want_dx or dx is not None:

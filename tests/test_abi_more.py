@@ -362,3 +362,14 @@ def test_outputs_are_no_other_argument(L):
     nb = q(G.OP_LINEAR_CE_BWD, G.MOE_F32, 0, 1, 1, 64, 101)
     assert L.moe_linear_ce_bwd(G.MOE_F32, None, None, ptr(1), None, None, 0, 64, 101, 0.0, None, ptr(1), ptr(2), nb,
                                None) == G.MOE_EINVAL
+
+
+def test_linear_ce_bwd_without_dloss():
+    """None stands for ones, as NULL does in C; the tensors' device is x's."""
+    x, w, t, l = torch.zeros(4, 64), torch.zeros(9, 64), torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU"):
+        G.linear_ce_bwd(None, x, w, t, l)
+    with pytest.raises(ValueError, match="GPU"):
+        G.linear_ce_bwd(dloss=None, x=x, w=w, targets=t, lse=l)
+    with pytest.raises(TypeError, match="needs x"):
+        G.linear_ce_bwd(l, None, w, t, l)

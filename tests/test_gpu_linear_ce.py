@@ -374,3 +374,16 @@ def test_streams_and_graph():
         torch.cuda.synchronize()
         for n, v in {**f, **b}.items():
             assert torch.equal(v, e[n]), (i, n)
+
+
+def test_no_dloss_in_python():
+    import grouped_gemm_top_amd as G
+    c = _case(50, 64, 300, BF, 0.1, 1e-3, seed=63)
+    c["g"][:] = 1.0
+    o, up = _run(c)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, dict(stream=st)):
+        b = G.linear_ce_bwd(None, up["x"], up["w"], up["t"], o["lse"], z_coef=1e-3, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(b["dx"], o["dx"]) and torch.equal(b["dw"], o["dw"])
