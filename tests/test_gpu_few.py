@@ -313,3 +313,107 @@ def test_streams_graph_and_repeats(kind):
         gr.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(e[n], r[n]) for n in e), i
+
+
+# ------------------------------------------------------------------ a single token: a choice of its own, by counting ranks
+# (with 64, 128 or 512 threads' worth of experts a part: E <= 128, <= 256 and beyond)
+
+@KINDS
+@pytest.mark.parametrize("H,I,E,k", [(64, 32, 128, 32), (96, 64, 129, 8), (128, 32, 200, 5), (64, 64, 256, 32), (160, 32, 257, 9),
+                                     (64, 32, 1000, 32), (64, 32, 1024, 1), (2048, 64, 256, 8), (4096, 32, 513, 8)])
+def test_one_token(H, I, E, k, kind):
+    c = _case(1, H, I, E, k, kind, seed=101 + E, bias=E % 2 == 0)
+    o, _ = _run(c)
+    _check(c, o)
+
+
+ONE = pytest.mark.parametrize("E,k", [(7, 7), (77, 9), (128, 32), (129, 17), (200, 32), (256, 8), (257, 32), (1000, 32), (1024, 20)])
+
+
+def _sorted_choice(z, k):
+    """Stable, -0 and +0 equal, NaN behind everything beside -inf."""
+    z = torch.where(torch.isnan(z), torch.full_like(z, -float("inf")), z) + 0.0
+    return torch.sort(z, dim=-1, descending=True, stable=True).indices[..., :k].int()
+
+
+@ONE
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_one_token_choice_is_exact_on_ties(E, k, seed):
+    """Whole-number logits with many ties (sums of 64 products of -1, 0 and 1 are exact in any order), -0 among the biases."""
+    gen = torch.Generator(device="cuda").manual_seed(1000 * seed + E)
+    c = _case(1, 64, 32, E, k, "bf16", seed=seed)
+    c["x"] = torch.randint(-1, 2, (1, 64), generator=gen, device="cuda").to(BF)
+    c["wr"] = torch.randint(-1, 2, (64, E), generator=gen, device="cuda").float()
+    c["b"] = torch.where(torch.rand(E, generator=gen, device="cuda") < 0.5, -0.0, 0.0)
+    o, _ = _run(c)
+    assert torch.equal(o["topk_idx"].cpu(), _sorted_choice(c["x"].float().cpu() @ c["wr"].cpu(), k))
+    _check(c, o)
+    c["wr"][:] = 0.0  # one tie of all
+    o, _ = _run(c)
+    assert o["topk_idx"][0].tolist() == list(range(k))
+    assert bool(((o["topk_w"] - 1 / k).abs() <= 40 * U / k).all())
+
+
+@ONE
+def test_one_token_experts_left_out(E, k):
+    """As for several tokens: -inf (and NaN) leave an expert out, too few others leave the rest without weight."""
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    c = _case(1, 64, 32, E, k, "bf16", seed=13)
+    c["x"] = torch.randint(-1, 2, (1, 64), generator=gen, device="cuda").to(BF)
+    c["wr"] = torch.randint(-1, 2, (64, E), generator=gen, device="cuda").float()
+    z = c["x"].float().cpu() @ c["wr"].cpu()
+    for share in (0.3, 0.9, 1.0):
+        out = torch.rand(E, generator=gen, device="cuda") < share
+        c["b"] = torch.where(out, -float("inf"), 0.0)
+        c["b"][out & (torch.rand(E, generator=gen, device="cuda") < 0.2)] = float("nan")
+        o, _ = _run(c)
+        zb = z + c["b"].cpu()
+        zb = torch.where(torch.isnan(zb), torch.full_like(zb, -float("inf")), zb)
+        idx = _sorted_choice(zb, k)
+        assert torch.equal(o["topk_idx"].cpu(), idx)
+        zi = zb.gather(1, idx.long()).double()
+        w = torch.softmax(zi, dim=1) if bool((zi > -float("inf")).any()) else torch.zeros_like(zi)
+        # (exponentials of whole numbers, k of them added, one division)
+        assert bool(((o["topk_w"].cpu().double() - w).abs() <= 32 * U * w).all())
+        if not bool((w > 0).any()):
+            assert bool((o["out"] == 0).all())
+
+
+@KINDS
+@pytest.mark.parametrize("E", [12, 200, 300])
+def test_one_spoilt_token(E, kind):
+    for value in (float("nan"), float("inf")):
+        c = _case(1, 96, 64, E, 3, kind, seed=17)
+        c["x"][0, 7] = value
+        o, _ = _run(c)
+        idx = o["topk_idx"][0].tolist()
+        assert len(set(idx)) == 3 and all(0 <= e < E for e in idx)
+        assert bool(torch.isnan(o["out"]).all())
+
+
+@KINDS
+@pytest.mark.parametrize("E", [200, 300])
+def test_one_token_streams_graph_and_repeats(E, kind):
+    import grouped_gemm_top_amd as G
+    c = _case(1, 128, 96, E, 4, kind, seed=23, bias=True)
+    o, a = _run(c)
+    st = [torch.cuda.Stream() for _ in range(2)]
+    for s in st:
+        s.wait_stream(torch.cuda.current_stream())
+    call = lambda x, **kw: G.layer_few(x, a["wr"], a["wg"], a["wu"], a["wd"], 4, bias=a["b"], **kw)  # noqa: E731
+    for _ in range(10):
+        r, q = call(a["x"], stream=st[0]), call(a["x"], stream=st[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(r[n], o[n]) and torch.equal(q[n], o[n]) for n in o)
+    x = a["x"].clone()
+    with torch.cuda.stream(st[0]):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st[0]):
+            r = call(x)
+    for i in range(5):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator(device="cuda").manual_seed(40 + i), device="cuda"))
+        e = call(x)
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(e[n], r[n]) for n in e), i
