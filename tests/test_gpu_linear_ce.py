@@ -387,3 +387,16 @@ def test_no_dloss_in_python():
         b = G.linear_ce_bwd(None, up["x"], up["w"], up["t"], o["lse"], z_coef=1e-3, **kw)
         torch.cuda.synchronize()
         assert torch.equal(b["dx"], o["dx"]) and torch.equal(b["dw"], o["dw"])
+
+
+@pytest.mark.parametrize("N,H,V", [(37, 4096, 45007), (300, 2048, 43617)])
+def test_fp32_pieces_of_a_large_projection(N, H, V):
+    """V H above 512 MB / 6: W's three parts are made and read piece by piece in the forward as well, in one buffer, the last
+    piece ragged (three pieces, and a second one of 97 columns), and the pairs of all pieces meet in each token's sum."""
+    c = _case(N, H, V, F32, 0.2, 1e-3, seed=95)
+    most = (512 << 20) // (6 * H) // 256 * 256
+    assert V > most and (V % most < 256 or V > 2 * most)
+    c["t"][2:6] = torch.tensor([most - 1, most, V // most * most, V // most * most - 1], dtype=torch.int32)
+    ref, bound = _exact(c)
+    o, _ = _run(c)
+    _check(o, ref, bound)
