@@ -193,8 +193,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear(Args a) {
   const int m0 = mt * BM, n0 = nt * BN;
   const KSlice sl = k_slice(C::TERMS, (a.K + BK - 1) / BK, s, a.S);
   const uint32_t pa = (uint32_t)a.M * (uint32_t)a.K * 2u, pb = (uint32_t)a.N * (uint32_t)a.K * 2u;
-  const Opnd A{a.A, a.M, AKC ? a.K : a.M, (long long)C::PLANES * a.M * a.K * 2, pa, nullptr};
-  const Opnd B{a.B, a.N, BKC ? a.K : a.N, (long long)C::PLANES * a.N * a.K * 2, pb, nullptr};
+  const Opnd A{a.A, a.M, AKC ? a.K : a.M, (long long)C::PLANES * a.M * a.K * 2, pa};
+  const Opnd B{a.B, a.N, BKC ? a.K : a.N, (long long)C::PLANES * a.N * a.K * 2, pb};
   f32x4 acc[MB][NB];
   C::run(s_ring, A, B, m0, n0, a.K, sl, w, L, acc);
 

@@ -329,8 +329,8 @@ __device__ __forceinline__ void z_tiles(const Args& a, int b, int G, char* s_rin
   };
   int m0, n0;
   if (!at(0, m0, n0)) return;
-  const Opnd A{a.x, n, a.H, (long long)C::PLANES * a.N * a.H * 2, (uint32_t)a.N * (uint32_t)a.H * 2u, nullptr};
-  const Opnd B{a.w, a.V, a.H, (long long)C::PLANES * a.V * a.H * 2, (uint32_t)a.V * (uint32_t)a.H * 2u, nullptr};
+  const Opnd A{a.x, n, a.H, (long long)C::PLANES * a.N * a.H * 2, (uint32_t)a.N * (uint32_t)a.H * 2u};
+  const Opnd B{a.w, a.V, a.H, (long long)C::PLANES * a.V * a.H * 2, (uint32_t)a.V * (uint32_t)a.H * 2u};
   P pipe;
   pipe.start(s_ring, A, B, a.H, w, L, at);
   const int c = L & 15, g = L >> 4;
@@ -534,8 +534,8 @@ __device__ __forceinline__ void dx_tile(const Args& a, int b, char* s_ring) {
   if (!my_tile(b, (n + BM - 1) / BM, (a.H + BN - 1) / BN, PART ? a.S : 1, mt, nt, s)) return;
   const int m0 = mt * BM, n0 = nt * BN;
   const KSlice sl = k_slice(C::TERMS, (a.V + BK - 1) / BK, s, PART ? a.S : 1);
-  const Opnd A{a.dz, n, a.ldz, (long long)C::PLANES * a.N * a.ldz * 2, (uint32_t)a.N * (uint32_t)a.ldz * 2u, nullptr};
-  const Opnd B{a.w, a.H, a.H, (long long)C::PLANES * a.V * a.H * 2, (uint32_t)a.V * (uint32_t)a.H * 2u, nullptr};
+  const Opnd A{a.dz, n, a.ldz, (long long)C::PLANES * a.N * a.ldz * 2, (uint32_t)a.N * (uint32_t)a.ldz * 2u};
+  const Opnd B{a.w, a.H, a.H, (long long)C::PLANES * a.V * a.H * 2, (uint32_t)a.V * (uint32_t)a.H * 2u};
   f32x4 acc[MB][NB];
   C::run(s_ring, A, B, m0, n0, a.V, sl, w, L, acc);
   char* sg = s_ring + w * 4096;
@@ -621,8 +621,8 @@ __device__ __forceinline__ void dw_tiles(const Args& a, int b, int G, char* s_ri
   };
   int m0, n0;
   if (!at(0, m0, n0)) return;
-  const Opnd A{a.dz, a.V, a.ldz, (long long)C::PLANES * a.N * a.ldz * 2, (uint32_t)a.N * (uint32_t)a.ldz * 2u, nullptr};
-  const Opnd B{a.x, a.H, a.H, (long long)C::PLANES * a.N * a.H * 2, (uint32_t)a.N * (uint32_t)a.H * 2u, nullptr};
+  const Opnd A{a.dz, a.V, a.ldz, (long long)C::PLANES * a.N * a.ldz * 2, (uint32_t)a.N * (uint32_t)a.ldz * 2u};
+  const Opnd B{a.x, a.H, a.H, (long long)C::PLANES * a.N * a.H * 2, (uint32_t)a.N * (uint32_t)a.H * 2u};
   f32x4 acc[MB][NB];
   P pipe;
   if constexpr (PART) {

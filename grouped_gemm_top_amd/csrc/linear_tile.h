@@ -41,13 +41,11 @@ __device__ __forceinline__ void store8(void* p, size_t o, const f32x4 (&v)[2]) {
 }
 // An operand: X rows (K-contiguous) or X columns (K-strided) of a matrix whose rows are ld elements apart
 // (a multiple of 8), `bytes` in all planes together; an fp32 operand's parts are `plane` bytes apart.
-// rows: the matrix row of each operand row (K-contiguous only; NULL: the same).
 struct Opnd {
   const void* p;
   int X, ld;
   long long bytes;
   uint32_t plane;
-  const int* rows;
 };
 
 // One operand's loads: R rows (K-contiguous) or R columns (K-strided) of a 64-wide k-step, as R / 8
@@ -75,7 +73,7 @@ struct Op {
         const int row = x0 + 8 * b + (L >> 3);
         const int c = (L & 7) ^ ((4 * (w & 1) + (L >> 4)) & 7);
         kl = 8 * c;  // (the same for every q: NW is even)
-        v[q] = row < X ? ((uint32_t)(d.rows ? d.rows[row] : row) * ld + 8u * c) * 2u : OOB;
+        v[q] = row < X ? ((uint32_t)row * ld + 8u * c) * 2u : OOB;
       } else {
         constexpr int CPR = R / 8;  // chunks per k-row
         const int k = b * (64 / CPR) + L / CPR;
