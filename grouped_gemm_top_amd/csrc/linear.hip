@@ -367,15 +367,6 @@ __device__ __forceinline__ void times_slope(float (&d)[8], const float (&v)[8]) 
   for (int j = 0; j < 8; ++j) d[j] *= act_bwd1<ACT>(v[j]);
 }
 
-// src (n values, a multiple of 8) -> its three parts, planes of n values
-__global__ __launch_bounds__(256) void k_linear_split(const float* __restrict__ src, size_t n, bf16_t* __restrict__ dst) {
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n / 8; i += (size_t)gridDim.x * 256) {
-    float v[8];
-    load8(src + 8 * i, v);
-    store_parts(dst + 8 * i, n, v);
-  }
-}
-
 // dz = dout act'(z) as the products take it: rounded to bf16, or in fp32 its three parts (dz NULL: not
 // written; act NONE: dz is dout), and the column sums of the unrounded dz over this workgroup's rows
 // (part NULL: not wanted).  A workgroup owns 512 columns (64 threads of 8) and the rows g, g + 4
@@ -475,7 +466,7 @@ hipError_t product(Kind kind, Args a, void* ws, hipStream_t s) {
 
 void split(const void* src, size_t n, bf16_t* dst, hipStream_t s) {
   const size_t b = (n / 8 + 255) / 256;
-  hipLaunchKernelGGL(k_linear_split, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), 0, s, (const float*)src, n, dst);
+  hipLaunchKernelGGL(k_split, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), 0, s, (const float*)src, n, dst);
 }
 
 // Calls whose W is streamed into registers (k_linear_few) rather than tiled.  Measured, us (few /

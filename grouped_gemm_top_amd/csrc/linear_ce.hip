@@ -60,11 +60,6 @@ struct Args {
 __device__ __forceinline__ bool in_vocab(int t, int V) { return (unsigned)t < (unsigned)V; }
 
 // ---- the counted tokens ----
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  load4(p, v[0], v[1], v[2], v[3]);
-  load4(p + 4, v[4], v[5], v[6], v[7]);
-}
-
 constexpr int GR = 16;  // tokens of a group: one a wavefront
 
 // A workgroup takes `groups` groups of tokens.  It counts the counted ones before them over all targets (a list of
@@ -147,15 +142,6 @@ __global__ __launch_bounds__(1024) void k_ce_select(const int* __restrict__ targ
       }
     }
     __syncthreads();  // s_pos has been read
-  }
-}
-
-// a piece of W as its three parts, planes of n values (a multiple of 8)
-__global__ __launch_bounds__(256) void k_ce_split(const float* __restrict__ src, size_t n, bf16_t* __restrict__ dst) {
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n / 8; i += (size_t)gridDim.x * 256) {
-    float v[8];
-    load8(src + 8 * i, v);
-    store_parts(dst + 8 * i, n, v);
   }
 }
 
@@ -855,7 +841,7 @@ hipError_t fwd(const T* x, const T* w, const int* target, int N, int H, int V, f
     a.w = w + (size_t)v0 * H;
     if (F) {
       const size_t n = (size_t)a.V * H;
-      hipLaunchKernelGGL(k_ce_split, dim3(grid_sum(n / 8)), dim3(256), 0, s, (const float*)a.w, n, wp);
+      hipLaunchKernelGGL(k_split, dim3(grid_sum(n / 8)), dim3(256), 0, s, (const float*)a.w, n, wp);
       a.w = wp;
     }
     launch_z<LSE, F>(a, b.tile, s);
@@ -910,7 +896,7 @@ hipError_t bwd(const float* dloss, const T* x, const T* w, const int* target, co
     q.dwo = dw + (size_t)v0 * H;
     if (F) {
       const size_t n = (size_t)q.V * H;
-      hipLaunchKernelGGL(k_ce_split, dim3(grid_sum(n / 8)), dim3(256), 0, s, (const float*)q.w, n, wp[i & 1]);
+      hipLaunchKernelGGL(k_split, dim3(grid_sum(n / 8)), dim3(256), 0, s, (const float*)q.w, n, wp[i & 1]);
       q.w = wp[i & 1];
     }
     return q;

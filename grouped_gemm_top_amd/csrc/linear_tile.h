@@ -289,6 +289,15 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   load4(p + 4, v[4], v[5], v[6], v[7]);
 }
 
+// src (n values, a multiple of 8) -> its three parts, planes of n values
+static __global__ __launch_bounds__(256) void k_split(const float* __restrict__ src, size_t n, bf16_t* __restrict__ dst) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n / 8; i += (size_t)gridDim.x * 256) {
+    float v[8];
+    load8(src + 8 * i, v);
+    store_parts(dst + 8 * i, n, v);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 enum Kind { K_FWD, K_DX, K_DW };
 struct Shape { int big, S; };  // big: 2 = 256 x 256, 1 = 128 x 128, 0 = 64 x 64 (64 x 128 for dx)
