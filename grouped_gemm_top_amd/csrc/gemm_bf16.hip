@@ -572,7 +572,7 @@ __device__ __forceinline__ void dswiglu4(const float (&G)[4], const float (&U)[4
 // at q ^ (r & 7), and leave as 64 contiguous bytes a half; the block of columns from I on is zeros, whose scale
 // code 0 fills the scale row's padding.  Rows >= mlen lie past the descriptors' ranges.  Codes of the fp32
 // accumulators, one rounding (of a bf16 [G | U] it would be two).  N = 4096, E = 128, H = 2048, I = 512, k = 8: 177 us
-// with 69 MB of codes and scales, 181 with 134 MB in bf16; the loads of the tile loop are the time of both.
+// with 35 MB of codes and scales, 181 with 67 MB in bf16 (A's 34 MB beside both); the loads of the tile loop are the time of both.
 __device__ __forceinline__ void ckpt_store(rsrc_t rq, rsrc_t rs, char* st, const f32x4 (&blk)[8], uint32_t m16,
                                            int i0, int I, int L) {
   const int c = L & 15, g = L >> 4;

@@ -307,7 +307,10 @@ struct Shape { int big, S; };  // big: 2 = 256 x 256, 1 = 128 x 128, 0 = 64 x 64
 //   time of a step when the CU is full) (+ the partial sums' way to memory and back)
 // in us.  The constants are fitted to 110 random shapes (65 <= N <= 16384, 64 <= K, O <= 8192) with
 // every tile and slice count timed: the choice is on average 0.7 % slower than the best one
-// measured, at worst 17 %.
+// measured, at worst 17 %.  The cross entropy asks outside that range, with V as N or K.  40 random shapes (1 <= N <= 8192, H
+// from 128 to 4096, V from 2000 to 107000), each product's tile and slices changed alone, whole calls: bf16 0.6 % (z), 1.1 %
+// (dx) and 1.0 % (dW) slower than with the best one, at worst 6 %; fp32 1.1, 2.3 and 0.8 %, at worst 14 % (dx of N = 103,
+// H = 1192, V = 37048: 455 us with 16 slices, 400 with 32).
 inline Shape choose(Kind kind, int M, int N, int K, int terms, int max_s = 16) {
   const int steps = terms * ((K + BK - 1) / BK);
   struct C { int bm, bn, occ; double fix, lat, thr; };
