@@ -15,11 +15,14 @@
 // alone, and the two other products take it from there while it is in the caches: dW of the piece is
 // complete, dx is summed over the pieces in fp32.  Where all three products fill the large tile, dx and dW of a
 // piece run in one launch with dz of the next.  Every sum has a fixed order (bitwise reproducible).
-// dz is rounded to bf16 as an operand of the matrix cores (the fp32 call: three bf16 parts, see linear.hip).
+// dz is rounded to bf16 as an operand of the matrix cores (the fp32 call: three bf16 parts, see linear.hip): dx and dW
+// are off by 0.0021-0.0025 of their norms, 0.0017 of it their own rounding, and by up to 0.0034 where a handful of tokens
+// count, whose few large dz do not average.  A second part of dz would double both products.
 //
-// Measured (bf16).  N = 4096, H = 2048, V = 32000, losses: 416-437 us on 256 x 256 tiles, 1.23-1.29
+// Measured (bf16).  N = 4096, H = 2048, V = 32000, losses: 414-448 us on 256 x 256 tiles, 1.20-1.30
 // PFLOP/s; torch's product alone, which writes z, takes 457.  N = 8192, V = 50021, a tenth of the tokens without target,
-// losses and gradients: 4.9-5.0 ms, 1.21 PFLOP/s over its four products (tiles of a piece apart, a launch each: 5.08).
+// losses and gradients: 4.9-5.2 ms, 1.16-1.24 PFLOP/s over its four products (tiles of a piece apart, a launch
+// each, where it took 4.9-5.0: 5.08).
 // What bounds these is the chip's power: on zeros the same forward is 15-20 % faster, as the library's products
 // are.  N = 300, H = 1024, V = 50021, 180 counted: 170 us in eight launches; z 43 and 38, dx 39 + 5, dW 39, each at
 // twice the time of W's 102 MB: a tile waits for loads that only two stages are ahead.  N = 1, V = 130001: 118 us, 532 MB of

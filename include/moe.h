@@ -520,7 +520,7 @@ moe_status moe_linear_bwd(moe_dtype dt, const void* dout, const void* x, const v
  * moe_layer_bwd_ckpt8: moe_layer_bwd for bf16 layers at the [G | U] that hq and hs stand for.  x is bf16 [N,H]
  * (xs NULL), or e4m3 codes [N,H] with their scale codes xs [N, KS(H)], as moe_add_rmsnorm or moe_quantize_mxfp8 make
  * them (16-byte aligned codes): dW_gate and dW_up are then taken at the values the codes stand for, in bf16 (exact from
- * 2^-133 on).  Outputs, plans and errors as moe_layer_bwd.
+ * 2^-133 on).  Outputs, plans, errors and roundings as moe_layer_bwd: dH, A' and the expert rows whose sum dx is are bf16.
  * Workspace: moe_workspace_bytes(MOE_OP_LAYER_BWD_CKPT8, MOE_BF16, N, E, k, H, I, M_cap).
  * Both: H a multiple of 8 (of 32 with xs), I a multiple of 32, hs 4-byte aligned.  The checkpoint is lossy: e4m3 has 4
  * significant bits, so a value v of a block with largest magnitude m is off by at most 2^-4 |v| or m 2^-17.
