@@ -21,8 +21,8 @@
 //
 // Measured (E = 128, H = 2048, I = 512, k = 8): N = 1 20.7 us a call, launches 3.3 + 11.7 + 5.8.  51 MB take 10 us
 // at copy rate; the rest are three starts (2.7 each with nothing to do) and the choice (2).  N = 16, E = 256: 644 MB in
-// 115 us, 5.5 TB/s.  fp32, N = 61, E = 64, H = 1432, I = 520, k = 4: 562 MB in 148-155; N = 1 as above 38.  MX-FP8: N = 1 19, N = 24, E = 256,
-// H = 4096, I = 256: 447 MB in 112.  Beyond a token or two what is above the stream is the router and the choice (12 us)
+// 115 us, 5.5 TB/s.  fp32, N = 61, E = 64, H = 1432, I = 520, k = 4: 562 MB in 148-155; N = 1 as above: 38.  MX-FP8: N = 1 19,
+// N = 24, E = 256, H = 4096, I = 256: 447 MB in 112.  Beyond a token or two what is above the stream is the router and the choice (12 us)
 // and gate/up's last round of tasks (2112 over 512 workgroups: four rounds and an eighth); cutting that round's tasks along
 // H, with their parts joined by a ticket, cost 2 to 10 % on most shapes.
 #include <type_traits>

@@ -581,9 +581,10 @@ moe_status moe_layer_few_mxfp8(const void* x, const float* w_r, const float* bia
  *   dz[t,v] = dloss[t] ((1 + 2 z_coef lse[t]) exp(z[t,v] - lse[t]) - [v == y])
  *   dx = dz w [N,H] (zero for tokens that take no part),  dw = dz^T x [V,H]      (NULL skips each)
  * z is formed again.  dz is rounded to MOE_BF16 for its two products, once (2^-8 of each value at most); MOE_F32
- * keeps fp32 accuracy throughout, by three bf16 parts an operand, with moe_linear_fwd's limits (infinities and
- * magnitudes from 3.38e38 on make their sums NaN).  Its working copy of dz is one or two pieces of the vocabulary, each
- * of at most 128 MB (MOE_F32: 192 MB), or 256 columns where N is above 262144 (131072).
+ * keeps fp32 accuracy throughout (where the target's p is next to 1, p - 1 is as far off as p), by three bf16 parts an
+ * operand, with moe_linear_fwd's limits (infinities and magnitudes from 3.38e38 on make their sums NaN).  Its working
+ * copy of dz is one or two pieces of the vocabulary, each of at most 128 MB (MOE_F32: 192 MB), or 256 columns where N is
+ * above 262144 (131072).
  * A counted token with NaN or infinite logits spoils its own loss, lse and dx, and all of dw.
  * H a multiple of 8, V >= 1 (any); tensors and workspace 16-byte aligned, targets, loss, lse and dloss 4-byte; each
  * output is no other argument of its call;
