@@ -316,7 +316,7 @@ def test_streams_graph_and_repeats(kind):
 
 
 # ------------------------------------------------------------------ a single token: a choice of its own, by counting ranks
-# (with 64, 128 or 512 threads' worth of experts a part: E <= 128, <= 256 and beyond)
+# (a kernel of its own each for E <= 128, E <= 256 and beyond)
 
 @KINDS
 @pytest.mark.parametrize("H,I,E,k", [(64, 32, 128, 32), (96, 64, 129, 8), (128, 32, 200, 5), (64, 64, 256, 32), (160, 32, 257, 9),
